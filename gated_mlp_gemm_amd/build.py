@@ -3,6 +3,7 @@
     python -m gated_mlp_gemm_amd.build [--jobs N]
 
 Compiles ``csrc/kernels.hip`` (elementwise kernels and the launch dispatch),
+``csrc/lora_kernels.hip`` (low-rank adapters), ``csrc/route_kernels.hip`` (the router),
 ``csrc/kernel_instances.hip`` once per group of its instance list (the tile
 kernels, one object per group) and ``csrc/api.cpp`` (the C ABI) with hipcc,
 in parallel (``--jobs``, else ``MAX_JOBS``, else the CPU count), and links
@@ -74,6 +75,8 @@ def _objects():
     instance groups first (the list puts the longest compiles first)."""
     objs = [(f"inst{g:02d}", INSTANCES, [f"-DSWIGLU_INSTANCE={g}"])
             for g in range(instance_groups())]
+    objs.append(("lora", os.path.join(CSRC, "lora_kernels.hip"), []))
+    objs.append(("route", os.path.join(CSRC, "route_kernels.hip"), []))
     objs.append(("kernels", os.path.join(CSRC, "kernels.hip"), []))
     objs.append(("api", os.path.join(CSRC, "api.cpp"), ["-x", "hip"]))
     return objs

@@ -209,6 +209,85 @@ int check_workspace(const void *workspace, uint64_t bytes) {
     return SWIGLU_OK;
 }
 
+// The operands of a call, for the checks that every pointer is there, is
+// aligned, and that no output overlaps another operand.
+struct Operand {
+    const char *name;
+    const void *p;
+    int64_t bytes;
+    uint32_t align;     // bytes, a power of two
+    bool output;
+    bool optional;      // may be NULL
+};
+int check_operands(const Operand *ops, int n) {
+    for (int i = 0; i < n; ++i)
+        if (!ops[i].p && !ops[i].optional) return fail(SWIGLU_ERR_NULL, "%s is required", ops[i].name);
+    for (int i = 0; i < n; ++i)
+        if (reinterpret_cast<uintptr_t>(ops[i].p) & (ops[i].align - 1))
+            return fail(SWIGLU_ERR_ALIGN, "%s must be %u-byte aligned", ops[i].name, ops[i].align);
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < n; ++j)
+            if (i != j && ops[i].output && ops[i].p && ops[j].p &&
+                overlap(ops[i].p, ops[i].bytes, ops[j].p, ops[j].bytes))
+                return fail(SWIGLU_ERR_ALIAS, "%s overlaps %s", ops[i].name, ops[j].name);
+    return SWIGLU_OK;
+}
+
+int check_route(int logits_type, int64_t M, int64_t E, int64_t k) {
+    if (logits_type != SWIGLU_F32 && logits_type != SWIGLU_BF16)
+        return fail(SWIGLU_ERR_UNSUPPORTED, "unknown logits type %d", logits_type);
+    if (M < 0 || M > kMaxM) return fail(SWIGLU_ERR_SHAPE, "M=%lld outside [0, 2^31 - 1]", (long long)M);
+    if (E < 1 || E > swiglu::kMaxRouteE)
+        return fail(SWIGLU_ERR_SHAPE, "E=%lld outside [1, %d]", (long long)E, swiglu::kMaxRouteE);
+    if (k < 1 || k > E || k > swiglu::kMaxRouteK)
+        return fail(SWIGLU_ERR_SHAPE, "k=%lld outside [1, min(E, %d)]", (long long)k,
+                    swiglu::kMaxRouteK);
+    return SWIGLU_OK;
+}
+
+int check_lora(int64_t slots, int64_t count, int64_t rank) {
+    if (slots < 1 || slots > swiglu::kMaxLoraSlots)
+        return fail(SWIGLU_ERR_SHAPE, "slots=%lld outside [1, %d]", (long long)slots,
+                    swiglu::kMaxLoraSlots);
+    if (rank < 8 || rank > swiglu::kMaxLoraRank || rank % 8 != 0)
+        return fail(SWIGLU_ERR_SHAPE, "rank=%lld must be a multiple of 8 in [8, %d]",
+                    (long long)rank, swiglu::kMaxLoraRank);
+    if (count < 1 || count > swiglu::kMaxLoraCount)
+        return fail(SWIGLU_ERR_SHAPE, "count=%lld adapters outside [1, %d]", (long long)count,
+                    swiglu::kMaxLoraCount);
+    return SWIGLU_OK;
+}
+
+// Bytes of the workspace that hold T [M][slots][width] (bf16), a multiple of 256.
+uint64_t lora_t_bytes(int64_t M, int64_t slots, int64_t width) {
+    return (static_cast<uint64_t>(M) * slots * width * 2 + 255) & ~uint64_t{255};
+}
+int check_lora_workspace(const void *workspace, uint64_t bytes, uint64_t need) {
+    if (!workspace) return fail(SWIGLU_ERR_NULL, "workspace is required");
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(SWIGLU_ERR_ALIGN, "workspace must be 256-byte aligned");
+    if (bytes < need)
+        return fail(SWIGLU_ERR_SHAPE, "workspace of %llu bytes, at least %llu are needed",
+                    (unsigned long long)bytes, (unsigned long long)need);
+    return SWIGLU_OK;
+}
+
+// One projection with adapters: the shrink, then the product with the expansion.
+hipError_t lora_projection(const uint16_t *X, const uint16_t *W, uint16_t *Y, int64_t M,
+                           int64_t cols, int64_t K, bool gated, const swiglu::LoraTable &t,
+                           const int32_t *ids, const float *weights, int64_t slots,
+                           void *workspace, uint64_t bytes, int cus, hipStream_t s) {
+    const int parts = gated ? 2 : 1;
+    const uint64_t t_bytes = lora_t_bytes(M, slots, parts * t.rank);
+    uint16_t *T = static_cast<uint16_t *>(workspace);
+    const hipError_t e = swiglu::launch_lora_shrink(X, t, ids, weights, (int)slots, T, (int)M,
+                                                    (int)K, parts, s);
+    if (e != hipSuccess) return e;
+    return swiglu::launch_lora_project(
+        X, W, Y, (int)M, (int)cols, (int)K, gated, t, ids, (int)slots, T,
+        make_ws(static_cast<char *>(workspace) + t_bytes, bytes - t_bytes, cus), s);
+}
+
 int launched(hipError_t e, const char *what) {
     if (e != hipSuccess) return fail(SWIGLU_ERR_HIP, "%s launch: %s", what, hipGetErrorString(e));
     return ok();
@@ -636,6 +715,211 @@ int swiglu_fused_gemm_fp8(const uint8_t *A8, const uint8_t *W_fused8, uint16_t *
                                                          make_ws(workspace, workspace_bytes, cus),
                                                          (hipStream_t)stream),
                     "fused interleaved fp8");
+}
+
+int swiglu_route_workspace_size(int64_t M, int64_t E, uint64_t *bytes) {
+    if (!bytes) return fail(SWIGLU_ERR_NULL, "bytes is required");
+    *bytes = 0;
+    int st = check_route(SWIGLU_F32, M, E, 1);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    *bytes = swiglu::route_partials_bytes(M, E, cus);
+    return ok();
+}
+
+int swiglu_route(const void *logits, int logits_type, const uint8_t *valid, int32_t *ids,
+                 float *weights, int32_t *counts, float *loss, int64_t M, int64_t E, int64_t k,
+                 int normalize, void *workspace, uint64_t workspace_bytes, void *stream) {
+    int st = check_route(logits_type, M, E, k);
+    if (st != SWIGLU_OK) return st;
+    const bool bf16 = logits_type == SWIGLU_BF16;
+    const uint32_t size = bf16 ? 2 : 4;
+    const bool none = M == 0;
+    const Operand ops[] = {
+        {"logits", logits, M * E * size, size, false, none},
+        {"valid", valid, M, 1, false, true},
+        {"ids", ids, M * k * 4, 4, true, none},
+        {"weights", weights, M * k * 4, 4, true, none},
+        {"counts", counts, (E + 1) * 4, 4, true, false},
+        {"loss", loss, 4, 4, true, false},
+        {"workspace", workspace_bytes ? workspace : nullptr, (int64_t)workspace_bytes, 256, true, true},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    const bool part = workspace != nullptr && workspace_bytes > 0;
+    return launched(swiglu::launch_route(logits, bf16, valid, ids, weights, counts, loss, M, (int)E,
+                                         (int)k, normalize != 0, part ? workspace : nullptr,
+                                         workspace_bytes, part ? next_counter_block() : nullptr,
+                                         cus, (hipStream_t)stream),
+                    "route");
+}
+
+int swiglu_route_backward(const void *logits, int logits_type, const uint8_t *valid,
+                          const int32_t *ids, const float *weights, const int32_t *counts,
+                          const float *d_weights, const float *d_loss, void *d_logits, int64_t M,
+                          int64_t E, int64_t k, int normalize, void *stream) {
+    int st = check_route(logits_type, M, E, k);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0) return ok();
+    const bool bf16 = logits_type == SWIGLU_BF16;
+    const uint32_t size = bf16 ? 2 : 4;
+    const Operand ops[] = {
+        {"logits", logits, M * E * size, size, false, false},
+        {"valid", valid, M, 1, false, true},
+        {"ids", ids, M * k * 4, 4, false, false},
+        {"weights", weights, M * k * 4, 4, false, false},
+        {"counts", counts, (E + 1) * 4, 4, false, false},
+        {"d_weights", d_weights, M * k * 4, 4, false, true},
+        {"d_loss", d_loss, 4, 4, false, true},
+        {"d_logits", d_logits, M * E * size, size, true, false},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    return launched(swiglu::launch_route_backward(logits, bf16, valid, ids, weights, counts,
+                                                  d_weights, d_loss, d_logits, M, (int)E, (int)k,
+                                                  normalize != 0, cus, (hipStream_t)stream),
+                    "route backward");
+}
+
+int swiglu_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t slots, int64_t rank,
+                               uint64_t *bytes) {
+    if (!bytes) return fail(SWIGLU_ERR_NULL, "bytes is required");
+    *bytes = 0;
+    int st = check_gemm_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_lora(slots, 1, rank);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0 || N == 0) return ok();
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    *bytes = lora_t_bytes(M, slots, 2 * rank) + swiglu::workspace_bytes_for(cus);
+    return ok();
+}
+
+int swiglu_fused_gemm_lora(const uint16_t *X, const uint16_t *W_fused, const uint16_t *lora_a,
+                           const uint16_t *lora_b, const float *lora_scale, int64_t count,
+                           int64_t rank, const int32_t *ids, const float *weights, uint16_t *Y,
+                           int64_t M, int64_t N, int64_t K, int64_t slots, void *workspace,
+                           uint64_t workspace_bytes, void *stream) {
+    int st = check_gemm_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_lora(slots, count, rank);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0 || N == 0) return ok();
+    st = check_lora_workspace(workspace, workspace_bytes, lora_t_bytes(M, slots, 2 * rank));
+    if (st != SWIGLU_OK) return st;
+    const Operand ops[] = {
+        {"X", X, M * K * 2, 16, false, false},
+        {"W_fused", W_fused, 2 * N * K * 2, 16, false, false},
+        {"lora_a", lora_a, count * 2 * rank * K * 2, 16, false, false},
+        {"lora_b", lora_b, count * 2 * N * rank * 2, 16, false, false},
+        {"lora_scale", lora_scale, count * 4, 4, false, false},
+        {"ids", ids, M * slots * 4, 4, false, false},
+        {"weights", weights, M * slots * 4, 4, false, true},
+        {"Y", Y, M * N * 2, 16, true, false},
+        {"workspace", workspace, (int64_t)workspace_bytes, 256, true, false},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    const swiglu::LoraTable t{lora_a, lora_b, lora_scale, (int)count, (int)rank};
+    return launched(lora_projection(X, W_fused, Y, M, 2 * N, K, true, t, ids, weights, slots,
+                                    workspace, workspace_bytes, cus, (hipStream_t)stream),
+                    "fused lora");
+}
+
+int swiglu_down_proj_lora(const uint16_t *H, const uint16_t *W3t, const uint16_t *lora_a,
+                          const uint16_t *lora_b, const float *lora_scale, int64_t count,
+                          int64_t rank, const int32_t *ids, const float *weights, uint16_t *Out,
+                          int64_t M, int64_t N, int64_t D, int64_t slots, void *workspace,
+                          uint64_t workspace_bytes, void *stream) {
+    int st = check_down_shape(M, N, D);
+    if (st == SWIGLU_OK) st = check_lora(slots, count, rank);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0 || D == 0) return ok();
+    st = check_lora_workspace(workspace, workspace_bytes, lora_t_bytes(M, slots, rank));
+    if (st != SWIGLU_OK) return st;
+    const Operand ops[] = {
+        {"H", H, M * N * 2, 16, false, false},
+        {"W3t", W3t, D * N * 2, 16, false, false},
+        {"lora_a", lora_a, count * rank * N * 2, 16, false, false},
+        {"lora_b", lora_b, count * D * rank * 2, 16, false, false},
+        {"lora_scale", lora_scale, count * 4, 4, false, false},
+        {"ids", ids, M * slots * 4, 4, false, false},
+        {"weights", weights, M * slots * 4, 4, false, true},
+        {"Out", Out, M * D * 2, 16, true, false},
+        {"workspace", workspace, (int64_t)workspace_bytes, 256, true, false},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    const swiglu::LoraTable t{lora_a, lora_b, lora_scale, (int)count, (int)rank};
+    return launched(lora_projection(H, W3t, Out, M, D, N, false, t, ids, weights, slots, workspace,
+                                    workspace_bytes, cus, (hipStream_t)stream),
+                    "down projection lora");
+}
+
+int swiglu_gated_mlp_lora(const uint16_t *X, const uint16_t *W_fused, const uint16_t *W3t,
+                          const uint16_t *gate_up_a, const uint16_t *gate_up_b,
+                          const float *gate_up_scale, int64_t gate_up_count, int64_t gate_up_rank,
+                          const uint16_t *down_a, const uint16_t *down_b, const float *down_scale,
+                          int64_t down_count, int64_t down_rank, const int32_t *ids,
+                          const float *weights, uint16_t *H, uint16_t *Out, int64_t M, int64_t N,
+                          int64_t K, int64_t slots, void *workspace, uint64_t workspace_bytes,
+                          void *stream) {
+    int st = check_gemm_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_down_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_lora(slots, gate_up_count, gate_up_rank);
+    if (st == SWIGLU_OK) st = check_lora(slots, down_count, down_rank);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0) return ok();
+    const uint64_t need_up = lora_t_bytes(M, slots, 2 * gate_up_rank);
+    const uint64_t need_down = lora_t_bytes(M, slots, down_rank);
+    st = check_lora_workspace(workspace, workspace_bytes, need_up > need_down ? need_up : need_down);
+    if (st != SWIGLU_OK) return st;
+    const Operand ops[] = {
+        {"X", X, M * K * 2, 16, false, false},
+        {"W_fused", W_fused, 2 * N * K * 2, 16, false, false},
+        {"W3t", W3t, K * N * 2, 16, false, false},
+        {"gate_up_a", gate_up_a, gate_up_count * 2 * gate_up_rank * K * 2, 16, false, false},
+        {"gate_up_b", gate_up_b, gate_up_count * 2 * N * gate_up_rank * 2, 16, false, false},
+        {"gate_up_scale", gate_up_scale, gate_up_count * 4, 4, false, false},
+        {"down_a", down_a, down_count * down_rank * N * 2, 16, false, false},
+        {"down_b", down_b, down_count * K * down_rank * 2, 16, false, false},
+        {"down_scale", down_scale, down_count * 4, 4, false, false},
+        {"ids", ids, M * slots * 4, 4, false, false},
+        {"weights", weights, M * slots * 4, 4, false, true},
+        {"H", H, M * N * 2, 16, true, false},
+        {"Out", Out, M * K * 2, 16, true, false},
+        {"workspace", workspace, (int64_t)workspace_bytes, 256, true, false},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    const hipStream_t s = (hipStream_t)stream;
+    const swiglu::LoraTable up{gate_up_a, gate_up_b, gate_up_scale, (int)gate_up_count,
+                               (int)gate_up_rank};
+    const swiglu::LoraTable down{down_a, down_b, down_scale, (int)down_count, (int)down_rank};
+    // the launches run in stream order, so they share the workspace
+    const hipError_t e = lora_projection(X, W_fused, H, M, 2 * N, K, true, up, ids, weights, slots,
+                                         workspace, workspace_bytes, cus, s);
+    if (e != hipSuccess) return launched(e, "gated MLP lora: fused SwiGLU");
+    return launched(lora_projection(H, W3t, Out, M, K, N, false, down, ids, weights, slots,
+                                    workspace, workspace_bytes, cus, s),
+                    "gated MLP lora: down projection");
 }
 
 }  // extern "C"

@@ -105,6 +105,17 @@ template struct ReduceLaunch<ShapeSmall, StoreEpilogue>;
 template struct ReduceLaunch<ShapeWide8, PairMulEpilogueFp8>;
 template struct ReduceLaunch<ShapeQuad8, PairMulEpilogueFp8>;
 template struct ReduceLaunch<ShapeSmall8, PairMulEpilogueFp8>;
+#elif SWIGLU_INSTANCE == 16
+template struct TilesLaunch<ShapeWide, PairMulLora, kTailQuarter>;
+#elif SWIGLU_INSTANCE == 17
+template struct TilesLaunch<ShapeWide, StoreLora, kTailQuarter>;
+#elif SWIGLU_INSTANCE == 18
+template struct TilesLaunch<ShapeWide, PairMulLora, kTailSplit>;
+#elif SWIGLU_INSTANCE == 19
+template struct TilesLaunch<ShapeWide, StoreLora, kTailSplit>;
+#elif SWIGLU_INSTANCE == 20
+template struct TilesLaunch<ShapeQuad, PairMulLora, kTailSplit>;
+template struct TilesLaunch<ShapeQuad, StoreLora, kTailSplit>;
 #else
 #error "SWIGLU_INSTANCE is past the end of the instance list"
 #endif

@@ -601,6 +601,50 @@ hipError_t launch_down_proj(const uint16_t *H, const uint16_t *W3t, uint16_t *Ou
     return launch_store_gemm(H, KMajor{W3t, D, 1, 0}, Out, M, D, N, ws, stream);
 }
 
+// The tile kernels with adapters: the same schedules, the adapters' terms
+// expanded before each tile's epilogue (or before a split tile's last piece
+// stores its partial).  The kernels without tail work are those with a tail,
+// given none.
+template <class S, class Epi, class Base>
+static hipError_t launch_lora_gemm(const KMajor &A, KMajor B, int M, int cols, int K,
+                                   const Epi &epi, const GemmWorkspace &ws, hipStream_t stream) {
+    Schedule sch = make_schedule<S>(M, cols, K, ws);
+    sch.grid = launch_grid<S>(sch, ws.cus);
+    B.pairs = Epi::template paired<S>() ? 1 : 0;   // de-interleaved weight panels
+    if (sch.grid <= 0) return hipSuccess;
+    if constexpr (kQuarterable<S>)
+        if (sch.pieces == 0)
+            return TilesLaunch<S, Epi, kTailQuarter>::run(sch.grid, A, B, M, K, epi, sch, stream);
+    const hipError_t e =
+        TilesLaunch<S, Epi, kTailSplit>::run(sch.grid, A, B, M, K, epi, sch, stream);
+    if (e != hipSuccess || sch.pieces == 0) return e;
+    constexpr int kWavesPerTile = S::kWaves * S::TM * S::TN / Epi::template unit_blocks<S>();
+    return ReduceLaunch<S, Base>::run(sch.split_tiles * kWavesPerTile, epi, sch, stream);
+}
+
+hipError_t launch_lora_project(const uint16_t *X, const uint16_t *W, uint16_t *Y, int M, int cols,
+                               int K, bool gated, const LoraTable &t, const int *ids, int slots,
+                               const uint16_t *T, const GemmWorkspace &ws, hipStream_t stream) {
+    if (M <= 128)
+        return launch_lora_stream(X, W, Y, M, cols, K, gated, t, ids, slots, T, ws, stream);
+    const KMajor A{X, M, 1, 0, 0, 0};
+    const KMajor B{W, cols, 1, 0, 0, 0};
+    const LoraTerm lora{T, t.B, ids, M, slots, t.rank, t.count, cols};
+    const bool quad = quad_tiles_faster(M, cols, K, ws);
+    if (gated) {
+        const PairMulLora epi{{Y, M, cols / 2, cols / 2, 1.0f}, lora};
+        return quad ? launch_lora_gemm<ShapeQuad, PairMulLora, PairMulEpilogue>(A, B, M, cols, K, epi,
+                                                                               ws, stream)
+                    : launch_lora_gemm<ShapeWide, PairMulLora, PairMulEpilogue>(A, B, M, cols, K, epi,
+                                                                               ws, stream);
+    }
+    const StoreLora epi{{Y, M, cols}, lora};
+    return quad ? launch_lora_gemm<ShapeQuad, StoreLora, StoreEpilogue>(A, B, M, cols, K, epi, ws,
+                                                                       stream)
+                : launch_lora_gemm<ShapeWide, StoreLora, StoreEpilogue>(A, B, M, cols, K, epi, ws,
+                                                                       stream);
+}
+
 // One 256x256 fp32 slot per CU: a split schedule has at most one piece per
 // workgroup slot, and a CU holds one 256x256 workgroup or two of the smaller
 // shapes (whose slots are a quarter the size or less).

@@ -66,6 +66,41 @@ hipError_t launch_fused_interleaved_fp8(const uint8_t *A8, const uint8_t *Wf8, u
 hipError_t launch_fused_sequential_fp8(const uint8_t *A8, const uint8_t *Wf8, uint16_t *Y, int M,
                                        int N, int K, float scale, hipStream_t stream);
 int describe_gemm_fp8(int M, int cols, int K, const GemmWorkspace &ws, char *buf, size_t n);
+// The router and its gradient (route_kernels.hip).
+constexpr int kMaxRouteE = 512, kMaxRouteK = 16;
+uint64_t route_partials_bytes(int64_t M, int64_t E, int cus);
+// partials / counter: without them (or too few bytes) one workgroup does it all.
+hipError_t launch_route(const void *logits, bool bf16, const uint8_t *valid, int *ids,
+                        float *weights, int *counts, float *loss, int64_t M, int E, int k,
+                        bool normalize, void *partials, uint64_t partial_bytes, unsigned *counter,
+                        int cus, hipStream_t stream);
+hipError_t launch_route_backward(const void *logits, bool bf16, const uint8_t *valid,
+                                 const int *ids, const float *weights, const int *counts,
+                                 const float *d_weights, const float *d_loss, void *d_logits,
+                                 int64_t M, int E, int k, bool normalize, int cus,
+                                 hipStream_t stream);
+// Low-rank adapters (lora.hpp): a table of `count` of them beside a projection.
+constexpr int kMaxLoraCount = 8192;   // adapters of a table
+constexpr int kMaxLoraSlots = 8;      // adapters of a row
+constexpr int kMaxLoraRank = 256;
+struct LoraTable {
+    const uint16_t *A, *B;   // [count][parts * rank][K], [count][cols][rank]
+    const float *scale;      // [count]
+    int count, rank;
+};
+// T [M][slots][parts * rank] = bf16(weight scale X . A^T) of each row's adapters.
+hipError_t launch_lora_shrink(const uint16_t *X, const LoraTable &t, const int *ids,
+                              const float *weights, int slots, uint16_t *T, int M, int K,
+                              int parts, hipStream_t stream);
+// The projection of X [M][K] with the expansion of T, and its epilogue: gated,
+// W the packed [cols = 2N][K] weight and Y [M][N]; else W [cols][K], Y [M][cols].
+hipError_t launch_lora_project(const uint16_t *X, const uint16_t *W, uint16_t *Y, int M, int cols,
+                               int K, bool gated, const LoraTable &t, const int *ids, int slots,
+                               const uint16_t *T, const GemmWorkspace &ws, hipStream_t stream);
+// launch_lora_project for M <= 128 (kernels that stream the weight).
+hipError_t launch_lora_stream(const uint16_t *X, const uint16_t *W, uint16_t *Y, int M, int cols,
+                              int K, bool gated, const LoraTable &t, const int *ids, int slots,
+                              const uint16_t *T, const GemmWorkspace &ws, hipStream_t stream);
 // Largest workgroup count any launcher uses for an M x cols output tile grid.
 int64_t max_tiles(int64_t M, int64_t cols);
 

@@ -15,6 +15,7 @@
 
 #include "device.hpp"
 #include "gemm_core.hpp"
+#include "lora.hpp"
 #include "split_tail.hpp"
 
 namespace swiglu {
@@ -275,6 +276,24 @@ struct StoreEpilogue {
     __device__ __forceinline__ static int unit_block(int u, int) { return u; }
 };
 
+// An epilogue whose projection has low-rank adapters beside it: their terms are
+// expanded into the accumulators before Base's epilogue (lora.hpp).
+template <class Base>
+struct WithLora : Base {
+    LoraTerm lora;
+};
+using PairMulLora = WithLora<PairMulEpilogue>;
+using StoreLora = WithLora<StoreEpilogue>;
+template <class S, class Epi>
+__device__ __forceinline__ void expand_adapters(SWIGLU_LDS char *lds, const Epi &epi,
+                                                typename S::Acc (&acc)[S::TM][S::TN], int m0,
+                                                int n0) {
+    if constexpr (std::is_same<Epi, PairMulLora>::value)
+        lora_expand<S, true>(lds, epi.lora, acc, m0, n0);
+    else if constexpr (std::is_same<Epi, StoreLora>::value)
+        lora_expand<S, false>(lds, epi.lora, acc, m0, n0);
+}
+
 // The K steps [0, len) of one tile into `acc`.  With 16x16 MFMAs the first
 // step's MFMAs start the accumulators (C = 0): no vector instructions zero its
 // 256 registers first.  32x32 MFMAs accumulate onto zeros (zero_acc_mi32
@@ -379,6 +398,7 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
                 run_tile<S, kEven>(pl, issue, nk, acc);
                 pl.drain(acc);
                 const int m0 = tm * S::BM, n0 = tn * S::BN;
+                expand_adapters<S>(lds, epi, acc, m0, n0);
                 if (j + grid < sch.dp) {
                     tile_coords(xcd_order(j + grid, sch.dp), sch.tiles_m, sch.tiles_n, sch.group_m, tm,
                                 tn);
@@ -407,6 +427,7 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             if (m0 >= M || n0 >= B.rows) continue;   // quarter wholly past the output's edge
             typename Q::Acc acc[Q::TM][Q::TN];
             tile_mainloop<Q, kEven>(lds, Ak, B, M, K, m0, n0, 0, sch.nk, sch.nk, acc);
+            expand_adapters<Q>(lds, epi, acc, m0, n0);
             epi.template apply<Q>(acc, m0, n0, threadIdx.x);
         }
         whole_tiles();
@@ -470,6 +491,8 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             tile_coords(t, sch.tiles_m, sch.tiles_n, sch.group_m, tm, tn);
             typename S::Acc acc[S::TM][S::TN];
             tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
+            // (the adapters' terms once a tile)
+            if (piece == sch.pieces - 1) expand_adapters<S>(lds, epi, acc, tm * S::BM, tn * S::BN);
             store_partial<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN, acc,
                              threadIdx.x);
         }

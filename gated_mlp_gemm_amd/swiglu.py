@@ -33,6 +33,8 @@ SWIGLU_ERR_ALIAS = -6
 SWIGLU_AUTO = 0
 SWIGLU_VARIANT_S = 1
 SWIGLU_VARIANT_I = 2
+SWIGLU_F32 = 0
+SWIGLU_BF16 = 1
 VARIANTS = {"auto": SWIGLU_AUTO, "s": SWIGLU_VARIANT_S, "i": SWIGLU_VARIANT_I}
 
 
@@ -71,6 +73,15 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.swiglu_fp8_scale_exp.argtypes = [ctypes.c_double]
     lib.swiglu_quantize_fp8.argtypes = [P, P, I64, I32, P]
     lib.swiglu_fused_gemm_fp8.argtypes = [P, P, P, I64, I64, I64, I32, I32, I32, P, U64, P]
+    lib.swiglu_route_workspace_size.argtypes = [I64, I64, ctypes.POINTER(U64)]
+    lib.swiglu_route.argtypes = [P, I32, P, P, P, P, P, I64, I64, I64, I32, P, U64, P]
+    lib.swiglu_route_backward.argtypes = [P, I32, P, P, P, P, P, P, P, I64, I64, I64, I32, P]
+    lib.swiglu_lora_workspace_size.argtypes = [I64, I64, I64, I64, I64, ctypes.POINTER(U64)]
+    lib.swiglu_fused_gemm_lora.argtypes = [P, P, P, P, P, I64, I64, P, P, P, I64, I64, I64, I64, P,
+                                           U64, P]
+    lib.swiglu_down_proj_lora.argtypes = lib.swiglu_fused_gemm_lora.argtypes
+    lib.swiglu_gated_mlp_lora.argtypes = [P, P, P, P, P, P, I64, I64, P, P, P, I64, I64, P, P, P, P,
+                                          I64, I64, I64, I64, P, U64, P]
     lib.swiglu_select_variant.argtypes = [I64, I64, I64]
     lib.swiglu_m_switch.argtypes = []
     lib.swiglu_m_switch.restype = I64
@@ -83,7 +94,9 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
                  "swiglu_describe_launch", "swiglu_pack_weights_nk", "swiglu_down_proj",
                  "swiglu_gated_mlp", "swiglu_fp8_scale_exp", "swiglu_quantize_fp8",
                  "swiglu_fused_gemm_fp8", "swiglu_fused_gemm_strided",
-                 "swiglu_fused_gemm_noalloc"):
+                 "swiglu_fused_gemm_noalloc", "swiglu_route_workspace_size", "swiglu_route",
+                 "swiglu_route_backward", "swiglu_lora_workspace_size", "swiglu_fused_gemm_lora",
+                 "swiglu_down_proj_lora", "swiglu_gated_mlp_lora"):
         getattr(lib, name).restype = I32
     _lib = lib
     return lib
@@ -444,6 +457,267 @@ def swiglu_fused_gemm_fp8(A8: torch.Tensor, W_fused8: torch.Tensor, a_exp: int, 
                                          int(w_exp), v, ws, wsb, _stream(A8.device)),
                "swiglu_fused_gemm_fp8")
     return Y
+
+
+# ---------------------------------------------------------------------------
+# router
+# ---------------------------------------------------------------------------
+_LOGITS_TYPES = {torch.float32: SWIGLU_F32, torch.bfloat16: SWIGLU_BF16}
+
+
+def _dev_typed(t: torch.Tensor, name: str, dtype, shape) -> torch.Tensor:
+    """A contiguous device tensor of the given type and shape."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a ROCm device, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.shape != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _logits_type(logits: torch.Tensor) -> int:
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if logits.dtype not in _LOGITS_TYPES:
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [M, E], got {tuple(logits.shape)}")
+    return _LOGITS_TYPES[logits.dtype]
+
+
+def swiglu_route_workspace_size(M: int, E: int) -> int:
+    """Bytes of scratch that let swiglu_route use more than one workgroup."""
+    out = ctypes.c_uint64(0)
+    _check(load_library().swiglu_route_workspace_size(M, E, ctypes.byref(out)),
+           "swiglu_route_workspace_size")
+    return int(out.value)
+
+
+def swiglu_route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] = None,
+                 normalize: bool = True, ids: Optional[torch.Tensor] = None,
+                 weights: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                 loss: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None
+                 ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Top-k of the softmax of logits [M, E] (float32 or bfloat16).
+
+    Returns (ids [M, k] int32, weights [M, k] float32, counts [E + 1] int32,
+    loss, a float32 scalar): the picks in descending order with -1 / 0 where a
+    row has none, the picks of each expert followed by the rows that route, and
+    the balance loss.  valid: [M] uint8 or bool, 0 for rows of padding.
+    """
+    lib = load_library()
+    kind = _logits_type(logits)
+    M, E = logits.shape
+    _dev_typed(logits, "logits", logits.dtype, (M, E))
+    dev, k = logits.device, int(k)
+    if valid is not None:
+        if isinstance(valid, torch.Tensor) and valid.dtype == torch.bool:
+            valid = valid.view(torch.uint8)
+        _dev_typed(valid, "valid", torch.uint8, (M,))
+    rows = (M, max(k, 0))
+    ids = torch.empty(rows, dtype=torch.int32, device=dev) if ids is None else ids
+    weights = torch.empty(rows, dtype=torch.float32, device=dev) if weights is None else weights
+    counts = torch.empty(E + 1, dtype=torch.int32, device=dev) if counts is None else counts
+    loss = torch.empty((), dtype=torch.float32, device=dev) if loss is None else loss
+    _dev_typed(ids, "ids", torch.int32, rows)
+    _dev_typed(weights, "weights", torch.float32, rows)
+    _dev_typed(counts, "counts", torch.int32, (E + 1,))
+    _dev_typed(loss, "loss", torch.float32, ())
+    with _on_device(dev):
+        if workspace is None:
+            n = swiglu_route_workspace_size(M, E)
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_route(_ptr(logits), kind, _ptr(valid), _ptr(ids), _ptr(weights),
+                                _ptr(counts), _ptr(loss), M, E, k, int(bool(normalize)), ws, wsb,
+                                _stream(dev)), "swiglu_route")
+    return ids, weights, counts, loss
+
+
+def swiglu_route_backward(logits: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
+                          counts: torch.Tensor, d_weights: Optional[torch.Tensor] = None,
+                          d_loss: Optional[torch.Tensor] = None,
+                          valid: Optional[torch.Tensor] = None, normalize: bool = True,
+                          d_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient by the logits (of their type) from the gradients of
+    swiglu_route's weights [M, k] and loss (a device scalar), None for none;
+    ids, weights, counts: what swiglu_route returned for these logits."""
+    lib = load_library()
+    kind = _logits_type(logits)
+    M, E = logits.shape
+    _dev_typed(logits, "logits", logits.dtype, (M, E))
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be [M, k]")
+    k = ids.shape[1]
+    _dev_typed(ids, "ids", torch.int32, (M, k))
+    _dev_typed(weights, "weights", torch.float32, (M, k))
+    _dev_typed(counts, "counts", torch.int32, (E + 1,))
+    if valid is not None:
+        if isinstance(valid, torch.Tensor) and valid.dtype == torch.bool:
+            valid = valid.view(torch.uint8)
+        _dev_typed(valid, "valid", torch.uint8, (M,))
+    if d_weights is not None:
+        _dev_typed(d_weights, "d_weights", torch.float32, (M, k))
+    if d_loss is not None:
+        _dev_typed(d_loss, "d_loss", torch.float32, ())
+    if d_logits is None:
+        d_logits = torch.empty_like(logits)
+    _dev_typed(d_logits, "d_logits", logits.dtype, (M, E))
+    with _on_device(logits.device):
+        _check(lib.swiglu_route_backward(_ptr(logits), kind, _ptr(valid), _ptr(ids), _ptr(weights),
+                                         _ptr(counts), _ptr(d_weights), _ptr(d_loss),
+                                         _ptr(d_logits), M, E, k, int(bool(normalize)),
+                                         _stream(logits.device)), "swiglu_route_backward")
+    return d_logits
+
+
+# ---------------------------------------------------------------------------
+# low-rank adapters
+# ---------------------------------------------------------------------------
+class SwigluLora:
+    """A table of low-rank adapters beside a projection: A [count, parts * rank, K],
+    B [count, columns, rank] (bfloat16) and scale [count] (float32), checked once
+    here.  parts is 2 beside W_fused (columns 2N, Gate and Up rows interleaved as
+    in it; A's first `rank` rows Gate's), 1 beside W3t."""
+    __slots__ = ("A", "B", "scale", "count", "rank", "columns", "a_rows", "K", "_args")
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor):
+        for name, t in (("A", A), ("B", B)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dim() != 3:
+                raise ValueError(f"{name} must have three dimensions, got {tuple(t.shape)}")
+        self.count, self.a_rows, self.K = A.shape
+        self.columns, self.rank = B.shape[1], B.shape[2]
+        self.A = _dev_tensor(A, "A", (self.count, self.a_rows, self.K))
+        self.B = _dev_tensor(B, "B", (self.count, self.columns, self.rank))
+        self.scale = _dev_typed(scale, "scale", torch.float32, (self.count,))
+        self._args = (A.data_ptr(), B.data_ptr(), scale.data_ptr(), self.count, self.rank)
+
+    def _beside(self, name: str, parts: int, columns: int, K: int):
+        """The C arguments, once the table is one for a [columns, K] weight."""
+        if (self.columns, self.K, self.a_rows) != (columns, K, parts * self.rank):
+            raise ValueError(
+                f"{name}: A {tuple(self.A.shape)} and B {tuple(self.B.shape)} do not fit a "
+                f"[{columns}, {K}] weight with {parts} part(s)")
+        return self._args
+
+
+def swiglu_lora_workspace_size(M: int, N: int, K: int, slots: int, rank: int) -> int:
+    """Bytes of scratch for the calls with adapters ([M, N] SwiGLU output, model
+    width K; `rank` the larger of the two tables' for the MLP block)."""
+    out = ctypes.c_uint64(0)
+    _check(load_library().swiglu_lora_workspace_size(M, N, K, slots, rank, ctypes.byref(out)),
+           "swiglu_lora_workspace_size")
+    return int(out.value)
+
+
+def make_lora_workspace(M: int, N: int, K: int, slots: int, rank: int,
+                        device="cuda") -> torch.Tensor:
+    """A device scratch tensor of swiglu_lora_workspace_size() bytes; needs no
+    initialisation and may be reused by later stream-ordered calls."""
+    return torch.empty(swiglu_lora_workspace_size(M, N, K, slots, rank), dtype=torch.uint8,
+                       device=device)
+
+
+def _slots(ids: torch.Tensor, weights: Optional[torch.Tensor], M: int) -> int:
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be [M, slots]")
+    J = ids.shape[1]
+    _dev_typed(ids, "ids", torch.int32, (M, J))
+    if weights is not None:
+        _dev_typed(weights, "weights", torch.float32, (M, J))
+    return J
+
+
+def swiglu_fused_gemm_lora(A: torch.Tensor, W_fused: torch.Tensor, lora: SwigluLora,
+                           ids: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                           Y: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """swiglu_fused_gemm with each row's adapters added to Gate and Up: ids
+    [M, slots] int32 (-1: none), weights [M, slots] float32 (None: ones)."""
+    lib = load_library()
+    M, K = A.shape
+    _dev_tensor(A, "A", (M, K))
+    N = W_fused.shape[0] // 2
+    _dev_tensor(W_fused, "W_fused", (2 * N, K))
+    J = _slots(ids, weights, M)
+    table = lora._beside("lora", 2, 2 * N, K)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+    _dev_tensor(Y, "Y", (M, N))
+    with _on_device(A.device):
+        if workspace is None:
+            workspace = make_lora_workspace(M, N, K, J, lora.rank, A.device)
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_fused_gemm_lora(_ptr(A), _ptr(W_fused), *table, _ptr(ids), _ptr(weights),
+                                          _ptr(Y), M, N, K, J, ws, wsb, _stream(A.device)),
+               "swiglu_fused_gemm_lora")
+    return Y
+
+
+def swiglu_down_proj_lora(H: torch.Tensor, W3t: torch.Tensor, lora: SwigluLora,
+                          ids: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                          Out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """swiglu_down_proj with each row's adapters added (ids, weights as in
+    swiglu_fused_gemm_lora)."""
+    lib = load_library()
+    M, N = H.shape
+    D = W3t.shape[0]
+    _dev_tensor(H, "H", (M, N))
+    _dev_tensor(W3t, "W3t", (D, N))
+    J = _slots(ids, weights, M)
+    table = lora._beside("lora", 1, D, N)
+    if Out is None:
+        Out = torch.empty((M, D), dtype=torch.bfloat16, device=H.device)
+    _dev_tensor(Out, "Out", (M, D))
+    with _on_device(H.device):
+        if workspace is None:
+            workspace = make_lora_workspace(M, N, D, J, lora.rank, H.device)
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_down_proj_lora(_ptr(H), _ptr(W3t), *table, _ptr(ids), _ptr(weights),
+                                         _ptr(Out), M, N, D, J, ws, wsb, _stream(H.device)),
+               "swiglu_down_proj_lora")
+    return Out
+
+
+def swiglu_gated_mlp_lora(A: torch.Tensor, W_fused: torch.Tensor, W3t: torch.Tensor,
+                          gate_up: SwigluLora, down: SwigluLora, ids: torch.Tensor,
+                          weights: Optional[torch.Tensor] = None,
+                          H: Optional[torch.Tensor] = None, Out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None
+                          ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """swiglu_gated_mlp with each row's adapters added to all three projections
+    (one table for Gate and Up, one for the down projection; the same ids and
+    weights, e.g. swiglu_route's); returns (Out, H)."""
+    lib = load_library()
+    M, K = A.shape
+    N = W_fused.shape[0] // 2
+    _dev_tensor(A, "A", (M, K))
+    _dev_tensor(W_fused, "W_fused", (2 * N, K))
+    _dev_tensor(W3t, "W3t", (K, N))
+    J = _slots(ids, weights, M)
+    up, dn = gate_up._beside("gate_up", 2, 2 * N, K), down._beside("down", 1, K, N)
+    if H is None:
+        H = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+    if Out is None:
+        Out = torch.empty((M, K), dtype=torch.bfloat16, device=A.device)
+    _dev_tensor(H, "H", (M, N))
+    _dev_tensor(Out, "Out", (M, K))
+    with _on_device(A.device):
+        if workspace is None:
+            workspace = make_lora_workspace(M, N, K, J, max(gate_up.rank, down.rank), A.device)
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_gated_mlp_lora(_ptr(A), _ptr(W_fused), _ptr(W3t), *up, *dn, _ptr(ids),
+                                         _ptr(weights), _ptr(H), _ptr(Out), M, N, K, J, ws, wsb,
+                                         _stream(A.device)), "swiglu_gated_mlp_lora")
+    return Out, H
 
 
 def swiglu_select_variant(M: int, N: int = 0, K: int = 0) -> int:

@@ -84,6 +84,9 @@ typedef enum swiglu_variant {
     SWIGLU_VARIANT_I = 2  /* interleaved: one GEMM over W_fused, paired epilogue */
 } swiglu_variant;
 
+/* Element types of the router's logits (swiglu_route). */
+typedef enum swiglu_type { SWIGLU_F32 = 0, SWIGLU_BF16 = 1 } swiglu_type;
+
 /*
  * Interleave W1 and W2 column by column into W_fused (the fused weight of the
  * pages' Kernel-2; gist.science technical summary, Method, Kernel-2: even
@@ -306,6 +309,98 @@ int swiglu_fused_gemm_fp8(const uint8_t *A8, const uint8_t *W_fused8,
                           uint16_t *Y, int64_t M, int64_t N, int64_t K,
                           int a_exp, int w_exp, int variant, void *workspace,
                           uint64_t workspace_bytes, void *stream);
+
+/*
+ * The router in front of a table of experts or adapters.  For row m of the
+ * logits z [M][E] (row-major, fp32 or bf16 as `logits_type` says) with
+ * p = softmax(z[m]), the k largest logits in descending order (of equal ones
+ * the lowest index first):
+ *     ids[m][j]      their indices; -1 where the row has no j-th logit above -inf
+ *     weights[m][j]  p[id], or, normalize != 0, p[id] / (the sum over the row's
+ *                    picks); 0 where ids is -1
+ * and over the n rows that route, with c[e] picks of e and C = sum c:
+ *     counts[E + 1]  c[0..E), then n
+ *     loss           E sum_e (c[e] / C) (sum_m p[m][e] / n), 0 when C is 0: the
+ *                    balance loss, 1 when probabilities and picks are even.
+ * A row routes if it has a logit above -inf and `valid` (NULL, or one byte a
+ * row) is not 0 for it; one that does not gets ids -1 and weights 0 and counts
+ * nowhere.  A NaN logit makes its row's weights and the loss NaN.  Sums over a
+ * row are fp32, sums over rows fp32 in each workgroup and 64-bit over
+ * workgroups, in a fixed order: the same call gives the same bits.
+ * Preconditions: 0 <= M <= 2^31 - 1, 1 <= E <= 512, 1 <= k <= min(E, 16);
+ * pointers aligned to their element; outputs overlap nothing.  M == 0: counts
+ * and loss are written (zeros).  workspace: at least
+ * swiglu_route_workspace_size() bytes, 256-byte aligned, no initialisation;
+ * NULL or too small: one workgroup does all rows.
+ *
+ * swiglu_route_backward: d_logits [M][E] (the logits' type) from d_weights
+ * [M][k] (NULL: zeros) and the scalar d_loss (NULL: zero), given what
+ * swiglu_route returned.  ids and counts are constants of the gradient.  Rows
+ * that do not route, and logits of -inf, get zeros.  M == 0 launches nothing.
+ */
+int swiglu_route_workspace_size(int64_t M, int64_t E, uint64_t *bytes);
+int swiglu_route(const void *logits, int logits_type, const uint8_t *valid, int32_t *ids,
+                 float *weights, int32_t *counts, float *loss, int64_t M, int64_t E, int64_t k,
+                 int normalize, void *workspace, uint64_t workspace_bytes, void *stream);
+int swiglu_route_backward(const void *logits, int logits_type, const uint8_t *valid,
+                          const int32_t *ids, const float *weights, const int32_t *counts,
+                          const float *d_weights, const float *d_loss, void *d_logits, int64_t M,
+                          int64_t E, int64_t k, int normalize, void *stream);
+
+/*
+ * Low-rank adapters of many requests at once beside the shared projections.
+ * A table holds `count` adapters of one `rank`:
+ *     lora_a      [count][parts * rank][K]   (K-contiguous rows)
+ *     lora_b      [count][columns][rank]
+ *     lora_scale  [count], fp32
+ * parts is 2 beside W_fused (columns = 2N, Gate and Up rows interleaved as the
+ * packed weight's; the first `rank` rows of an adapter's A are Gate's, the
+ * rest Up's; swiglu_pack_weights_nk interleaves B's Gate and Up rows too, as
+ * any two [N][rank] arrays), 1 beside W3t (columns = D).  Row m takes the
+ * adapters ids[m][0..slots) with weights[m][0..slots) (NULL: ones); an id
+ * outside [0, count), such as -1, takes none, and an adapter named twice
+ * counts with the sum of its weights:
+ *     D[m] = X[m] . W + sum_j weights[m][j] scale[id] (X[m] . A[id]^T) . B[id]^T
+ *
+ * swiglu_fused_gemm_lora   Y = bf16(SiLU(Gate) * Up) of that D over W_fused
+ * swiglu_down_proj_lora    Out = bf16(D) over W3t
+ * swiglu_gated_mlp_lora    the two in turn, H between them as in
+ *                          swiglu_gated_mlp, one table for each, the same ids
+ *                          and weights for both (e.g. swiglu_route's)
+ *
+ * X . A^T times weight and scale is rounded to bf16 before the product with B;
+ * all sums are fp32, Y, H and Out are rounded once.  Results are bitwise
+ * reproducible for the same arguments and workspace size.  A row's result does
+ * not depend on other rows' ids, except that infinities and NaN in the B of
+ * one row's adapter may reach the rows computed with it as NaN.
+ * Preconditions: those of the call without adapters; 1 <= slots <= 8; rank a
+ * multiple of 8 in [8, 256]; 1 <= count <= 8192; matrices 16-byte, ids,
+ * weights and scale 4-byte aligned; outputs and workspace overlap nothing.
+ * workspace: required, 256-byte aligned, no initialisation: at least
+ * M * slots * (2 * rank) * 2 bytes (gated; rank for the down projection)
+ * rounded up to 256, and with swiglu_lora_workspace_size() bytes the calls may
+ * also split tiles along K, as without adapters.
+ */
+int swiglu_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t slots, int64_t rank,
+                               uint64_t *bytes);
+int swiglu_fused_gemm_lora(const uint16_t *X, const uint16_t *W_fused, const uint16_t *lora_a,
+                           const uint16_t *lora_b, const float *lora_scale, int64_t count,
+                           int64_t rank, const int32_t *ids, const float *weights, uint16_t *Y,
+                           int64_t M, int64_t N, int64_t K, int64_t slots, void *workspace,
+                           uint64_t workspace_bytes, void *stream);
+int swiglu_down_proj_lora(const uint16_t *H, const uint16_t *W3t, const uint16_t *lora_a,
+                          const uint16_t *lora_b, const float *lora_scale, int64_t count,
+                          int64_t rank, const int32_t *ids, const float *weights, uint16_t *Out,
+                          int64_t M, int64_t N, int64_t D, int64_t slots, void *workspace,
+                          uint64_t workspace_bytes, void *stream);
+int swiglu_gated_mlp_lora(const uint16_t *X, const uint16_t *W_fused, const uint16_t *W3t,
+                          const uint16_t *gate_up_a, const uint16_t *gate_up_b,
+                          const float *gate_up_scale, int64_t gate_up_count, int64_t gate_up_rank,
+                          const uint16_t *down_a, const uint16_t *down_b, const float *down_scale,
+                          int64_t down_count, int64_t down_rank, const int32_t *ids,
+                          const float *weights, uint16_t *H, uint16_t *Out, int64_t M, int64_t N,
+                          int64_t K, int64_t slots, void *workspace, uint64_t workspace_bytes,
+                          void *stream);
 
 /*
  * What a call would launch, as text (host only; queries the current device's
