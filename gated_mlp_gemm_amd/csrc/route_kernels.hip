@@ -48,9 +48,14 @@ template <int STEP>
 __device__ __forceinline__ float partner_f(float v) {
     return __builtin_bit_cast(float, partner<STEP>(__builtin_bit_cast(uint32_t, v)));
 }
+// The larger of two, or NaN if one is NaN (one instruction): a row with a NaN
+// routes, with weights of NaN.
+__device__ __forceinline__ float nan_max(float a, float b) {
+    return __builtin_elementwise_maximum(a, b);
+}
 template <int LPR, int STEP = 0>
 __device__ __forceinline__ float row_max(float v) {
-    if constexpr ((1 << STEP) < LPR) return row_max<LPR, STEP + 1>(fmaxf(v, partner_f<STEP>(v)));
+    if constexpr ((1 << STEP) < LPR) return row_max<LPR, STEP + 1>(nan_max(v, partner_f<STEP>(v)));
     else return v;
 }
 template <int LPR, int STEP = 0>
@@ -122,9 +127,9 @@ __device__ __forceinline__ bool row_softmax(float (&v)[kRouteValues], bool wante
                                             float &inv) {
     float m = v[0];
 #pragma unroll
-    for (int i = 1; i < kRouteValues; ++i) m = fmaxf(m, v[i]);
+    for (int i = 1; i < kRouteValues; ++i) m = nan_max(m, v[i]);
     top = row_max<LPR>(m);
-    const bool live = wanted && top > kNegInf;
+    const bool live = wanted && top != kNegInf;
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < kRouteValues; ++i) {
