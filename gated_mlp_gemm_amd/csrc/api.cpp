@@ -258,9 +258,15 @@ int check_lora(int64_t slots, int64_t count, int64_t rank) {
     return SWIGLU_OK;
 }
 
-// Bytes of the workspace that hold T [M][slots][width] (bf16), a multiple of 256.
+// Bytes of the workspace that hold T [M][slots][width], and with the plans of
+// the expansion behind it; multiples of 256.
 uint64_t lora_t_bytes(int64_t M, int64_t slots, int64_t width) {
-    return (static_cast<uint64_t>(M) * slots * width * 2 + 255) & ~uint64_t{255};
+    return (static_cast<uint64_t>(M) * slots * width * 4 + 255) & ~uint64_t{255};
+}
+uint64_t lora_state_bytes(int64_t M, int64_t slots, int64_t width, int64_t count) {
+    const uint64_t plans = static_cast<uint64_t>((M + 63) / 64) *
+                           swiglu::lora_plan_bytes(swiglu::lora_capacity((int)count, (int)slots));
+    return lora_t_bytes(M, slots, width) + ((plans + 255) & ~uint64_t{255});
 }
 int check_lora_workspace(const void *workspace, uint64_t bytes, uint64_t need) {
     if (!workspace) return fail(SWIGLU_ERR_NULL, "workspace is required");
@@ -278,14 +284,17 @@ hipError_t lora_projection(const uint16_t *X, const uint16_t *W, uint16_t *Y, in
                            const int32_t *ids, const float *weights, int64_t slots,
                            void *workspace, uint64_t bytes, int cus, hipStream_t s) {
     const int parts = gated ? 2 : 1;
-    const uint64_t t_bytes = lora_t_bytes(M, slots, parts * t.rank);
+    const uint64_t state = lora_state_bytes(M, slots, parts * t.rank, t.count);
     uint16_t *T = static_cast<uint16_t *>(workspace);
-    const hipError_t e = swiglu::launch_lora_shrink(X, t, ids, weights, (int)slots, T, (int)M,
-                                                    (int)K, parts, s);
+    char *plans = static_cast<char *>(workspace) + lora_t_bytes(M, slots, parts * t.rank);
+    // the two launches run in stream order: they share scratch and counters
+    const swiglu::GemmWorkspace ws =
+        make_ws(static_cast<char *>(workspace) + state, bytes - state, cus);
+    const hipError_t e = swiglu::launch_lora_shrink(X, t, ids, weights, (int)slots, T, plans,
+                                                    (int)M, (int)K, parts, ws, s);
     if (e != hipSuccess) return e;
-    return swiglu::launch_lora_project(
-        X, W, Y, (int)M, (int)cols, (int)K, gated, t, ids, (int)slots, T,
-        make_ws(static_cast<char *>(workspace) + t_bytes, bytes - t_bytes, cus), s);
+    return swiglu::launch_lora_project(X, W, Y, (int)M, (int)cols, (int)K, gated, t,
+                                       (int)slots, T, plans, ws, s);
 }
 
 int launched(hipError_t e, const char *what) {
@@ -800,7 +809,8 @@ int swiglu_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t slots, i
     int cus = 0;
     st = check_device(&cus);
     if (st != SWIGLU_OK) return st;
-    *bytes = lora_t_bytes(M, slots, 2 * rank) + swiglu::workspace_bytes_for(cus);
+    *bytes = lora_state_bytes(M, slots, 2 * rank, swiglu::kMaxLoraCount) +
+             swiglu::workspace_bytes_for(cus);
     return ok();
 }
 
@@ -813,7 +823,8 @@ int swiglu_fused_gemm_lora(const uint16_t *X, const uint16_t *W_fused, const uin
     if (st == SWIGLU_OK) st = check_lora(slots, count, rank);
     if (st != SWIGLU_OK) return st;
     if (M == 0 || N == 0) return ok();
-    st = check_lora_workspace(workspace, workspace_bytes, lora_t_bytes(M, slots, 2 * rank));
+    st = check_lora_workspace(workspace, workspace_bytes,
+                              lora_state_bytes(M, slots, 2 * rank, count));
     if (st != SWIGLU_OK) return st;
     const Operand ops[] = {
         {"X", X, M * K * 2, 16, false, false},
@@ -846,7 +857,7 @@ int swiglu_down_proj_lora(const uint16_t *H, const uint16_t *W3t, const uint16_t
     if (st == SWIGLU_OK) st = check_lora(slots, count, rank);
     if (st != SWIGLU_OK) return st;
     if (M == 0 || D == 0) return ok();
-    st = check_lora_workspace(workspace, workspace_bytes, lora_t_bytes(M, slots, rank));
+    st = check_lora_workspace(workspace, workspace_bytes, lora_state_bytes(M, slots, rank, count));
     if (st != SWIGLU_OK) return st;
     const Operand ops[] = {
         {"H", H, M * N * 2, 16, false, false},
@@ -884,8 +895,8 @@ int swiglu_gated_mlp_lora(const uint16_t *X, const uint16_t *W_fused, const uint
     if (st == SWIGLU_OK) st = check_lora(slots, down_count, down_rank);
     if (st != SWIGLU_OK) return st;
     if (M == 0) return ok();
-    const uint64_t need_up = lora_t_bytes(M, slots, 2 * gate_up_rank);
-    const uint64_t need_down = lora_t_bytes(M, slots, down_rank);
+    const uint64_t need_up = lora_state_bytes(M, slots, 2 * gate_up_rank, gate_up_count);
+    const uint64_t need_down = lora_state_bytes(M, slots, down_rank, down_count);
     st = check_lora_workspace(workspace, workspace_bytes, need_up > need_down ? need_up : need_down);
     if (st != SWIGLU_OK) return st;
     const Operand ops[] = {

@@ -648,7 +648,7 @@ struct Pipeline {
     // barrier) 2, 4 and 8 are within 0.3 % of each other and 0.2-1.5 %
     // faster than 16 on those two workloads, M=8192 K=5120 N=13824 and
     // variant S, 24 and 32 are 0.8-4.6 % slower (more delays the refill loads).
-    static constexpr int kEarlyMfma = kMfma16 / 8;
+    static constexpr int kEarlyMfma = kMfma16 < 8 ? 1 : kMfma16 / 8;
     static_assert(S::MI != 16 || (kEarlyMfma > 0 && kEarlyMfma < kMfma16),
                   "MFMAs on both sides of the barrier");
 

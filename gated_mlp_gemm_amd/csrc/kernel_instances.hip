@@ -116,6 +116,12 @@ template struct TilesLaunch<ShapeWide, StoreLora, kTailSplit>;
 #elif SWIGLU_INSTANCE == 20
 template struct TilesLaunch<ShapeQuad, PairMulLora, kTailSplit>;
 template struct TilesLaunch<ShapeQuad, StoreLora, kTailSplit>;
+#elif SWIGLU_INSTANCE == 21
+template struct TilesLaunch<ShapeSplitK, PairMulLora, kTailReduceInKernel>;
+template struct TilesLaunch<ShapeSmallLora, PairMulLora, kTailSplit>;
+template struct TilesLaunch<ShapeSmallLora, StoreLora, kTailSplit>;
+template struct ReduceLaunch<ShapeSmallLora, PairMulEpilogue>;
+template struct ReduceLaunch<ShapeSmallLora, StoreEpilogue>;
 #else
 #error "SWIGLU_INSTANCE is past the end of the instance list"
 #endif

@@ -622,27 +622,35 @@ static hipError_t launch_lora_gemm(const KMajor &A, KMajor B, int M, int cols, i
     return ReduceLaunch<S, Base>::run(sch.split_tiles * kWavesPerTile, epi, sch, stream);
 }
 
+template <class Epi, class Base>
+static hipError_t launch_lora(const KMajor &A, const KMajor &B, int M, int cols, int K,
+                              const Epi &epi, const GemmWorkspace &ws, hipStream_t stream) {
+    if (M <= 128) {
+        if constexpr (std::is_same<Epi, PairMulLora>::value) {
+            const Schedule fx = make_fixup_schedule<ShapeSplitK>(M, cols, K, ws);
+            if (fx.pieces) return launch_reduce_in_kernel<ShapeSplitK>(A, B, M, K, epi, fx, stream);
+            if (small_m_quad_tiles(M, cols, ws))
+                return launch_lora_gemm<ShapeQuad, Epi, Base>(A, B, M, cols, K, epi, ws, stream);
+        }
+        return launch_lora_gemm<ShapeSmallLora, Epi, Base>(A, B, M, cols, K, epi, ws, stream);
+    }
+    if (quad_tiles_faster(M, cols, K, ws))
+        return launch_lora_gemm<ShapeQuad, Epi, Base>(A, B, M, cols, K, epi, ws, stream);
+    return launch_lora_gemm<ShapeWide, Epi, Base>(A, B, M, cols, K, epi, ws, stream);
+}
+
 hipError_t launch_lora_project(const uint16_t *X, const uint16_t *W, uint16_t *Y, int M, int cols,
-                               int K, bool gated, const LoraTable &t, const int *ids, int slots,
-                               const uint16_t *T, const GemmWorkspace &ws, hipStream_t stream) {
-    if (M <= 128)
-        return launch_lora_stream(X, W, Y, M, cols, K, gated, t, ids, slots, T, ws, stream);
+                               int K, bool gated, const LoraTable &t, int slots, const uint16_t *T,
+                               const char *plans, const GemmWorkspace &ws, hipStream_t stream) {
     const KMajor A{X, M, 1, 0, 0, 0};
     const KMajor B{W, cols, 1, 0, 0, 0};
-    const LoraTerm lora{T, t.B, ids, M, slots, t.rank, t.count, cols};
-    const bool quad = quad_tiles_faster(M, cols, K, ws);
-    if (gated) {
-        const PairMulLora epi{{Y, M, cols / 2, cols / 2, 1.0f}, lora};
-        return quad ? launch_lora_gemm<ShapeQuad, PairMulLora, PairMulEpilogue>(A, B, M, cols, K, epi,
-                                                                               ws, stream)
-                    : launch_lora_gemm<ShapeWide, PairMulLora, PairMulEpilogue>(A, B, M, cols, K, epi,
-                                                                               ws, stream);
-    }
-    const StoreLora epi{{Y, M, cols}, lora};
-    return quad ? launch_lora_gemm<ShapeQuad, StoreLora, StoreEpilogue>(A, B, M, cols, K, epi, ws,
-                                                                       stream)
-                : launch_lora_gemm<ShapeWide, StoreLora, StoreEpilogue>(A, B, M, cols, K, epi, ws,
-                                                                       stream);
+    const int capacity = lora_capacity(t.count, slots);
+    const LoraTerm lora{T, t.B, plans, lora_plan_bytes(capacity), capacity, M, slots, t.rank, cols};
+    if (gated)
+        return launch_lora<PairMulLora, PairMulEpilogue>(
+            A, B, M, cols, K, PairMulLora{{Y, M, cols / 2, cols / 2, 1.0f}, lora}, ws, stream);
+    return launch_lora<StoreLora, StoreEpilogue>(A, B, M, cols, K, StoreLora{{Y, M, cols}, lora}, ws,
+                                                 stream);
 }
 
 // One 256x256 fp32 slot per CU: a split schedule has at most one piece per

@@ -88,19 +88,19 @@ struct LoraTable {
     const float *scale;      // [count]
     int count, rank;
 };
-// T [M][slots][parts * rank] = bf16(weight scale X . A^T) of each row's adapters.
+// Entries of a plan of 64 rows and its bytes (lora.hpp).
+int lora_capacity(int count, int slots);
+int lora_plan_bytes(int capacity);
+// T [M][slots][parts * rank] = weight scale X . A^T of each row's adapters, 4 bytes an
+// element, and the plans of each 64 rows (lora.hpp).  ws: scratch to split K (may be empty).
 hipError_t launch_lora_shrink(const uint16_t *X, const LoraTable &t, const int *ids,
-                              const float *weights, int slots, uint16_t *T, int M, int K,
-                              int parts, hipStream_t stream);
+                              const float *weights, int slots, uint16_t *T, char *plans, int M,
+                              int K, int parts, const GemmWorkspace &ws, hipStream_t stream);
 // The projection of X [M][K] with the expansion of T, and its epilogue: gated,
 // W the packed [cols = 2N][K] weight and Y [M][N]; else W [cols][K], Y [M][cols].
 hipError_t launch_lora_project(const uint16_t *X, const uint16_t *W, uint16_t *Y, int M, int cols,
-                               int K, bool gated, const LoraTable &t, const int *ids, int slots,
-                               const uint16_t *T, const GemmWorkspace &ws, hipStream_t stream);
-// launch_lora_project for M <= 128 (kernels that stream the weight).
-hipError_t launch_lora_stream(const uint16_t *X, const uint16_t *W, uint16_t *Y, int M, int cols,
-                              int K, bool gated, const LoraTable &t, const int *ids, int slots,
-                              const uint16_t *T, const GemmWorkspace &ws, hipStream_t stream);
+                               int K, bool gated, const LoraTable &t, int slots, const uint16_t *T,
+                               const char *plans, const GemmWorkspace &ws, hipStream_t stream);
 // Largest workgroup count any launcher uses for an M x cols output tile grid.
 int64_t max_tiles(int64_t M, int64_t cols);
 

@@ -1,410 +1,290 @@
-// The low-rank adapter kernels outside the tile kernels: the shrink
-// T = weight scale X . A^T, and the projections of at most 128 rows, which
-// stream the weight through registers.  lora.hpp has the mathematics.
+// The shrink of the low-rank adapters, T = weight scale X . A^T, and the plans
+// of the expansion.  lora.hpp has the mathematics and the layouts.
 #include "launch.hpp"
 
 #include "lora.hpp"
 #include "split_tail.hpp"
 
-#include <cstdio>
-
 namespace swiglu {
 
 static inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// 16x16x32 MFMA through the builtin: the accumulators of these kernels are
-// few and short-lived enough for the compiler to place them.
-__device__ __forceinline__ f32x4 mfma_16x16x32(const u32x4 &a, const u32x4 &b, const f32x4 &c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-__device__ __forceinline__ u32x4 bload16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                         r, static_cast<int>(voff), static_cast<int>(soff), 0));
-}
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const uint16_t *base, int64_t row,
-                                                            int rows, int K) {
-    return make_rsrc(base + row * K, static_cast<uint32_t>(rows) * static_cast<uint32_t>(K) * 2u);
+// The adapters that 64 rows from row m0 on name: their slots' ids (-1: none)
+// and weights, and the list of the different adapters, ascending.  Built by one
+// wave: a bit per adapter, set by the slots, then read back 64 adapters at a
+// time (one ballot and one prefix count each, so a table of at most 64 takes
+// one pass).
+struct AdapterList {
+    uint32_t bits[kMaxLoraCount / 32];
+    int ids[kMaxLoraSlots][kPlanRows];
+    float weights[kMaxLoraSlots][kPlanRows];
+    uint16_t list[kPlanRows * kMaxLoraSlots];
+    int n;
+};
+__device__ __forceinline__ void build_list(SWIGLU_LDS AdapterList &l, const int *row_ids,
+                                           const float *row_weights, int m0, int M, int slots,
+                                           int count) {
+    const int lane = threadIdx.x & 63;
+    for (int w = lane; w < (count + 31) / 32; w += 64) l.bits[w] = 0u;
+    const bool here = m0 + lane < M;
+    const int64_t at = static_cast<int64_t>(m0 + lane) * slots;
+    int id[kMaxLoraSlots];
+    float weight[kMaxLoraSlots];
+#pragma unroll
+    for (int j = 0; j < kMaxLoraSlots; ++j) {
+        id[j] = here && j < slots ? row_ids[at + j] : -1;
+        weight[j] = here && j < slots && row_weights ? row_weights[at + j] : 1.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < kMaxLoraSlots; ++j) {
+        if (j >= slots) continue;
+        const bool named = id[j] >= 0 && id[j] < count;
+        l.ids[j][lane] = named ? id[j] : -1;
+        l.weights[j][lane] = weight[j];
+        if (named)
+            __hip_atomic_fetch_or(&l.bits[id[j] >> 5], 1u << (id[j] & 31), __ATOMIC_RELAXED,
+                                  __HIP_MEMORY_SCOPE_WAVEFRONT);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    int n = 0;
+    for (int base = 0; base < count; base += 64) {
+        const int a = base + lane;
+        const bool named = a < count && ((l.bits[a >> 5] >> (a & 31)) & 1u);
+        const uint64_t all = __ballot(named);
+        if (named)
+            l.list[n + __builtin_amdgcn_mbcnt_hi(
+                           static_cast<uint32_t>(all >> 32),
+                           __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(all), 0u))] =
+                static_cast<uint16_t>(a);
+        n += __popcll(all);
+    }
+    if (lane == 0) l.n = n;
 }
 
-// ---------------------------------------------------------------------------
-// Shrink.  One workgroup takes 32 rows of X, one of the adapters that they
-// name at a time, and 64 of that adapter's rows; its waves split K, and their
-// partial sums meet in LDS in wave order.  The adapter's rows are the MFMA's
-// first operand, so that a lane ends with four neighbouring elements of T.
-// Every operand goes from memory to registers, 16 bytes a lane.
-// ---------------------------------------------------------------------------
 struct ShrinkArgs {
     const uint16_t *X, *A;
     const float *scale, *weights;
     const int *ids;
     uint16_t *T;
-    int M, K, slots, rank, parts, count;
-};
-constexpr int kShrinkRows = 32;
-constexpr int kShrinkCols = 64;
-constexpr int kShrinkWaves = 8;
-
-__global__ __launch_bounds__(64 * kShrinkWaves) void lora_shrink_kernel(ShrinkArgs x) {
-    constexpr int kCB = kShrinkCols / 16, kMB = kShrinkRows / 16;
-    using List = AdapterList<kShrinkRows>;
-    __shared__ __attribute__((aligned(16))) char list_lds[List::kBytes];
-    __shared__ __attribute__((aligned(16))) f32x4 part[kShrinkWaves][kCB * kMB][64];
-    __shared__ int list_n;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-    const int r16 = lane & 15, g = lane >> 4;
-    const int m0 = blockIdx.x * kShrinkRows;
-    const int c0 = blockIdx.z * kShrinkCols;
-    const int cols = x.parts * x.rank;
-
-    List list;
-    if (wave == 0) {
-        list.build((SWIGLU_LDS char *)list_lds, x.ids, m0, x.M, x.slots, x.count);
-        if (lane == 0) list_n = list.n;
-    }
-    __syncthreads();
-    list.at((SWIGLU_LDS char *)list_lds);
-    list.n = list_n;
-
-    const int rows = min(kShrinkRows, x.M - m0);
-    const __amdgpu_buffer_rsrc_t xr = rows_rsrc(x.X, m0, rows, x.K);
-    const uint32_t voff = static_cast<uint32_t>(r16) * static_cast<uint32_t>(x.K) * 2u + g * 16u;
-    const uint32_t blk = 16u * static_cast<uint32_t>(x.K) * 2u;
-    const int units = (x.K + 63) / 64;
-    const int u_begin = wave * units / kShrinkWaves, u_end = (wave + 1) * units / kShrinkWaves;
-
-    for (int at = blockIdx.y; at < list.n; at += gridDim.y) {
-        const int a = __builtin_amdgcn_readfirstlane(static_cast<int>(list.list[at]));
-        const __amdgpu_buffer_rsrc_t ar =
-            rows_rsrc(x.A, static_cast<int64_t>(a) * cols + c0, min(kShrinkCols, cols - c0), x.K);
-        f32x4 acc[kCB][kMB];
-#pragma unroll
-        for (int c = 0; c < kCB; ++c)
-#pragma unroll
-            for (int m = 0; m < kMB; ++m) acc[c][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma nounroll
-        for (int u = u_begin; u < u_end; ++u) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k0 = u * 64 + h * 32;
-                const uint32_t v = k0 + g * 8 < x.K ? voff : kOutOfRange;
-                u32x4 af[kCB], xf[kMB];
-#pragma unroll
-                for (int m = 0; m < kMB; ++m) xf[m] = bload16(xr, v, m * blk + k0 * 2u);
-#pragma unroll
-                for (int c = 0; c < kCB; ++c) af[c] = bload16(ar, v, c * blk + k0 * 2u);
-#pragma unroll
-                for (int c = 0; c < kCB; ++c)
-#pragma unroll
-                    for (int m = 0; m < kMB; ++m) acc[c][m] = mfma_16x16x32(af[c], xf[m], acc[c][m]);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < kCB; ++c)
-#pragma unroll
-            for (int m = 0; m < kMB; ++m) part[wave][c * kMB + m][lane] = acc[c][m];
-        __syncthreads();
-        for (int q = wave; q < kCB * kMB; q += kShrinkWaves) {
-            f32x4 sum = part[0][q][lane];
-#pragma unroll
-            for (int w = 1; w < kShrinkWaves; ++w) sum += part[w][q][lane];
-            const int c = c0 + 16 * (q / kMB) + 4 * g;
-            const int row = 16 * (q % kMB) + r16;
-            const int slot = list.slot_of(row, a, x.slots);
-            if (slot >= 0 && c < cols) {
-                const int64_t at_row = static_cast<int64_t>(m0 + row) * x.slots;
-                // the weights of every slot that names a, the first one's T holding the sum
-                float w = 0.0f;
-                for (int j = slot; j < x.slots; ++j)
-                    if (list.ids[row * x.slots + j] == a) w += x.weights ? x.weights[at_row + j] : 1.0f;
-                w *= x.scale[a];
-                const u32x2 v = {pack_bf16x2(sum[0] * w, sum[1] * w), pack_bf16x2(sum[2] * w, sum[3] * w)};
-                *reinterpret_cast<u32x2 *>(x.T + (at_row + slot) * cols + c) = v;
-            }
-        }
-        __syncthreads();
-    }
-}
-
-hipError_t launch_lora_shrink(const uint16_t *X, const LoraTable &t, const int *ids,
-                              const float *weights, int slots, uint16_t *T, int M, int K,
-                              int parts, hipStream_t stream) {
-    const int64_t tiles = ceil_div(M, kShrinkRows);
-    const int64_t most = static_cast<int64_t>(kShrinkRows) * slots;
-    int64_t y = t.count < most ? t.count : most;
-    // about four workgroups a compute unit: with more rows, a workgroup takes
-    // several of its rows' adapters
-    const int64_t fill = ceil_div(1024, tiles);
-    if (y > fill) y = fill;
-    const ShrinkArgs a{X, t.A, t.scale, weights, ids, T, M, K, slots, t.rank, parts, t.count};
-    hipLaunchKernelGGL(lora_shrink_kernel,
-                       dim3((unsigned)tiles, (unsigned)y,
-                            (unsigned)ceil_div(static_cast<int64_t>(parts) * t.rank, kShrinkCols)),
-                       dim3(64 * kShrinkWaves), 0, stream, a);
-    return hipGetLastError();
-}
-
-// ---------------------------------------------------------------------------
-// Projections of at most 128 rows.  Bound by the weight's bytes: each
-// workgroup takes 16 RB rows of the weight (columns of D) and all rows of X
-// (16 MB of them), its four waves split K, and with few column tiles `splits`
-// workgroups split K further.  The weight is the MFMA's first operand, read
-// once from memory straight into registers (16 rows by 128 bytes at a time, no
-// LDS and no barrier in the loop); X, small enough to stay in L2, is the
-// second.  Gate and Up of an output are then neighbouring accumulator
-// registers of one lane (the packed weight's rows alternate), so the epilogue
-// needs no lane exchange.  The expansion goes on in the same accumulators: B's
-// rows as the weight's, T as X, with Gate rows masked out of the Up product
-// and the other way round.  The waves' sums meet in LDS, the workgroups' in
-// the workspace (device-scope stores and an arrival count, split_tail.hpp),
-// each in a fixed order.
-// ---------------------------------------------------------------------------
-struct StreamArgs {
-    const uint16_t *X, *W;
-    uint16_t *Y;
-    int M, K, cols;    // W [cols][K]
-    int splits;
+    char *plans;
+    int plan_bytes, capacity;
+    int M, K, slots, cols, count;   // cols = parts * rank
     float *partials;
     unsigned *counters;
-    LoraTerm lora;
+    int most_splits;
 };
-constexpr int kStreamWaves = 4;
 
-template <int MB, int RB, bool kGated>
-__global__ __launch_bounds__(64 * kStreamWaves, 2) void lora_stream_kernel(StreamArgs x) {
-    constexpr int kParts = kGated ? 2 : 1;
-    constexpr int kQuads = RB * MB;
-    constexpr int kRows = 16 * MB;
-    using List = AdapterList<kRows>;
-    constexpr int kSumBytes = kStreamWaves * kQuads * 64 * 16;
-    constexpr int kLds = kSumBytes > List::kBytes ? kSumBytes : List::kBytes;
-    __shared__ __attribute__((aligned(16))) char smem[kLds];
-    __shared__ int shared_word;
+// The plan of the workgroup's 64 rows (lora.hpp).
+__device__ __forceinline__ void write_plan(const ShrinkArgs &x, const SWIGLU_LDS AdapterList &l,
+                                           int n, char *plan) {
+    int *ids = reinterpret_cast<int *>(plan) + 4;
+    uint16_t *map = reinterpret_cast<uint16_t *>(ids + x.capacity);
+    if (threadIdx.x == 0) *reinterpret_cast<int *>(plan) = n;
+    if (n == 0) return;
+    for (int i = threadIdx.x; i < (n + 4) * 16; i += blockDim.x) {
+        const int e = i / 16, r = i % 16;
+        const int a = l.list[e < n ? e : 0];
+        uint32_t word = 0u;
+        if (e < n)
+            for (int j = x.slots - 1; j >= 0; --j)
+#pragma unroll
+                for (int t = 0; t < kPlanRows / 16; ++t)
+                    if (l.ids[j][16 * t + r] == a)
+                        word = (word & ~(15u << (4 * t))) | (static_cast<uint32_t>(j + 1) << (4 * t));
+        map[i] = static_cast<uint16_t>(word);
+        if (r == 0) ids[e] = a;
+    }
+}
+
+// Shrink.  blockIdx.x takes 64 rows of X and lists the adapters that they
+// name; the rows of A of those, one after the other, make the columns of
+// T^T = A . X^T in items of 64, shared out over gridDim.y workgroups, which
+// split K where there are fewer items than workgroups (their sums meet in the
+// workspace as in split_tail.hpp: device-scope stores and an arrival count, the
+// last to arrive adds them up in order, nobody waits).  Every row of X is
+// multiplied with every adapter listed: T takes the ones that it names.  Bound
+// by the bytes of X and A, and where those are few by the latency of a handful
+// of dependent memory accesses; the products that no row takes cost nothing
+// beside.  Both operands stream through LDS (the pipeline of gemm_core.hpp):
+// loaded straight into MFMA registers, 64 bytes of a row an instruction, the
+// same product streamed its operands at less than half the rate.
+using ShapeShrink = TileShape<64, 64, 64, 2, 2, 4, 2, 4, 16>;
+
+// Panel A of the pipeline: 64 of the listed adapters' rows, 8 of which, always
+// of one adapter, are one load of one wave.
+struct AdapterPanel {
+    using S = ShapeShrink;
+    static_assert(S::kChunksPerRow == 8, "a wave loads 8 rows");
+    __amdgpu_buffer_rsrc_t rsrc[S::kDmaA];
+    uint32_t voff;
+    int klim, lds_base;
+
+    __device__ __forceinline__ void init(const ShrinkArgs &x, const SWIGLU_LDS AdapterList &l,
+                                         int first, int total) {
+        const int lane = threadIdx.x & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+        const int c = (lane % 8) ^ swz<S>(wave * 8 + lane / 8);
+        voff = static_cast<uint32_t>(lane / 8) * static_cast<uint32_t>(x.K) * 2u + c * 16u;
+        klim = x.K - c * 8;
+        lds_base = wave * 1024;
+#pragma unroll
+        for (int j = 0; j < S::kDmaA; ++j) {
+            const int at = first + 32 * j + 8 * wave;
+            const bool in = at < total;
+            const int i = in ? at / x.cols : 0, row = in ? at - i * x.cols : 0;
+            const int id = __builtin_amdgcn_readfirstlane(static_cast<int>(l.list[i]));
+            rsrc[j] = make_rsrc(x.A + (static_cast<int64_t>(id) * x.cols + row) * x.K,
+                                in ? 8u * static_cast<uint32_t>(x.K) * 2u : 0u);
+        }
+    }
+    __device__ __forceinline__ void issue(int k0, SWIGLU_LDS char *dst, int only) const {
+        const uint32_t v = k0 < klim ? voff : kOutOfRange;
+#pragma unroll
+        for (int j = 0; j < S::kDmaA; ++j)
+            if (only < 0 || only == j)
+                dma16(rsrc[j], dst + lds_base + j * 4096, v, static_cast<uint32_t>(k0) * 2u);
+    }
+};
+
+__global__ __launch_bounds__(ShapeShrink::kThreads, 2) void lora_shrink_kernel(ShrinkArgs x) {
+    using S = ShapeShrink;
+    __shared__ __attribute__((aligned(16))) char smem[S::kLdsBytes];
+    __shared__ AdapterList list_;
+    __shared__ unsigned word;
     SWIGLU_LDS char *lds = (SWIGLU_LDS char *)smem;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-    const int r16 = lane & 15, g = lane >> 4;
-    const int tile = blockIdx.x / x.splits, split = blockIdx.x % x.splits;
-    const int n0 = tile * 16 * RB;
-    const int rows = min(16 * RB, x.cols - n0);
+    SWIGLU_LDS AdapterList &list = *(SWIGLU_LDS AdapterList *)&list_;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / S::WN, wn = wave % S::WN;
+    const int m0 = blockIdx.x * kPlanRows;
 
-    const __amdgpu_buffer_rsrc_t wr = rows_rsrc(x.W, n0, rows, x.K);
-    const __amdgpu_buffer_rsrc_t xr = rows_rsrc(x.X, 0, x.M, x.K);
-    const uint32_t voff = static_cast<uint32_t>(r16) * static_cast<uint32_t>(x.K) * 2u + g * 16u;
-    const uint32_t blk = 16u * static_cast<uint32_t>(x.K) * 2u;
-    // units of 64 k shared out over the waves of all splits
-    const int workers = x.splits * kStreamWaves, worker = split * kStreamWaves + wave;
-    const int units = (x.K + 63) / 64;
-    const int u_begin = static_cast<int>(static_cast<int64_t>(worker) * units / workers);
-    const int u_end = static_cast<int>(static_cast<int64_t>(worker + 1) * units / workers);
-
-    f32x4 acc[RB][MB];
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int m = 0; m < MB; ++m) acc[b][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma nounroll
-    for (int u = u_begin; u < u_end; ++u) {
-        u32x4 wf[2][RB], xf[2][MB];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k0 = u * 64 + h * 32;
-            const uint32_t v = k0 + g * 8 < x.K ? voff : kOutOfRange;
-#pragma unroll
-            for (int b = 0; b < RB; ++b) wf[h][b] = bload16(wr, v, b * blk + k0 * 2u);
-#pragma unroll
-            for (int m = 0; m < MB; ++m) xf[h][m] = bload16(xr, v, m * blk + k0 * 2u);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int b = 0; b < RB; ++b)
-#pragma unroll
-                for (int m = 0; m < MB; ++m)
-                    acc[b][m] = mfma_16x16x32(wf[h][b], xf[h][m], acc[b][m]);
-    }
-
-    // expansion
-    const LoraTerm &lt = x.lora;
-    List list;
-    if (wave == 0) {
-        list.build(lds, lt.ids, 0, lt.M, lt.slots, lt.count);
-        if (lane == 0) shared_word = list.n;
-    }
+    if (wave == 0) build_list(list, x.ids, x.weights, m0, x.M, x.slots, x.count);
     __syncthreads();
-    list.at(lds);
-    list.n = shared_word;
-    const int slot_bytes = kParts * lt.rank * 2;
-    const __amdgpu_buffer_rsrc_t tr =
-        make_rsrc(lt.T, static_cast<uint32_t>(lt.M * lt.slots * slot_bytes));
-    const int rank8 = lt.rank / 8;
-    const int steps = (list.n * rank8 + 3) / 4;
-    for (int s = worker; s < steps; s += workers) {
-        const ChunkOf ch = chunk_of(list, 4 * s + g, rank8);
-        u32x4 bf[RB];
-#pragma unroll
-        for (int b = 0; b < RB; ++b) {
-            // past the last column: any row, its results are not stored
-            const int n = min(n0 + 16 * b + r16, x.cols - 1);
-            bf[b] = gload16(lt.B + (static_cast<int64_t>(ch.adapter) * x.cols + n) * lt.rank +
-                            ch.element);
-        }
-        u32x4 tf[kParts][MB];
-#pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            const int row = 16 * m + r16;
-            const int slot = list.slot_of(row, ch.adapter, lt.slots);
-            const uint32_t off =
-                ch.live && slot >= 0
-                    ? static_cast<uint32_t>((row * lt.slots + slot) * slot_bytes + ch.element * 2)
-                    : kOutOfRange;
-#pragma unroll
-            for (int p = 0; p < kParts; ++p) tf[p][m] = bload16(tr, off, p * lt.rank * 2u);
-        }
-#pragma unroll
-        for (int p = 0; p < kParts; ++p)
-#pragma unroll
-            for (int b = 0; b < RB; ++b) {
-                u32x4 w = bf[b];
-                if constexpr (kGated)
-                    if ((lane & 1) != p) w = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int m = 0; m < MB; ++m) acc[b][m] = mfma_16x16x32(w, tf[p][m], acc[b][m]);
-            }
-    }
-    __syncthreads();   // the list is read; its LDS takes the sums
+    const int n = __builtin_amdgcn_readfirstlane(list.n);
+    if (blockIdx.y == 0)
+        write_plan(x, list, n, x.plans + static_cast<int64_t>(blockIdx.x) * x.plan_bytes);
+    const int total = n * x.cols;
+    const int items = (total + S::BM - 1) / S::BM;
+    if (items == 0) return;
+    const int G = gridDim.y;
+    const int splits = max(1, min(G / items, x.most_splits));
+    const int nk = (x.K + S::BK - 1) / S::BK;
 
-    SWIGLU_LDS f32x4 *sums = reinterpret_cast<SWIGLU_LDS f32x4 *>(lds);
+    PanelLoader<S, S::BN, S::kDmaB> xp;
+    xp.init(KMajor{x.X, x.M, 1, 0, 0, 0}, m0, x.K);
+    for (int job = blockIdx.y; job < items * splits; job += G) {
+        const int item = job / splits, split = job % splits;
+        const int kb = split * nk / splits, len = (split + 1) * nk / splits - kb;
+        AdapterPanel ap;
+        ap.init(x, list, item * S::BM, total);
+        Pipeline<S> pl;
+        pl.init(lds);
+        // steps past the range load nothing (K step nk is past the end of K)
+        auto issue = [&](int s, int part, SWIGLU_LDS char *dst, int j) {
+            const int k0 = (s < len ? kb + s : nk) * S::BK;
+            if (part == 0) ap.issue(k0, dst, j);
+            else xp.issue<false>(k0, dst, j);
+        };
+        S::Acc acc[S::TM][S::TN];
+        pl.prologue(issue);
+        pl.run_init0(issue, len, len, acc);
+        pl.drain(acc);
+
+        // quad q of a lane: rows c .. c + 3 of the item's, and one row of X
+        f32x4 sum[4];
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int m = 0; m < MB; ++m) sums[(wave * kQuads + b * MB + m) * 64 + lane] = acc[b][m];
-    __syncthreads();
-    constexpr int kMine = (kQuads + kStreamWaves - 1) / kStreamWaves;
-    f32x4 d[kMine];
+            for (int i = 0; i < 4; ++i) sum[q][i] = read_acc(acc[0][0].v[q][i]);
+        if (splits > 1) {
+            constexpr uint32_t kSlot = 4 * S::kThreads * 16;
+            const __amdgpu_buffer_rsrc_t pr = make_rsrc(
+                x.partials + static_cast<int64_t>(blockIdx.x * G + item * splits) * (kSlot / 4),
+                splits * kSlot);
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-        const int q = i * kStreamWaves + wave;
-        if (q < kQuads) {
-            d[i] = sums[q * 64 + lane];
-#pragma unroll
-            for (int w = 1; w < kStreamWaves; ++w) d[i] += sums[(w * kQuads + q) * 64 + lane];
-        }
-    }
-    if (x.splits > 1) {
-        // partial sums of quad q of split j of this tile at [(tile, j, q)][lane]
-        constexpr uint32_t kSlot = kQuads * 64 * 16;
-        float *slots = x.partials + static_cast<int64_t>(tile) * x.splits * (kSlot / 4);
-        const __amdgpu_buffer_rsrc_t pr = make_rsrc(slots, x.splits * kSlot);
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int q = i * kStreamWaves + wave;
-            if (q < kQuads)
+            for (int q = 0; q < 4; ++q)
                 __builtin_amdgcn_raw_buffer_store_b128(
-                    __builtin_bit_cast(u32x4, d[i]), pr,
-                    static_cast<int>(split * kSlot + (q * 64 + lane) * 16), 0, kDeviceScope);
-        }
-        wait_vmcnt<0>();
-        __syncthreads();
-        if (threadIdx.x == 0)
-            shared_word = static_cast<int>(__hip_atomic_fetch_add(
-                x.counters + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-        __syncthreads();
-        if (shared_word + 1 != x.splits) return;
-        if (threadIdx.x == 0)
-            __hip_atomic_store(x.counters + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    __builtin_bit_cast(u32x4, sum[q]), pr,
+                    static_cast<int>(split * kSlot + (q * S::kThreads + tid) * 16), 0, kDeviceScope);
+            wait_vmcnt<0>();   // this wave's sums are visible device-wide
+            __syncthreads();   // ... and every wave's
+            unsigned *counter = x.counters + blockIdx.x * (G / 2) + item;
+            if (tid == 0)
+                word = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED,
+                                              __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            // (a workgroup has one job where K is split)
+            if (word + 1 != static_cast<unsigned>(splits)) return;
+            if (tid == 0)
+                __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-            const int q = i * kStreamWaves + wave;
-            if (q < kQuads) {
-                f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-                for (int j = 0; j < x.splits; ++j)
-                    sum += __builtin_bit_cast(
+            for (int q = 0; q < 4; ++q) sum[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+            for (int p = 0; p < splits; ++p)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    sum[q] += __builtin_bit_cast(
                         f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                   pr, static_cast<int>(j * kSlot + (q * 64 + lane) * 16), 0,
+                                   pr, static_cast<int>(p * kSlot + (q * S::kThreads + tid) * 16), 0,
                                    kDeviceScope));
-                d[i] = sum;
-            }
         }
-    }
-    // lane (r16, g) of quad (b, m) holds columns n0 + 16 b + 4 g + 0..3 of row 16 m + r16
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-        const int q = i * kStreamWaves + wave;
-        const int row = 16 * (q % MB) + r16, col = n0 + 16 * (q / MB) + 4 * g;
-        if (q < kQuads && row < x.M && col < x.cols) {
-            if constexpr (kGated) {
-                const uint32_t v = pack_bf16x2(silu(d[i][0]) * d[i][1], silu(d[i][2]) * d[i][3]);
-                *reinterpret_cast<uint32_t *>(x.Y + static_cast<int64_t>(row) * (x.cols / 2) +
-                                              col / 2) = v;
-            } else {
-                const u32x2 v = {pack_bf16x2(d[i][0], d[i][1]), pack_bf16x2(d[i][2], d[i][3])};
-                *reinterpret_cast<u32x2 *>(x.Y + static_cast<int64_t>(row) * x.cols + col) = v;
-            }
+        for (int q = 0; q < 4; ++q) {
+            const int at = item * S::BM + 32 * wm + 16 * (q / 2) + 4 * (lane >> 4);
+            const int row = 32 * wn + 16 * (q % 2) + (lane & 15);
+            if (at >= total) continue;
+            const int i = at / x.cols, c = at - i * x.cols;
+            const int id = list.list[i];
+            // the weights of every slot that names id, the first one's T holding the sum
+            int slot = -1;
+            float w = 0.0f;
+            for (int j = x.slots - 1; j >= 0; --j)
+                if (list.ids[j][row] == id) {
+                    slot = j;
+                    w += list.weights[j][row];
+                }
+            if (slot >= 0)
+                store_t(x.T + (static_cast<int64_t>(m0 + row) * x.slots + slot) * (2 * x.cols), c,
+                        sum[q] * (w * x.scale[id]));
         }
+        __syncthreads();   // the ring and `word` are free
     }
 }
 
-template <int MB, int RB, bool kGated>
-static hipError_t run_stream(StreamArgs a, int tiles, hipStream_t stream) {
-    hipLaunchKernelGGL((lora_stream_kernel<MB, RB, kGated>), dim3(tiles * a.splits),
-                       dim3(64 * kStreamWaves), 0, stream, a);
+int lora_capacity(int count, int slots) {
+    const int named = kPlanRows * slots;
+    return ((count < named ? count : named) + 7) / 4 * 4;
+}
+// The plans' bytes of one 64 rows, with room for the four entries past the end.
+int lora_plan_bytes(int capacity) { return 16 + capacity * (4 + 2 * 16); }
+
+hipError_t launch_lora_shrink(const uint16_t *X, const LoraTable &t, const int *ids,
+                              const float *weights, int slots, uint16_t *T, char *plans, int M,
+                              int K, int parts, const GemmWorkspace &ws, hipStream_t stream) {
+    using S = ShapeShrink;
+    const int cols = parts * t.rank;
+    const int64_t tiles = ceil_div(M, kPlanRows);
+    const int64_t named = static_cast<int64_t>(kPlanRows) * slots;
+    const int64_t items = ceil_div((t.count < named ? t.count : named) * cols, S::BM);
+    // a split keeps at least four K steps
+    int64_t most = ceil_div(K, S::BK) / 4;
+    if (most < 1) most = 1;
+    // workgroups a row block: two a compute unit in all, and no more than there
+    // can be work for
+    int64_t G = 2 * ws.cus / tiles;
+    if (G > items * most) G = items * most;
+    if (G < 1) G = 1;
+    if (ws.base == nullptr || ws.counters == nullptr ||
+        static_cast<uint64_t>(tiles) * G * (S::BM * S::BN * 4) > ws.bytes ||
+        tiles * G > 2 * ws.max_counters)
+        most = 1;
+    const int capacity = lora_capacity(t.count, slots);
+    const ShrinkArgs a{X, t.A, t.scale, weights, ids, T, plans, lora_plan_bytes(capacity), capacity,
+                       M, K, slots, cols, t.count, static_cast<float *>(ws.base), ws.counters,
+                       static_cast<int>(most)};
+    hipLaunchKernelGGL(lora_shrink_kernel, dim3((unsigned)tiles, (unsigned)G), dim3(S::kThreads), 0,
+                       stream, a);
     return hipGetLastError();
-}
-
-// Weight rows of a workgroup (16 RB) and its splits along K.  The more rows,
-// the fewer times X is read; the fewer, the more workgroups there are to keep
-// loads in flight: at least two a compute unit, else K is split (a worker
-// keeps at least two 64-k units).
-struct StreamPlan {
-    int rb, tiles, splits;
-};
-static StreamPlan stream_plan(int M, int cols, int K, const GemmWorkspace &ws) {
-    const int want = 2 * ws.cus;
-    StreamPlan p{};
-    p.rb = M <= 64 ? 4 : 2;   // (at most 16 accumulator quads a lane: 64 KiB of sums in LDS)
-    while (p.rb > 1 && ceil_div(cols, 16 * p.rb) < want) p.rb /= 2;
-    p.tiles = static_cast<int>(ceil_div(cols, 16 * p.rb));
-    p.splits = 1;
-    if (p.tiles < want && ws.base != nullptr && ws.counters != nullptr &&
-        p.tiles <= ws.max_counters) {
-        int s = want / p.tiles;
-        const int most = static_cast<int>(ceil_div(K, 64) / (2 * kStreamWaves));
-        if (s > most) s = most;
-        const int mb = M <= 16 ? 1 : M <= 32 ? 2 : M <= 64 ? 4 : 8;
-        const uint64_t slot = static_cast<uint64_t>(p.rb) * mb * 1024;
-        if (s > 1 && static_cast<uint64_t>(p.tiles) * s * slot <= ws.bytes) p.splits = s;
-    }
-    return p;
-}
-
-template <int MB, bool kGated>
-static hipError_t stream_rb(const StreamArgs &a, const StreamPlan &p, hipStream_t stream) {
-    if constexpr (MB <= 4)
-        if (p.rb == 4) return run_stream<MB, 4, kGated>(a, p.tiles, stream);
-    if (p.rb == 2) return run_stream<MB, 2, kGated>(a, p.tiles, stream);
-    return run_stream<MB, 1, kGated>(a, p.tiles, stream);
-}
-
-template <bool kGated>
-static hipError_t launch_stream(const uint16_t *X, const uint16_t *W, uint16_t *Y, int M, int cols,
-                                int K, const LoraTerm &lora, const GemmWorkspace &ws,
-                                hipStream_t stream) {
-    const StreamPlan p = stream_plan(M, cols, K, ws);
-    const StreamArgs a{X, W, Y, M, K, cols, p.splits, static_cast<float *>(ws.base), ws.counters, lora};
-    if (M <= 16) return stream_rb<1, kGated>(a, p, stream);
-    if (M <= 32) return stream_rb<2, kGated>(a, p, stream);
-    if (M <= 64) return stream_rb<4, kGated>(a, p, stream);
-    return stream_rb<8, kGated>(a, p, stream);
-}
-
-hipError_t launch_lora_stream(const uint16_t *X, const uint16_t *W, uint16_t *Y, int M, int cols,
-                              int K, bool gated, const LoraTable &t, const int *ids, int slots,
-                              const uint16_t *T, const GemmWorkspace &ws, hipStream_t stream) {
-    const LoraTerm lora{T, t.B, ids, M, slots, t.rank, t.count, cols};
-    return gated ? launch_stream<true>(X, W, Y, M, cols, K, lora, ws, stream)
-                 : launch_stream<false>(X, W, Y, M, cols, K, lora, ws, stream);
 }
 
 }  // namespace swiglu

@@ -369,8 +369,9 @@ int swiglu_route_backward(const void *logits, int logits_type, const uint8_t *va
  *                          swiglu_gated_mlp, one table for each, the same ids
  *                          and weights for both (e.g. swiglu_route's)
  *
- * X . A^T times weight and scale is rounded to bf16 before the product with B;
- * all sums are fp32, Y, H and Out are rounded once.  Results are bitwise
+ * X . A^T times weight and scale is held as two bf16 numbers (16 bits of its
+ * value) for the product with B; all sums are fp32, Y, H and Out are rounded
+ * once.  Results are bitwise
  * reproducible for the same arguments and workspace size.  A row's result does
  * not depend on other rows' ids, except that infinities and NaN in the B of
  * one row's adapter may reach the rows computed with it as NaN.
@@ -378,8 +379,9 @@ int swiglu_route_backward(const void *logits, int logits_type, const uint8_t *va
  * multiple of 8 in [8, 256]; 1 <= count <= 8192; matrices 16-byte, ids,
  * weights and scale 4-byte aligned; outputs and workspace overlap nothing.
  * workspace: required, 256-byte aligned, no initialisation: at least
- * M * slots * (2 * rank) * 2 bytes (gated; rank for the down projection)
- * rounded up to 256, and with swiglu_lora_workspace_size() bytes the calls may
+ * M * slots * (2 * rank) * 4 bytes (gated; rank for the down projection),
+ * rounded up to 256, and as much again of ceil(M / 64) * (16 + 36 c) bytes, c
+ * being min(count, 64 slots) + 7 rounded down to a multiple of 4; and with swiglu_lora_workspace_size() bytes the calls may
  * also split tiles along K, as without adapters.
  */
 int swiglu_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t slots, int64_t rank,
