@@ -264,8 +264,8 @@ uint64_t lora_t_bytes(int64_t M, int64_t slots, int64_t width) {
     return (static_cast<uint64_t>(M) * slots * width * 4 + 255) & ~uint64_t{255};
 }
 uint64_t lora_state_bytes(int64_t M, int64_t slots, int64_t width, int64_t count) {
-    const uint64_t plans = static_cast<uint64_t>((M + 63) / 64) *
-                           swiglu::lora_plan_bytes(swiglu::lora_capacity((int)count, (int)slots));
+    const uint64_t plans =
+        static_cast<uint64_t>((M + 255) / 256) * swiglu::lora_plan_bytes((int)count, (int)slots);
     return lora_t_bytes(M, slots, width) + ((plans + 255) & ~uint64_t{255});
 }
 int check_lora_workspace(const void *workspace, uint64_t bytes, uint64_t need) {

@@ -606,8 +606,13 @@ hipError_t launch_down_proj(const uint16_t *H, const uint16_t *W3t, uint16_t *Ou
 // stores its partial).  The kernels without tail work are those with a tail,
 // given none.
 template <class S, class Epi, class Base>
-static hipError_t launch_lora_gemm(const KMajor &A, KMajor B, int M, int cols, int K,
-                                   const Epi &epi, const GemmWorkspace &ws, hipStream_t stream) {
+static hipError_t launch_lora_gemm(const KMajor &A, KMajor B, int M, int cols, int K, Epi epi,
+                                   const GemmWorkspace &ws, hipStream_t stream) {
+    constexpr bool kGated = std::is_same<Epi, PairMulLora>::value;
+    epi.lora.whole = LoraExpand<S, kGated, false>::chunks(epi.lora.slots, epi.lora.rank);
+    if constexpr (kQuarterable<S>)
+        epi.lora.quarter = LoraExpand<typename QuarterOf<S>::type, kGated, true>::chunks(
+            epi.lora.slots, epi.lora.rank);
     Schedule sch = make_schedule<S>(M, cols, K, ws);
     sch.grid = launch_grid<S>(sch, ws.cus);
     B.pairs = Epi::template paired<S>() ? 1 : 0;   // de-interleaved weight panels
@@ -623,12 +628,16 @@ static hipError_t launch_lora_gemm(const KMajor &A, KMajor B, int M, int cols, i
 }
 
 template <class Epi, class Base>
-static hipError_t launch_lora(const KMajor &A, const KMajor &B, int M, int cols, int K,
-                              const Epi &epi, const GemmWorkspace &ws, hipStream_t stream) {
+static hipError_t launch_lora(const KMajor &A, const KMajor &B, int M, int cols, int K, Epi epi,
+                              const GemmWorkspace &ws, hipStream_t stream) {
     if (M <= 128) {
         if constexpr (std::is_same<Epi, PairMulLora>::value) {
             const Schedule fx = make_fixup_schedule<ShapeSplitK>(M, cols, K, ws);
-            if (fx.pieces) return launch_reduce_in_kernel<ShapeSplitK>(A, B, M, K, epi, fx, stream);
+            if (fx.pieces) {
+                epi.lora.whole =
+                    LoraExpand<ShapeSplitK, true, false>::chunks(epi.lora.slots, epi.lora.rank);
+                return launch_reduce_in_kernel<ShapeSplitK>(A, B, M, K, epi, fx, stream);
+            }
             if (small_m_quad_tiles(M, cols, ws))
                 return launch_lora_gemm<ShapeQuad, Epi, Base>(A, B, M, cols, K, epi, ws, stream);
         }
@@ -644,8 +653,7 @@ hipError_t launch_lora_project(const uint16_t *X, const uint16_t *W, uint16_t *Y
                                const char *plans, const GemmWorkspace &ws, hipStream_t stream) {
     const KMajor A{X, M, 1, 0, 0, 0};
     const KMajor B{W, cols, 1, 0, 0, 0};
-    const int capacity = lora_capacity(t.count, slots);
-    const LoraTerm lora{T, t.B, plans, lora_plan_bytes(capacity), capacity, M, slots, t.rank, cols};
+    const LoraTerm lora{T, t.B, plans, lora_plan_bytes(t.count, slots), M, slots, t.rank, cols, {}, {}};
     if (gated)
         return launch_lora<PairMulLora, PairMulEpilogue>(
             A, B, M, cols, K, PairMulLora{{Y, M, cols / 2, cols / 2, 1.0f}, lora}, ws, stream);

@@ -88,11 +88,10 @@ struct LoraTable {
     const float *scale;      // [count]
     int count, rank;
 };
-// Entries of a plan of 64 rows and its bytes (lora.hpp).
-int lora_capacity(int count, int slots);
-int lora_plan_bytes(int capacity);
+// Bytes of a plan of 256 rows (lora.hpp).
+int lora_plan_bytes(int count, int slots);
 // T [M][slots][parts * rank] = weight scale X . A^T of each row's adapters, 4 bytes an
-// element, and the plans of each 64 rows (lora.hpp).  ws: scratch to split K (may be empty).
+// element, and the plans of each 256 rows (lora.hpp).  ws: scratch to split K (may be empty).
 hipError_t launch_lora_shrink(const uint16_t *X, const LoraTable &t, const int *ids,
                               const float *weights, int slots, uint16_t *T, char *plans, int M,
                               int K, int parts, const GemmWorkspace &ws, hipStream_t stream);

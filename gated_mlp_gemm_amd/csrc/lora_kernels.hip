@@ -9,6 +9,8 @@ namespace swiglu {
 
 static inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+constexpr int kShrinkRows = 64;
+
 // The adapters that 64 rows from row m0 on name: their slots' ids (-1: none)
 // and weights, and the list of the different adapters, ascending.  Built by one
 // wave: a bit per adapter, set by the slots, then read back 64 adapters at a
@@ -16,9 +18,9 @@ static inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // one pass).
 struct AdapterList {
     uint32_t bits[kMaxLoraCount / 32];
-    int ids[kMaxLoraSlots][kPlanRows];
-    float weights[kMaxLoraSlots][kPlanRows];
-    uint16_t list[kPlanRows * kMaxLoraSlots];
+    int ids[kMaxLoraSlots][kShrinkRows];
+    float weights[kMaxLoraSlots][kShrinkRows];
+    uint16_t list[kShrinkRows * kMaxLoraSlots];
     int n;
 };
 __device__ __forceinline__ void build_list(SWIGLU_LDS AdapterList &l, const int *row_ids,
@@ -67,38 +69,78 @@ struct ShrinkArgs {
     const int *ids;
     uint16_t *T;
     char *plans;
-    int plan_bytes, capacity;
+    int plan_bytes, plan_wgs;   // the last workgroups of the grid write the plans
     int M, K, slots, cols, count;   // cols = parts * rank
     float *partials;
     unsigned *counters;
-    int most_splits;
+    int most_splits, per_rows;   // workgroups a row block
 };
 
-// The plan of the workgroup's 64 rows (lora.hpp).
-__device__ __forceinline__ void write_plan(const ShrinkArgs &x, const SWIGLU_LDS AdapterList &l,
-                                           int n, char *plan) {
-    int *ids = reinterpret_cast<int *>(plan) + 4;
-    uint16_t *map = reinterpret_cast<uint16_t *>(ids + x.capacity);
-    if (threadIdx.x == 0) *reinterpret_cast<int *>(plan) = n;
-    if (n == 0) return;
-    for (int i = threadIdx.x; i < (n + 4) * 16; i += blockDim.x) {
-        const int e = i / 16, r = i % 16;
-        const int a = l.list[e < n ? e : 0];
-        uint32_t word = 0u;
-        if (e < n)
-            for (int j = x.slots - 1; j >= 0; --j)
+// The plan of 256 rows (lora.hpp), a row a thread: a bit per adapter, set by
+// the slots; an adapter's list index is the number of bits below its own.
+struct PlanLists {
+    uint32_t bits[kMaxLoraCount / 32];
+    uint16_t before[kMaxLoraCount / 32];   // bits of the words below
+    uint16_t wave_bits[4];
+};
+static_assert(kMaxLoraCount / 32 == kPlanRows, "a word of bits and a row a thread");
+__device__ __forceinline__ void write_plan(const ShrinkArgs &x, PlanLists &l, int block) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int64_t row = static_cast<int64_t>(block) * kPlanRows + tid;
+    int id[kMaxLoraSlots];
 #pragma unroll
-                for (int t = 0; t < kPlanRows / 16; ++t)
-                    if (l.ids[j][16 * t + r] == a)
-                        word = (word & ~(15u << (4 * t))) | (static_cast<uint32_t>(j + 1) << (4 * t));
-        map[i] = static_cast<uint16_t>(word);
-        if (r == 0) ids[e] = a;
+    for (int j = 0; j < kMaxLoraSlots; ++j) {
+        id[j] = j < x.slots && row < x.M ? x.ids[row * x.slots + j] : -1;
+        if (id[j] < 0 || id[j] >= x.count) id[j] = -1;
+    }
+    l.bits[tid] = 0u;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMaxLoraSlots; ++j)
+        if (id[j] >= 0) atomicOr(&l.bits[id[j] >> 5], 1u << (id[j] & 31));
+    __syncthreads();
+    uint32_t mine = l.bits[tid];
+    int upto = __popc(mine);   // over the lanes up to this one, then the waves
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int below = __shfl_up(upto, d);
+        if (lane >= d) upto += below;
+    }
+    if (lane == 63) l.wave_bits[wave] = static_cast<uint16_t>(upto);
+    __syncthreads();
+    int before = upto - __popc(mine), n = 0;
+    for (int w = 0; w < 4; ++w) {
+        if (w < wave) before += l.wave_bits[w];
+        n += l.wave_bits[w];
+    }
+    l.before[tid] = static_cast<uint16_t>(before);
+    __syncthreads();
+
+    char *plan = x.plans + static_cast<int64_t>(block) * x.plan_bytes;
+    if (tid == 0) *reinterpret_cast<int *>(plan) = n;
+    uint16_t *ids = reinterpret_cast<uint16_t *>(plan + kPlanIds);
+    for (; mine; mine &= mine - 1) ids[before++] = static_cast<uint16_t>(32 * tid + __ffs(mine) - 1);
+    uint32_t *where = reinterpret_cast<uint32_t *>(plan + kPlanWhere);
+#pragma unroll
+    for (int i = 0; i < kMaxLoraSlots / 2; ++i) {
+        uint32_t word = 0u;
+#pragma unroll
+        for (int j = 2 * i; j < 2 * i + 2; ++j) {
+            bool first = id[j] >= 0;
+#pragma unroll
+            for (int e = 0; e < j; ++e) first = first && id[e] != id[j];
+            if (first)
+                word |= static_cast<uint32_t>(1 + l.before[id[j] >> 5] +
+                                              __popc(l.bits[id[j] >> 5] & ((1u << (id[j] & 31)) - 1u)))
+                        << (16 * (j & 1));
+        }
+        where[i * kPlanRows + tid] = word;
     }
 }
 
-// Shrink.  blockIdx.x takes 64 rows of X and lists the adapters that they
+// Shrink.  A workgroup takes 64 rows of X and lists the adapters that they
 // name; the rows of A of those, one after the other, make the columns of
-// T^T = A . X^T in items of 64, shared out over gridDim.y workgroups, which
+// T^T = A . X^T in items of 64, shared out over per_rows workgroups, which
 // split K where there are fewer items than workgroups (their sums meet in the
 // workspace as in split_tail.hpp: device-scope stores and an arrival count, the
 // last to arrive adds them up in order, nobody waits).  Every row of X is
@@ -108,7 +150,9 @@ __device__ __forceinline__ void write_plan(const ShrinkArgs &x, const SWIGLU_LDS
 // beside.  Both operands stream through LDS (the pipeline of gemm_core.hpp):
 // loaded straight into MFMA registers, 64 bytes of a row an instruction, the
 // same product streamed its operands at less than half the rate.
-using ShapeShrink = TileShape<64, 64, 64, 2, 2, 4, 2, 4, 16>;
+// Eight stages, one workgroup a compute unit: a split of up to eight K steps
+// has all its loads in flight at once.
+using ShapeShrink = TileShape<64, 64, 64, 2, 2, 8, 2, 8, 16>;
 
 // Panel A of the pipeline: 64 of the listed adapters' rows, 8 of which, always
 // of one adapter, are one load of one wave.
@@ -146,7 +190,7 @@ struct AdapterPanel {
     }
 };
 
-__global__ __launch_bounds__(ShapeShrink::kThreads, 2) void lora_shrink_kernel(ShrinkArgs x) {
+__global__ __launch_bounds__(ShapeShrink::kThreads, 1) void lora_shrink_kernel(ShrinkArgs x) {
     using S = ShapeShrink;
     __shared__ __attribute__((aligned(16))) char smem[S::kLdsBytes];
     __shared__ AdapterList list_;
@@ -156,23 +200,29 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 2) void lora_shrink_kernel(S
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / S::WN, wn = wave % S::WN;
-    const int m0 = blockIdx.x * kPlanRows;
+    // neighbouring row blocks, which often name the same adapters, on one XCD
+    const int G = x.per_rows;
+    const int workers = gridDim.x - x.plan_wgs;
+    if (static_cast<int>(blockIdx.x) >= workers) {
+        write_plan(x, *reinterpret_cast<PlanLists *>(smem), blockIdx.x - workers);
+        return;
+    }
+    const int at_ = xcd_order(blockIdx.x, workers);
+    const int rows_at = at_ / G, y = at_ % G;
+    const int m0 = rows_at * kShrinkRows;
 
     if (wave == 0) build_list(list, x.ids, x.weights, m0, x.M, x.slots, x.count);
     __syncthreads();
     const int n = __builtin_amdgcn_readfirstlane(list.n);
-    if (blockIdx.y == 0)
-        write_plan(x, list, n, x.plans + static_cast<int64_t>(blockIdx.x) * x.plan_bytes);
     const int total = n * x.cols;
     const int items = (total + S::BM - 1) / S::BM;
     if (items == 0) return;
-    const int G = gridDim.y;
     const int splits = max(1, min(G / items, x.most_splits));
     const int nk = (x.K + S::BK - 1) / S::BK;
 
     PanelLoader<S, S::BN, S::kDmaB> xp;
     xp.init(KMajor{x.X, x.M, 1, 0, 0, 0}, m0, x.K);
-    for (int job = blockIdx.y; job < items * splits; job += G) {
+    for (int job = y; job < items * splits; job += G) {
         const int item = job / splits, split = job % splits;
         const int kb = split * nk / splits, len = (split + 1) * nk / splits - kb;
         AdapterPanel ap;
@@ -199,7 +249,7 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 2) void lora_shrink_kernel(S
         if (splits > 1) {
             constexpr uint32_t kSlot = 4 * S::kThreads * 16;
             const __amdgpu_buffer_rsrc_t pr = make_rsrc(
-                x.partials + static_cast<int64_t>(blockIdx.x * G + item * splits) * (kSlot / 4),
+                x.partials + (static_cast<int64_t>(rows_at) * G + item * splits) * (kSlot / 4),
                 splits * kSlot);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -208,7 +258,7 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 2) void lora_shrink_kernel(S
                     static_cast<int>(split * kSlot + (q * S::kThreads + tid) * 16), 0, kDeviceScope);
             wait_vmcnt<0>();   // this wave's sums are visible device-wide
             __syncthreads();   // ... and every wave's
-            unsigned *counter = x.counters + blockIdx.x * (G / 2) + item;
+            unsigned *counter = x.counters + rows_at * (G / 2) + item;
             if (tid == 0)
                 word = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED,
                                               __HIP_MEMORY_SCOPE_AGENT);
@@ -219,7 +269,7 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 2) void lora_shrink_kernel(S
                 __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
             for (int q = 0; q < 4; ++q) sum[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
+#pragma unroll 8
             for (int p = 0; p < splits; ++p)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -251,39 +301,38 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 2) void lora_shrink_kernel(S
     }
 }
 
-int lora_capacity(int count, int slots) {
+int lora_plan_bytes(int count, int slots) {
     const int named = kPlanRows * slots;
-    return ((count < named ? count : named) + 7) / 4 * 4;
+    return kPlanIds + ((count < named ? count : named) + 7) / 8 * 16;
 }
-// The plans' bytes of one 64 rows, with room for the four entries past the end.
-int lora_plan_bytes(int capacity) { return 16 + capacity * (4 + 2 * 16); }
 
 hipError_t launch_lora_shrink(const uint16_t *X, const LoraTable &t, const int *ids,
                               const float *weights, int slots, uint16_t *T, char *plans, int M,
                               int K, int parts, const GemmWorkspace &ws, hipStream_t stream) {
     using S = ShapeShrink;
     const int cols = parts * t.rank;
-    const int64_t tiles = ceil_div(M, kPlanRows);
-    const int64_t named = static_cast<int64_t>(kPlanRows) * slots;
+    const int64_t tiles = ceil_div(M, kShrinkRows);
+    const int64_t named = static_cast<int64_t>(kShrinkRows) * slots;
     const int64_t items = ceil_div((t.count < named ? t.count : named) * cols, S::BM);
-    // a split keeps at least four K steps
-    int64_t most = ceil_div(K, S::BK) / 4;
+    // a split keeps at least six K steps, and the last to arrive has its reads
+    // of the others' sums in flight in two goes
+    int64_t most = ceil_div(K, S::BK) / 6;
+    if (most > 16) most = 16;
     if (most < 1) most = 1;
-    // workgroups a row block: two a compute unit in all, and no more than there
+    // workgroups a row block: one a compute unit in all, and no more than there
     // can be work for
-    int64_t G = 2 * ws.cus / tiles;
+    int64_t G = ws.cus / tiles;
     if (G > items * most) G = items * most;
     if (G < 1) G = 1;
     if (ws.base == nullptr || ws.counters == nullptr ||
         static_cast<uint64_t>(tiles) * G * (S::BM * S::BN * 4) > ws.bytes ||
         tiles * G > 2 * ws.max_counters)
         most = 1;
-    const int capacity = lora_capacity(t.count, slots);
-    const ShrinkArgs a{X, t.A, t.scale, weights, ids, T, plans, lora_plan_bytes(capacity), capacity,
-                       M, K, slots, cols, t.count, static_cast<float *>(ws.base), ws.counters,
-                       static_cast<int>(most)};
-    hipLaunchKernelGGL(lora_shrink_kernel, dim3((unsigned)tiles, (unsigned)G), dim3(S::kThreads), 0,
-                       stream, a);
+    const int64_t plan_wgs = ceil_div(M, kPlanRows);
+    const ShrinkArgs a{X, t.A, t.scale, weights, ids, T, plans, lora_plan_bytes(t.count, slots),
+                       static_cast<int>(plan_wgs), M, K, slots, cols, t.count, static_cast<float *>(ws.base), ws.counters,
+                       static_cast<int>(most), static_cast<int>(G)};
+    hipLaunchKernelGGL(lora_shrink_kernel, dim3((unsigned)(tiles * G + plan_wgs)), dim3(S::kThreads), 0, stream, a);
     return hipGetLastError();
 }
 

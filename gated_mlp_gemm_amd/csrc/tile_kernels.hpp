@@ -284,14 +284,14 @@ struct WithLora : Base {
 };
 using PairMulLora = WithLora<PairMulEpilogue>;
 using StoreLora = WithLora<StoreEpilogue>;
-template <class S, class Epi>
-__device__ __forceinline__ void expand_adapters(const Epi &epi,
+template <class S, bool kQuarter = false, class Epi>
+__device__ __forceinline__ void expand_adapters(SWIGLU_LDS char *lds, const Epi &epi,
                                                 typename S::Acc (&acc)[S::TM][S::TN], int m0,
                                                 int n0) {
     if constexpr (std::is_same<Epi, PairMulLora>::value)
-        lora_expand<S, true>(epi.lora, acc, m0, n0);
+        LoraExpand<S, true, kQuarter>::run(lds, epi.lora, acc, m0, n0);
     else if constexpr (std::is_same<Epi, StoreLora>::value)
-        lora_expand<S, false>(epi.lora, acc, m0, n0);
+        LoraExpand<S, false, kQuarter>::run(lds, epi.lora, acc, m0, n0);
 }
 
 // The K steps [0, len) of one tile into `acc`.  With 16x16 MFMAs the first
@@ -398,7 +398,7 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
                 run_tile<S, kEven>(pl, issue, nk, acc);
                 pl.drain(acc);
                 const int m0 = tm * S::BM, n0 = tn * S::BN;
-                expand_adapters<S>(epi, acc, m0, n0);
+                expand_adapters<S>(lds, epi, acc, m0, n0);
                 if (j + grid < sch.dp) {
                     tile_coords(xcd_order(j + grid, sch.dp), sch.tiles_m, sch.tiles_n, sch.group_m, tm,
                                 tn);
@@ -427,7 +427,7 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             if (m0 >= M || n0 >= B.rows) continue;   // quarter wholly past the output's edge
             typename Q::Acc acc[Q::TM][Q::TN];
             tile_mainloop<Q, kEven>(lds, Ak, B, M, K, m0, n0, 0, sch.nk, sch.nk, acc);
-            expand_adapters<Q>(epi, acc, m0, n0);
+            expand_adapters<Q, true>(lds, epi, acc, m0, n0);
             epi.template apply<Q>(acc, m0, n0, threadIdx.x);
         }
         whole_tiles();
@@ -450,7 +450,8 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             typename S::Acc acc[S::TM][S::TN];
             tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
             // (the adapters' terms once a tile)
-            if (piece == sch.pieces - 1) expand_adapters<S>(epi, acc, tm * S::BM, tn * S::BN);
+            if (piece == sch.pieces - 1)
+                expand_adapters<S>(lds, epi, acc, tm * S::BM, tn * S::BN);
             const float *slots = sch.partials + static_cast<int64_t>(i) * sch.pieces * S::BM * S::BN;
             store_partial_coherent<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN,
                                       acc, threadIdx.x);
@@ -494,7 +495,8 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             typename S::Acc acc[S::TM][S::TN];
             tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
             // (the adapters' terms once a tile)
-            if (piece == sch.pieces - 1) expand_adapters<S>(epi, acc, tm * S::BM, tn * S::BN);
+            if (piece == sch.pieces - 1)
+                expand_adapters<S>(lds, epi, acc, tm * S::BM, tn * S::BN);
             store_partial<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN, acc,
                              threadIdx.x);
         }

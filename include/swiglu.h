@@ -380,9 +380,10 @@ int swiglu_route_backward(const void *logits, int logits_type, const uint8_t *va
  * weights and scale 4-byte aligned; outputs and workspace overlap nothing.
  * workspace: required, 256-byte aligned, no initialisation: at least
  * M * slots * (2 * rank) * 4 bytes (gated; rank for the down projection),
- * rounded up to 256, and as much again of ceil(M / 64) * (16 + 36 c) bytes, c
- * being min(count, 64 slots) + 7 rounded down to a multiple of 4; and with swiglu_lora_workspace_size() bytes the calls may
- * also split tiles along K, as without adapters.
+ * rounded up to 256, and another ceil(M / 256) * (4112 + 2 c), c being
+ * min(count, 256 slots) rounded up to a multiple of 8, rounded up to 256; with
+ * swiglu_lora_workspace_size() bytes the calls may also split K, as without
+ * adapters.
  */
 int swiglu_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t slots, int64_t rank,
                                uint64_t *bytes);

@@ -273,7 +273,7 @@ def test_smallest_workspace(dev):
         x, w, t, ids, weights = case_of(kind, M, 1024, 264, 5, 16, 1, "mixed", True, 8)
         up = lambda n: (n + 255) // 256 * 256  # noqa: E731
         need = (up(M * 1 * (2 if kind == "gated" else 1) * 16 * 4) +
-                up((M + 63) // 64 * (16 + 36 * ((5 + 7) // 4 * 4))))
+                up((M + 255) // 256 * (4112 + 2 * 8)))
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
         y = run(kind, dev, x, w, t, ids, weights, workspace=ws)
         want, tol = (gated(x, w, t, ids, weights) if kind == "gated"
