@@ -55,10 +55,19 @@ struct LoraTerm {
     LoraChunks whole, quarter;   // of a tile of the kernel's shape, and of a quarter tile
 };
 
-// e / d for 0 <= e < 2^20 and 1 <= d <= 64 (the rounded quotient is exact).
-__device__ __forceinline__ int small_quotient(int e, int d) {
-    return static_cast<int>((static_cast<float>(e) + 0.5f) / static_cast<float>(d));
-}
+// Quotients by a small divisor that is the same for all lanes, by its
+// reciprocal: exact while the quotient is below 2^12 and the divisor at most 64
+// (e + 1/2 is at least 1/2 from the next multiple of d, 2^-7 of a quotient, and
+// the two roundings move it by less than 2^-10).
+struct Divisor {
+    int d;
+    float inverse;
+    __device__ __forceinline__ explicit Divisor(int by)
+        : d(by), inverse(1.0f / static_cast<float>(by)) {}
+    __device__ __forceinline__ int quotient(int e) const {
+        return static_cast<int>((static_cast<float>(e) + 0.5f) * inverse);
+    }
+};
 
 // Elements c .. c + 3 (c a multiple of 4) of a row of T.
 __device__ __forceinline__ void store_t(uint16_t *row, int c, const f32x4 &v) {
@@ -76,9 +85,9 @@ __device__ __forceinline__ void store_t(uint16_t *row, int c, const f32x4 &v) {
         u32x2{pack_bf16x2(rest[0], rest[1]), pack_bf16x2(rest[2], rest[3])};
 }
 
-// LDS reads that the compiler does not see (as asm_read_b128): it would wait
-// for every direct-to-LDS load in flight first.  wait_lgkmcnt0() and an empty
-// "+v" statement stand before the use.
+// LDS accesses that the compiler does not see (as asm_read_b128): it would
+// wait for every direct-to-LDS load in flight first.  wait_lgkmcnt0() and an
+// empty "+v" statement stand before the use of what is read.
 __device__ __forceinline__ uint32_t asm_read_b32(uint32_t addr) {
     uint32_t r;
     asm volatile("ds_read_b32 %0, %1" : "=v"(r) : "v"(addr));
@@ -88,6 +97,9 @@ __device__ __forceinline__ uint32_t asm_read_u16(uint32_t addr) {
     uint32_t r;
     asm volatile("ds_read_u16 %0, %1" : "=v"(r) : "v"(addr));
     return r;
+}
+__device__ __forceinline__ void asm_write_b128(uint32_t addr, const u32x4 &v) {
+    asm volatile("ds_write_b128 %0, %1" ::"v"(addr), "v"(v) : "memory");
 }
 __device__ __forceinline__ uint32_t landed(uint32_t v) {
     asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(v));
@@ -103,13 +115,17 @@ __device__ __forceinline__ void gdma16(const uint16_t *p, SWIGLU_LDS char *lds) 
 // accumulators are settled before and after, the tile's LDS is idle).
 //
 // K runs over the adapters of the tile's plan, rank8 chunks of 8 elements each,
-// 32 k a step.  LDS holds T of the tile's rows as it is in memory (only the
-// slots that there are; a lane whose row does not name the adapter of its 8 k
-// reads zeros from beside it) and a ring of B's rows of one step, both by
-// direct-to-LDS loads, so that every byte is read once a tile and by the
-// waves from LDS: loaded by each wave straight into its MFMA operands (T's
-// rows by 2 waves, B's by 2, in 16-byte pieces of many cache lines), the
-// expansion was bound by the L1 cache at about 2.5 times its MFMAs' time.
+// 32 k a step.  LDS holds T of the tile's rows (only the slots that there are;
+// a lane whose row does not name the adapter of its 8 k reads zeros from beside
+// it) and a ring of B's rows, kSteps steps a stage, loaded straight to LDS; so
+// every byte is read once a tile.  One wave a SIMD issues an instruction about
+// every 6 clocks, so what bounds this is the instructions around the MFMAs, not
+// bytes: the addresses and LDS reads of a group of row blocks stand between
+// the MFMAs of the group before it, those of the next step between the last
+// group's.  (In clocks, 256 x 256 tile, Gate and Up, 2 slots of rank 16: a step
+// 4500 and what comes before the first 5100 with addresses and MFMAs one after
+// the other and T copied to LDS by 16-byte chunks of any row length.)  The first
+// stages' adapters are looked up before the tile's K steps (begin).
 template <class S, bool kGated, bool kQuarter>
 struct LoraExpand {
     static_assert(S::MI == 16 && S::kWaves == 4, "16x16 MFMAs, 4 waves");
@@ -119,194 +135,329 @@ struct LoraExpand {
     // LDS: where [4][256] | ids | zeros | T ... | ring of B
     static constexpr int kIds = 4 * kPlanRows * 4;
     static constexpr int kZeros = kIds + kPlanRows * kMaxLoraSlots * 2;
-    static constexpr int kT = kZeros + 64;
-    static constexpr int kStageBytes = S::BN * 64;
-    static constexpr int kStages = S::BN <= 64 ? 8 : S::kLdsBytes > 65536 && S::BN <= 128 ? 4 : 2;
-    static constexpr int kRing = S::kLdsBytes - kStages * kStageBytes;
-    static constexpr int kDma = kStageBytes / 4096;   // loads a wave and stage
-    // 16-byte chunks of T a row: an odd count, so that 16 rows lie on 16
-    // different banks
+    static constexpr int kZeroBytes = 1024;
+    static constexpr int kT = kZeros + kZeroBytes;
+    // a stage of few columns takes four steps: its barrier and its latency are
+    // most of its time
+    static constexpr int kSteps = S::BN <= 64 ? 4 : 1;
+    static constexpr int kStages = S::BN <= 64 ? 3 : S::kLdsBytes > 65536 && S::BN <= 128 ? 4 : 2;
+    static constexpr int kStepBytes = S::BN * 64;
+    static constexpr int kRing = S::kLdsBytes - kStages * kSteps * kStepBytes;
+    static constexpr int kDma = kStepBytes / 4096;   // loads a wave and step
+    static constexpr int kEarly = (kStages - 1) * kSteps;
+    // 16-byte chunks of a row of T in LDS: an odd count, so that 16 rows lie on
+    // 16 different banks.  A slot's part takes kSegment-chunk groups.
     static constexpr int kRowChunks = (((kRing - kT) / (16 * S::BM)) - 1) | 1;
-    static_assert(kRowChunks * 16 * S::BM <= kRing - kT && kRowChunks >= 2 * kParts + 1, "T fits");
+    static constexpr int kSegment = 4;
+    static constexpr int kGroups = kRowChunks / kSegment < 10 ? kRowChunks / kSegment : 10;
+    static_assert(kRowChunks * 16 * S::BM <= kRing - kT && kGroups >= kParts, "T fits");
+    static_assert(kGroups * kSegment * 16 <= kZeroBytes, "zeros as long as a row");
 
+    // groups of 4 chunks (16 elements) of a slot's part
+    static constexpr int segments(int rank8) { return (rank8 + 1) / 2; }
     static LoraChunks chunks(int slots, int rank) {
-        const int rank8 = rank / 8, most = (kRowChunks - 1) / (2 * kParts);
-        if (slots > most) return {most, 1};
-        const int r = most / slots < rank8 ? most / slots : rank8;
+        const int rank8 = rank / 8, most = kGroups / kParts;   // groups there are
+        if (slots > most) return {most, rank8 < 2 ? rank8 : 2};
+        const int r = most / slots * 2 < rank8 ? most / slots * 2 : rank8;
         const int n = (rank8 + r - 1) / r;   // as even as they can be
         return {slots, (rank8 + n - 1) / n};
     }
 
-    __device__ __forceinline__ static int swizzle(int row) { return ((row >> 1) ^ (row >> 3)) & 3; }
+    int n;                 // adapters of the plan
+    uint32_t id[kEarly];   // the lane's adapter in each of the first steps
 
-    __device__ __forceinline__ static void run(SWIGLU_LDS char *lds, const LoraTerm &x,
-                                               typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0) {
-        const int lane = threadIdx.x & 63;
-        const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    __device__ __forceinline__ static int swizzle(int row) { return ((row >> 1) ^ (row >> 3)) & 3; }
+    // the lane's row of B and its 16 bytes of a step
+    __device__ __forceinline__ static int b_row(int tid) { return (tid >> 6) * 16 + (tid & 63) / 4; }
+    __device__ __forceinline__ static int b_chunk(int tid) { return (tid & 3) ^ swizzle((tid & 63) / 4); }
+    // The thread's number, of which the compiler does not know that it is the
+    // same for every tile: what follows from it is computed for each, not kept
+    // in registers over the K steps.
+    __device__ __forceinline__ static int thread() {
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        return tid;
+    }
+
+    __device__ __forceinline__ void begin(const LoraTerm &x, int m0) {
+        const int tid = thread();
+        const char *plan = x.plans + static_cast<int64_t>(m0 / kPlanRows) * x.plan_bytes;
+        // (uniform: a scalar load)
+        n = *reinterpret_cast<const __attribute__((address_space(4))) int *>(
+            reinterpret_cast<uintptr_t>(plan));
+        const Divisor rank8(kQuarter ? x.quarter.rank8 : x.whole.rank8);
+        const uint16_t *ids = reinterpret_cast<const uint16_t *>(plan + kPlanIds);
+#pragma unroll
+        for (int s = 0; s < kEarly; ++s)
+            id[s] = n > 0 ? ids[min(rank8.quotient(4 * s + b_chunk(tid)), n - 1)] : 0u;
+    }
+
+    // after MFMA i of 4 kRows S::TN: hook(i)
+    template <int kRows, class Hook>
+    __device__ __forceinline__ static void multiply(typename S::Acc (&acc)[S::TM][S::TN], int rb0,
+                                                    const u32x4 (&tf)[kRows][kParts][2],
+                                                    const u32x4 (&bf)[S::TN][2], const Hook &hook) {
+        asm volatile("s_nop 1");
+#pragma unroll
+        for (int rest = 0; rest < 2; ++rest)
+#pragma unroll
+            for (int t = 0; t < kRows; ++t)
+#pragma unroll
+                for (int c = 0; c < S::TN; ++c)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int rb = rb0 + t;
+                        mfma_16x16x32_acc(acc[rb / 2][c].v[2 * (rb % 2) + h],
+                                          tf[t][kGated ? c % 2 : 0][rest], bf[c][h]);
+                        hook(((rest * kRows + t) * S::TN + c) * 2 + h);
+                    }
+    }
+
+    __device__ __forceinline__ void run(SWIGLU_LDS char *lds, const LoraTerm &x,
+                                        typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0) const {
+        if (n == 0) return;
+        const int tid = thread(), lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / S::WN, wn = wave % S::WN;
         const int r16 = lane & 15, g = lane >> 4;
         const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
-        const char *plan = x.plans + static_cast<int64_t>(m0 / kPlanRows) * x.plan_bytes;
-        // (uniform: a scalar load)
-        const int n = *reinterpret_cast<const __attribute__((address_space(4))) int *>(
-            reinterpret_cast<uintptr_t>(plan));
-        if (n == 0) return;
         const LoraChunks by = kQuarter ? x.quarter : x.whole;
         const int rank8 = x.rank / 8;
-        const int slot_bytes = kParts * x.rank * 4;
-        const int rows = min(S::BM, x.M - m0);
-        const __amdgpu_buffer_rsrc_t pr = make_rsrc(plan, static_cast<uint32_t>(x.plan_bytes));
+        const int slot_bytes = kParts * x.rank * 4, row_bytes = x.slots * slot_bytes;
+        const __amdgpu_buffer_rsrc_t pr =
+            make_rsrc(x.plans + static_cast<int64_t>(m0 / kPlanRows) * x.plan_bytes,
+                      static_cast<uint32_t>(x.plan_bytes));
         const __amdgpu_buffer_rsrc_t tr =
-            make_rsrc(x.T + static_cast<int64_t>(m0) * x.slots * (2 * kParts * x.rank),
-                      static_cast<uint32_t>(rows * x.slots * slot_bytes));
+            make_rsrc(x.T + static_cast<int64_t>(m0) * (row_bytes / 2),
+                      static_cast<uint32_t>(min(S::BM, x.M - m0) * row_bytes));
         // where of the tile's rows: one of the four planes a wave; ids: 1 KiB a wave
         dma16(pr, lds + wave * 1024, static_cast<uint32_t>(kPlanWhere + (m0 % kPlanRows) * 4) + lane * 16u,
               wave * (kPlanRows * 4));
         dma16(pr, lds + kIds + wave * 1024, kPlanIds + lane * 16u, wave * 1024);
-        if (threadIdx.x < 16)
-            asm volatile("ds_write_b32 %0, %1" ::"v"(at + kZeros + threadIdx.x * 4u), "v"(0u) : "memory");
+        if (wave == 0) asm_write_b128(at + kZeros + lane * 16u, u32x4{0u, 0u, 0u, 0u});
 
-        // the lane's row and 16 bytes of a step of B
-        const int b_row = wave * 16 + lane / 4, b_chunk = (lane & 3) ^ swizzle(lane / 4);
+        uint32_t col[kDma];   // elements from an adapter's B to the lane's rows
+#pragma unroll
+        for (int j = 0; j < kDma; ++j) {
+            const int r = j * 64 + b_row(tid);
+            // past the last column any row does, its results are not stored
+            col[j] = static_cast<uint32_t>(min(n0 + (kGated ? pair_row(r) : r), x.cols - 1)) * x.rank;
+        }
+        const int64_t b_adapter = static_cast<int64_t>(x.cols) * x.rank;
+        const Divisor by_rank8(by.rank8);
+        const int parts_chunks = segments(by.rank8) * kSegment;   // of a slot's part, in LDS
+        const int groups = by.slots * kParts * segments(by.rank8);
+        const int steps = (n * by.rank8 + 3) / 4;
+
         const int row0 = wm * S::kWaveM + r16;   // the lane's row of T in row block 0
         constexpr int kRowBlocks = S::kWaveM / 16;
         // row blocks whose T is in registers at once, one such group ahead
-        constexpr int kRows = kRowBlocks > 4 ? 4 / kParts : kRowBlocks;
-        constexpr int kGroups = kRowBlocks / kRows;
+        constexpr int kRows = kRowBlocks > 2 ? 2 / kParts : kRowBlocks;
+        constexpr int kRowGroups = kRowBlocks / kRows;
+        constexpr uint32_t kBelow = 16u * kRowChunks * 16u;   // from one row block to the next
+        const uint32_t t_row = at + kT + static_cast<uint32_t>(row0 * kRowChunks) * 16u;
+        const uint32_t t_part = static_cast<uint32_t>(parts_chunks) * 16u;
         const uint32_t b_read = at + kRing + (wn * S::kWaveN + r16) * 64u + ((g ^ swizzle(r16)) * 16u);
 
 #pragma nounroll
         for (int j0 = 0; j0 < x.slots; j0 += by.slots)
 #pragma nounroll
             for (int r0 = 0; r0 < rank8; r0 += by.rank8) {
-                const int per_slot = by.rank8 * 2;   // 16-byte chunks of a slot's part
-                const int row_chunks = by.slots * kParts * per_slot + 1;
-                const int steps = (n * by.rank8 + 3) / 4;
-                // T: chunk i of the rows' chunks, in memory's order
-                const int total = S::BM * row_chunks;
+                // T: a wave a quarter of the rows, 16 rows by 4 chunks a load; group i is
+                // 4 chunks of one slot's part
+                {
+                    constexpr int kLoads = S::BM / 64, kBatch = S::BM == 256 || S::kOccupancy > 1 ? 2 : 4;
+                    const int row = wave * (S::BM / 4) + lane / 4;
+                    const uint32_t from = static_cast<uint32_t>(row * row_bytes) + (lane & 3) * 16u;
+                    const uint32_t to = at + kT + static_cast<uint32_t>(row * kRowChunks) * 16u + (lane & 3) * 16u;
+                    int sp = 0, seg = 0;
 #pragma nounroll
-                for (int i0 = wave * 64; i0 < total; i0 += 256) {
-                    const int i = i0 + lane;
-                    const int row = small_quotient(i, row_chunks), c = i - row * row_chunks;
-                    const int sp = small_quotient(c, per_slot), k = c - sp * per_slot;
-                    const int j = j0 + sp / kParts, part = sp % kParts;
-                    const bool in = j < x.slots && sp < by.slots * kParts && r0 + k / 2 < rank8;
-                    dma16(tr, lds + kT + i0 * 16,
-                          in ? static_cast<uint32_t>((row * x.slots + j) * slot_bytes +
-                                                     part * x.rank * 4 + r0 * 32 + k * 16)
-                             : kOutOfRange,
-                          0);
-                }
-                if (j0 + r0 == 0) {
-                    wait_vmcnt<0>();
-                    wait_lgkmcnt0();
-                    block_barrier();   // the plan has landed
-                }
-                auto issue_b = [&](int s) {
-                    const int e = 4 * s + b_chunk;
-                    const int i = small_quotient(e, by.rank8);
-                    // past the end: something there is, multiplied with zeros
-                    const int element = 8 * min(r0 + e - i * by.rank8, rank8 - 1);
-                    const uint32_t id = landed(asm_read_u16(at + kIds + min(i, n - 1) * 2));
-                    const uint16_t *p =
-                        x.B + static_cast<int64_t>(id) * x.cols * x.rank + element;
+                    for (int first = 0; first < groups; first += kBatch) {
+                        u32x4 v[kBatch][kLoads];
 #pragma unroll
-                    for (int j = 0; j < kDma; ++j) {
-                        const int r = j * 64 + b_row;
-                        const int col = min(n0 + (kGated ? pair_row(r) : r), x.cols - 1);
-                        gdma16(p + col * x.rank,
-                               lds + kRing + (s % kStages) * kStageBytes + (j * 4 + wave) * 1024);
+                        for (int i = 0; i < kBatch; ++i)
+                            if (first + i < groups) {
+                                // (past the last slot: past the row, or zeros; never read)
+                                const uint32_t soff = static_cast<uint32_t>(
+                                    (j0 * kParts + sp) * x.rank * 4 + r0 * 32 + seg * (kSegment * 16));
+#pragma unroll
+                                for (int t = 0; t < kLoads; ++t)
+                                    v[i][t] = __builtin_bit_cast(
+                                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   tr, static_cast<int>(from),
+                                                   static_cast<int>(soff + t * 16u * row_bytes), 0));
+                                if (++seg == segments(by.rank8)) {
+                                    seg = 0;
+                                    ++sp;
+                                }
+                            }
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i)
+                            if (first + i < groups)
+#pragma unroll
+                                for (int t = 0; t < kLoads; ++t)
+                                    asm_write_b128(to + (first + i) * (kSegment * 16) + t * kBelow, v[i][t]);
                     }
+                }
+                // step s of B to its stage, from the adapter `of` of the lane
+                auto issue_b = [&](int s, uint32_t of) {
+                    const int e = 4 * s + b_chunk(tid);
+                    // past the end: something there is, multiplied with zeros
+                    const int element = min(r0 + e - by_rank8.quotient(e) * by.rank8, rank8 - 1);
+                    const uint16_t *p = x.B + (of * b_adapter + 8 * element);
+                    SWIGLU_LDS char *to =
+                        lds + kRing + (s % (kStages * kSteps)) * kStepBytes + wave * 1024;
+#pragma unroll
+                    for (int j = 0; j < kDma; ++j) gdma16(p + col[j], to + j * 4096);
+                };
+                auto next_stage = [&](int stage) {
+                    uint32_t of[kSteps];
+#pragma unroll
+                    for (int q = 0; q < kSteps; ++q)
+                        of[q] = asm_read_u16(
+                            at + kIds +
+                            min(by_rank8.quotient(4 * (stage * kSteps + q) + b_chunk(tid)), n - 1) * 2);
+#pragma unroll
+                    for (int q = 0; q < kSteps; ++q) issue_b(stage * kSteps + q, landed(of[q]));
                 };
 #pragma unroll
-                for (int s = 0; s < kStages - 1; ++s) issue_b(s);
-#pragma nounroll
-                for (int s = 0; s < steps; ++s) {
-                    wait_vmcnt<(kStages - 2) * kDma>();
-                    block_barrier();   // T and step s are there, and step s - 1 is read
-                    issue_b(s + kStages - 1);
-                    const int e = 4 * s + g;
-                    const int i = small_quotient(e, by.rank8), k = e - i * by.rank8;
-                    // the slots of the lane's rows that name the adapter of its k
-                    int slot[kRowBlocks];
+                for (int s = 0; s < kEarly; ++s) issue_b(s, id[s]);
+                wait_vmcnt<(kStages - 2) * kSteps * kDma>();
+                wait_lgkmcnt0();
+                block_barrier();   // the plan, T and stage 0 are there
+                next_stage(kStages - 1);
+
+                // the rows' first two slots of the chunk stay in registers
+                const int pair0 = j0 / 2, pairs = (min(x.slots, j0 + by.slots) + 1) / 2;
+                uint32_t where[kRowBlocks];
 #pragma unroll
-                    for (int t = 0; t < kRowBlocks; ++t) slot[t] = -1;
+                for (int t = 0; t < kRowBlocks; ++t)
+                    where[t] = asm_read_b32(at + pair0 * (kPlanRows * 4) + (row0 + 16 * t) * 4u);
+                wait_lgkmcnt0();
+#pragma unroll
+                for (int t = 0; t < kRowBlocks; ++t) asm volatile("" : "+v"(where[t]));
+
+                // T of row block t for step s, if the row names the adapter of the lane's
+                // k, else zeros: the LDS address, of part 0
+                uint32_t t_read[kRowBlocks];
+                struct {
+                    uint32_t a0, a1, key0, key1;
+                } look;
+                auto look_at = [&](int s, int pair) {
+                    const int e = 4 * s + g;
+                    const int i = by_rank8.quotient(e), k = e - i * by.rank8;
+                    const uint32_t key = r0 + k < rank8 ? i + 1 : 0xFFFFu;   // (no index is that far)
+                    look.key0 = 2 * pair >= j0 ? key : 0xFFFFu;
+                    look.key1 = 2 * pair + 1 < j0 + by.slots ? key << 16 : 0xFFFF0000u;
+                    look.a0 = t_row + 32u * k + (2 * pair - j0) * kParts * t_part;
+                    look.a1 = look.a0 + kParts * t_part;
+                };
+                auto find = [&](int t, uint32_t w, uint32_t otherwise) {
+                    const uint32_t a = (w & 0xFFFF0000u) == look.key1 ? look.a1 + t * kBelow : otherwise;
+                    t_read[t] = (w & 0xFFFFu) == look.key0 ? look.a0 + t * kBelow : a;
+                };
+                // slots past the first two
+                auto find_more = [&](int s) {
 #pragma nounroll
-                    for (int j = j0 / 2; 2 * j < min(x.slots, j0 + by.slots); ++j) {
+                    for (int pair = pair0 + 1; pair < pairs; ++pair) {
+                        look_at(s, pair);
                         uint32_t w[kRowBlocks];
 #pragma unroll
                         for (int t = 0; t < kRowBlocks; ++t)
-                            w[t] = asm_read_b32(at + j * (kPlanRows * 4) + (row0 + 16 * t) * 4u);
+                            w[t] = asm_read_b32(at + pair * (kPlanRows * 4) + (row0 + 16 * t) * 4u);
                         wait_lgkmcnt0();
 #pragma unroll
                         for (int t = 0; t < kRowBlocks; ++t) {
                             asm volatile("" : "+v"(w[t]));
-                            if (static_cast<int>(w[t] >> 16) == i + 1) slot[t] = 2 * j + 1;
-                            if (static_cast<int>(w[t] & 0xFFFFu) == i + 1) slot[t] = 2 * j;
+                            find(t, w[t], t_read[t]);
                         }
                     }
-                    uint32_t t_read[kRowBlocks];   // of part 0; 0: the zeros
+                };
+                u32x4 bf[2][S::TN][2], tf[2][kRows][kParts][2];
+                auto read_t = [&](u32x4 (&f)[kRows][kParts][2], int rb0, int t, int p) {
+                    const uint32_t from = t_read[rb0 + t] + p * t_part;
+                    f[t][p][0] = asm_read_b128<0>(from);
+                    f[t][p][1] = asm_read_b128<16>(from);
+                };
+                auto have = [&](u32x4 (&ft)[kRows][kParts][2], u32x4 (&fb)[S::TN][2]) {
+                    asm volatile("s_waitcnt lgkmcnt(0)");
 #pragma unroll
-                    for (int t = 0; t < kRowBlocks; ++t) {
-                        const int j = slot[t] - j0;
-                        t_read[t] = j >= 0 && j < by.slots && r0 + k < rank8
-                                        ? at + kT + ((row0 + 16 * t) * row_chunks +
-                                                     j * kParts * per_slot + 2 * k) * 16u
-                                        : 0u;
-                    }
-                    const uint32_t b_at = b_read + (s % kStages) * kStageBytes;
-                    u32x4 bf[S::TN][2], tf[2][kRows][kParts][2];
-                    auto read_t = [&](int group) {
+                    for (int t = 0; t < kRows; ++t)
 #pragma unroll
-                        for (int t = 0; t < kRows; ++t)
+                        for (int p = 0; p < kParts; ++p)
 #pragma unroll
-                            for (int p = 0; p < kParts; ++p) {
-                                const uint32_t a = t_read[group * kRows + t];
-                                const uint32_t from = a ? a + p * per_slot * 16u : at + kZeros;
-                                tf[group % 2][t][p][0] = asm_read_b128<0>(from);
-                                tf[group % 2][t][p][1] = asm_read_b128<16>(from);
+                            for (int h = 0; h < 2; ++h) asm volatile("" : "+v"(ft[t][p][h]));
+#pragma unroll
+                    for (int c = 0; c < S::TN; ++c)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) asm volatile("" : "+v"(fb[c][h]));
+                };
+                // step 0
+                look_at(0, pair0);
+#pragma unroll
+                for (int t = 0; t < kRowBlocks; ++t) find(t, where[t], at + kZeros);
+                if (pair0 + 1 < pairs) find_more(0);
+                read_b<0>(b_read, bf[0]);
+#pragma unroll
+                for (int t = 0; t < kRows; ++t)
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p) read_t(tf[0], 0, t, p);
+
+                // one step with B in bf[BUF]; the next step's B goes to the other buffer
+                auto step = [&](int s, auto buf_) {
+                    constexpr int buf = decltype(buf_)::value;
+                    constexpr int kMfma = 4 * kRows * S::TN;
+                    // T's buffers alternate over the groups of all steps
+                    constexpr int first = kRowGroups % 2 ? buf : 0;
+#pragma unroll
+                    for (int group = 0; group < kRowGroups; ++group) {
+                        have(tf[(first + group) % 2], bf[buf]);
+                        if (group + 1 < kRowGroups) {
+                            constexpr int kEvery = kMfma / (kRows * kParts) / 2;
+                            multiply<kRows>(acc, group * kRows, tf[(first + group) % 2], bf[buf], [&](int i) {
+                                if (i % kEvery == 0 && i / kEvery < kRows * kParts)
+                                    read_t(tf[(first + group + 1) % 2], (group + 1) * kRows,
+                                           i / kEvery / kParts, i / kEvery % kParts);
+                            });
+                            continue;
+                        }
+                        if (s + 1 < steps && (s + 1) % kSteps == 0) {
+                            // the next stage is there, and everyone has read this one
+                            wait_vmcnt<(kStages - 2) * kSteps * kDma>();
+                            block_barrier();
+                            next_stage((s + 1) / kSteps + kStages - 1);
+                        }
+                        const uint32_t b_at = b_read + ((s + 1) % (kStages * kSteps)) * kStepBytes;
+                        look_at(s + 1, pair0);
+                        // between the MFMAs: B of the next step, its addresses of T, its first T
+                        constexpr int kB = 2 * S::TN, kFinds = kB + kRowBlocks,
+                                      kAll = kFinds + kRows * kParts;
+                        multiply<kRows>(acc, group * kRows, tf[(first + group) % 2], bf[buf], [&](int i) {
+#pragma unroll
+                            for (int w = 0; w < kAll; ++w) {
+                                if (w * kMfma / kAll != i) continue;
+                                if (w < kB) {
+                                    bf[buf ^ 1][w / 2][w % 2] = read_b_one(b_at, w);
+                                } else if (w < kFinds) {
+                                    find(w - kB, where[w - kB], at + kZeros);
+                                    if (w + 1 == kFinds && pair0 + 1 < pairs) find_more(s + 1);
+                                } else {
+                                    read_t(tf[(first + group + 1) % 2], 0, (w - kFinds) / kParts,
+                                           (w - kFinds) % kParts);
+                                }
                             }
-                    };
-                    auto have_t = [&](int group) {
-                        asm volatile("s_waitcnt lgkmcnt(0)");
-#pragma unroll
-                        for (int t = 0; t < kRows; ++t)
-#pragma unroll
-                            for (int p = 0; p < kParts; ++p)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    asm volatile("" : "+v"(tf[group % 2][t][p][h]));
-                    };
-                    read_b<0>(b_at, bf);
-                    read_t(0);
-#pragma unroll
-                    for (int group = 0; group < kGroups; ++group) {
-                        have_t(group);
-                        if (group == 0)
-#pragma unroll
-                            for (int c = 0; c < S::TN; ++c)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) asm volatile("" : "+v"(bf[c][h]));
-                        if (group + 1 < kGroups) read_t(group + 1);
-                        asm volatile("s_nop 1");
-#pragma unroll
-                        for (int rest = 0; rest < 2; ++rest)
-#pragma unroll
-                            for (int t = 0; t < kRows; ++t)
-#pragma unroll
-                                for (int c = 0; c < S::TN; ++c)
-#pragma unroll
-                                    for (int h = 0; h < 2; ++h) {
-                                        const int rb = group * kRows + t;
-                                        mfma_16x16x32_acc(acc[rb / 2][c].v[2 * (rb % 2) + h],
-                                                          tf[group % 2][t][kGated ? c % 2 : 0][rest],
-                                                          bf[c][h]);
-                                    }
-                        __builtin_amdgcn_sched_barrier(0);
+                        });
                     }
-                    __builtin_amdgcn_sched_barrier(0);
+                };
+                constexpr std::integral_constant<int, 0> k0{};
+                constexpr std::integral_constant<int, 1> k1{};
+#pragma nounroll
+                for (int s = 0; s < steps; s += 2) {
+                    step(s, k0);
+                    if (s + 1 < steps) step(s + 1, k1);
                 }
                 wait_vmcnt<0>();
+                wait_lgkmcnt0();
                 block_barrier();   // T and the ring are free
             }
         wait_mfma_results();
@@ -316,6 +467,11 @@ struct LoraExpand {
             for (int c = 0; c < S::TN; ++c)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) asm volatile("" : "+a"(acc[a][c].v[q]));
+    }
+    __device__ __forceinline__ static u32x4 read_b_one(uint32_t from, int i) {
+        u32x4 r;
+        asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(r) : "v"(from), "i"((i / 2) * 2048 + (i % 2) * 1024));
+        return r;
     }
     template <int I>
     __device__ __forceinline__ static void read_b(uint32_t from, u32x4 (&bf)[S::TN][2]) {

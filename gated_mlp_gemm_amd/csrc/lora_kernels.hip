@@ -235,12 +235,32 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 1) void lora_shrink_kernel(S
             if (part == 0) ap.issue(k0, dst, j);
             else xp.issue<false>(k0, dst, j);
         };
+        // quad q of a lane: rows f .. f + 3 of the item's (8 of them are always of
+        // one adapter), and one row of X
+        int slot[4], c[4];
+        float weight[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int f = item * S::BM + 32 * wm + 16 * (q / 2) + 4 * (lane >> 4);
+            const int row = 32 * wn + 16 * (q % 2) + (lane & 15);
+            const int i = f < total ? f / x.cols : 0;
+            const int id = f < total ? list.list[i] : -2;
+            c[q] = f - i * x.cols;
+            // the weights of every slot that names id, the first one's T holding the sum
+            slot[q] = -1;
+            weight[q] = 0.0f;
+            for (int j = x.slots - 1; j >= 0; --j)
+                if (list.ids[j][row] == id) {
+                    slot[q] = j;
+                    weight[q] += list.weights[j][row];
+                }
+            weight[q] *= x.scale[max(id, 0)];
+        }
         S::Acc acc[S::TM][S::TN];
         pl.prologue(issue);
         pl.run_init0(issue, len, len, acc);
         pl.drain(acc);
 
-        // quad q of a lane: rows c .. c + 3 of the item's, and one row of X
         f32x4 sum[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -280,22 +300,9 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 1) void lora_shrink_kernel(S
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int at = item * S::BM + 32 * wm + 16 * (q / 2) + 4 * (lane >> 4);
-            const int row = 32 * wn + 16 * (q % 2) + (lane & 15);
-            if (at >= total) continue;
-            const int i = at / x.cols, c = at - i * x.cols;
-            const int id = list.list[i];
-            // the weights of every slot that names id, the first one's T holding the sum
-            int slot = -1;
-            float w = 0.0f;
-            for (int j = x.slots - 1; j >= 0; --j)
-                if (list.ids[j][row] == id) {
-                    slot = j;
-                    w += list.weights[j][row];
-                }
-            if (slot >= 0)
-                store_t(x.T + (static_cast<int64_t>(m0 + row) * x.slots + slot) * (2 * x.cols), c,
-                        sum[q] * (w * x.scale[id]));
+            const int64_t row = m0 + 32 * wn + 16 * (q % 2) + (lane & 15);
+            if (slot[q] >= 0)
+                store_t(x.T + (row * x.slots + slot[q]) * (2 * x.cols), c[q], sum[q] * weight[q]);
         }
         __syncthreads();   // the ring and `word` are free
     }
@@ -314,14 +321,17 @@ hipError_t launch_lora_shrink(const uint16_t *X, const LoraTable &t, const int *
     const int64_t tiles = ceil_div(M, kShrinkRows);
     const int64_t named = static_cast<int64_t>(kShrinkRows) * slots;
     const int64_t items = ceil_div((t.count < named ? t.count : named) * cols, S::BM);
-    // a split keeps at least six K steps, and the last to arrive has its reads
+    // a split keeps at least eight K steps, and the last to arrive has its reads
     // of the others' sums in flight in two goes
-    int64_t most = ceil_div(K, S::BK) / 6;
+    const int64_t nk = ceil_div(K, S::BK);
+    int64_t most = nk / 8;
     if (most > 16) most = 16;
     if (most < 1) most = 1;
-    // workgroups a row block: one a compute unit in all, and no more than there
-    // can be work for
+    // workgroups a row block: one a compute unit in all (two where that leaves
+    // them 64 K steps and more: row blocks that name one adapter more than
+    // others would else end last), and no more than there can be work for
     int64_t G = ws.cus / tiles;
+    if (G * 64 <= nk) G = 2 * ws.cus / tiles;
     if (G > items * most) G = items * most;
     if (G < 1) G = 1;
     if (ws.base == nullptr || ws.counters == nullptr ||

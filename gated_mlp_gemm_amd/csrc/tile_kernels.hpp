@@ -284,15 +284,24 @@ struct WithLora : Base {
 };
 using PairMulLora = WithLora<PairMulEpilogue>;
 using StoreLora = WithLora<StoreEpilogue>;
-template <class S, bool kQuarter = false, class Epi>
-__device__ __forceinline__ void expand_adapters(SWIGLU_LDS char *lds, const Epi &epi,
-                                                typename S::Acc (&acc)[S::TM][S::TN], int m0,
-                                                int n0) {
-    if constexpr (std::is_same<Epi, PairMulLora>::value)
-        LoraExpand<S, true, kQuarter>::run(lds, epi.lora, acc, m0, n0);
-    else if constexpr (std::is_same<Epi, StoreLora>::value)
-        LoraExpand<S, false, kQuarter>::run(lds, epi.lora, acc, m0, n0);
-}
+// begin() before a tile's K steps, run() behind them.
+template <class S, class Epi, bool kQuarter = false>
+struct Adapters {
+    __device__ __forceinline__ void begin(const Epi &, int) {}
+    __device__ __forceinline__ void run(SWIGLU_LDS char *, const Epi &,
+                                        typename S::Acc (&)[S::TM][S::TN], int, int) {}
+};
+template <class S, class Base, bool kQuarter>
+struct Adapters<S, WithLora<Base>, kQuarter> {
+    LoraExpand<S, std::is_same<Base, PairMulEpilogue>::value, kQuarter> expand;
+    __device__ __forceinline__ void begin(const WithLora<Base> &epi, int m0) {
+        expand.begin(epi.lora, m0);
+    }
+    __device__ __forceinline__ void run(SWIGLU_LDS char *lds, const WithLora<Base> &epi,
+                                        typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0) {
+        expand.run(lds, epi.lora, acc, m0, n0);
+    }
+};
 
 // The K steps [0, len) of one tile into `acc`.  With 16x16 MFMAs the first
 // step's MFMAs start the accumulators (C = 0): no vector instructions zero its
@@ -394,11 +403,13 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             for (; j < sch.dp; j += grid) {
                 typename S::Acc acc[S::TM][S::TN];
                 zero_acc_mi32<S>(acc);
+                const int m0 = tm * S::BM, n0 = tn * S::BN;
+                Adapters<S, Epi> adapters;
+                adapters.begin(epi, m0);
                 pl.prologue_wait();
                 run_tile<S, kEven>(pl, issue, nk, acc);
                 pl.drain(acc);
-                const int m0 = tm * S::BM, n0 = tn * S::BN;
-                expand_adapters<S>(lds, epi, acc, m0, n0);
+                adapters.run(lds, epi, acc, m0, n0);
                 if (j + grid < sch.dp) {
                     tile_coords(xcd_order(j + grid, sch.dp), sch.tiles_m, sch.tiles_n, sch.group_m, tm,
                                 tn);
@@ -426,8 +437,10 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             const int n0 = tn * S::BN + (q & 1) * Q::BN;
             if (m0 >= M || n0 >= B.rows) continue;   // quarter wholly past the output's edge
             typename Q::Acc acc[Q::TM][Q::TN];
+            Adapters<Q, Epi, true> adapters;
+            adapters.begin(epi, m0);
             tile_mainloop<Q, kEven>(lds, Ak, B, M, K, m0, n0, 0, sch.nk, sch.nk, acc);
-            expand_adapters<Q, true>(lds, epi, acc, m0, n0);
+            adapters.run(lds, epi, acc, m0, n0);
             epi.template apply<Q>(acc, m0, n0, threadIdx.x);
         }
         whole_tiles();
@@ -448,10 +461,12 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             int tm, tn;
             tile_coords(sch.dp + i, sch.tiles_m, sch.tiles_n, sch.group_m, tm, tn);
             typename S::Acc acc[S::TM][S::TN];
+            Adapters<S, Epi> adapters;
+            adapters.begin(epi, tm * S::BM);
             tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
             // (the adapters' terms once a tile)
             if (piece == sch.pieces - 1)
-                expand_adapters<S>(lds, epi, acc, tm * S::BM, tn * S::BN);
+                adapters.run(lds, epi, acc, tm * S::BM, tn * S::BN);
             const float *slots = sch.partials + static_cast<int64_t>(i) * sch.pieces * S::BM * S::BN;
             store_partial_coherent<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN,
                                       acc, threadIdx.x);
@@ -493,10 +508,12 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             int tm, tn;
             tile_coords(t, sch.tiles_m, sch.tiles_n, sch.group_m, tm, tn);
             typename S::Acc acc[S::TM][S::TN];
+            Adapters<S, Epi> adapters;
+            adapters.begin(epi, tm * S::BM);
             tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
             // (the adapters' terms once a tile)
             if (piece == sch.pieces - 1)
-                expand_adapters<S>(lds, epi, acc, tm * S::BM, tn * S::BN);
+                adapters.run(lds, epi, acc, tm * S::BM, tn * S::BN);
             store_partial<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN, acc,
                              threadIdx.x);
         }
