@@ -117,14 +117,15 @@ __device__ __forceinline__ void gdma16(const uint16_t *p, SWIGLU_LDS char *lds) 
 // K runs over the adapters of the tile's plan, rank8 chunks of 8 elements each,
 // 32 k a step.  LDS holds T of the tile's rows (only the slots that there are;
 // a lane whose row does not name the adapter of its 8 k reads zeros from beside
-// it) and a ring of B's rows, kSteps steps a stage, loaded straight to LDS; so
-// every byte is read once a tile.  One wave a SIMD issues an instruction about
-// every 6 clocks, so what bounds this is the instructions around the MFMAs, not
-// bytes: the addresses and LDS reads of a group of row blocks stand between
-// the MFMAs of the group before it, those of the next step between the last
-// group's.  (In clocks, 256 x 256 tile, Gate and Up, 2 slots of rank 16: a step
-// 4500 and what comes before the first 5100 with addresses and MFMAs one after
-// the other and T copied to LDS by 16-byte chunks of any row length.)  The first
+// it) and a ring of B's rows, kSteps steps a stage, both loaded straight to
+// LDS; so every byte is read once a tile.  Both lie in planes of 64 bytes a
+// row, the 16-byte chunks swizzled by the row (16 rows on 16 different banks).
+// One wave a SIMD issues an instruction about every 6 clocks, so what bounds
+// this is the instructions around the MFMAs, not bytes: the addresses and LDS
+// reads of a group of row blocks stand between the MFMAs of the group before.
+// (256 x 256 tile, Gate and Up, 2 slots of rank 16: 4500 clocks a step with
+// addresses and MFMAs one after the other, of which the MFMAs are 2048, and
+// 5100 before the first with rows of T of any length in LDS.)  The first
 // stages' adapters are looked up before the tile's K steps (begin).
 template <class S, bool kGated, bool kQuarter>
 struct LoraExpand {
@@ -135,8 +136,8 @@ struct LoraExpand {
     // LDS: where [4][256] | ids | zeros | T ... | ring of B
     static constexpr int kIds = 4 * kPlanRows * 4;
     static constexpr int kZeros = kIds + kPlanRows * kMaxLoraSlots * 2;
-    static constexpr int kZeroBytes = 1024;
-    static constexpr int kT = kZeros + kZeroBytes;
+    static constexpr int kRowBlocks = S::kWaveM / 16;
+    static constexpr int kT = kZeros + kRowBlocks * 1024;   // (a wave's rows, 64 bytes each)
     // a stage of few columns takes four steps: its barrier and its latency are
     // most of its time
     static constexpr int kSteps = S::BN <= 64 ? 4 : 1;
@@ -145,18 +146,14 @@ struct LoraExpand {
     static constexpr int kRing = S::kLdsBytes - kStages * kSteps * kStepBytes;
     static constexpr int kDma = kStepBytes / 4096;   // loads a wave and step
     static constexpr int kEarly = (kStages - 1) * kSteps;
-    // 16-byte chunks of a row of T in LDS: an odd count, so that 16 rows lie on
-    // 16 different banks.  A slot's part takes kSegment-chunk groups.
-    static constexpr int kRowChunks = (((kRing - kT) / (16 * S::BM)) - 1) | 1;
-    static constexpr int kSegment = 4;
-    static constexpr int kGroups = kRowChunks / kSegment < 10 ? kRowChunks / kSegment : 10;
-    static_assert(kRowChunks * 16 * S::BM <= kRing - kT && kGroups >= kParts, "T fits");
-    static_assert(kGroups * kSegment * 16 <= kZeroBytes, "zeros as long as a row");
+    // a plane of T: 16 elements (4 chunks, rounded and rest) of a slot's part
+    static constexpr int kPlane = S::BM * 64;
+    static constexpr int kPlanes = (kRing - kT) / kPlane;
+    static_assert(kPlanes >= kParts, "T fits");
 
-    // groups of 4 chunks (16 elements) of a slot's part
-    static constexpr int segments(int rank8) { return (rank8 + 1) / 2; }
+    static constexpr int planes(int rank8) { return (rank8 + 1) / 2; }   // of a slot's part
     static LoraChunks chunks(int slots, int rank) {
-        const int rank8 = rank / 8, most = kGroups / kParts;   // groups there are
+        const int rank8 = rank / 8, most = kPlanes / kParts;
         if (slots > most) return {most, rank8 < 2 ? rank8 : 2};
         const int r = most / slots * 2 < rank8 ? most / slots * 2 : rank8;
         const int n = (rank8 + r - 1) / r;   // as even as they can be
@@ -234,7 +231,8 @@ struct LoraExpand {
         dma16(pr, lds + wave * 1024, static_cast<uint32_t>(kPlanWhere + (m0 % kPlanRows) * 4) + lane * 16u,
               wave * (kPlanRows * 4));
         dma16(pr, lds + kIds + wave * 1024, kPlanIds + lane * 16u, wave * 1024);
-        if (wave == 0) asm_write_b128(at + kZeros + lane * 16u, u32x4{0u, 0u, 0u, 0u});
+        for (int i = wave; i < kRowBlocks; i += 4)
+            asm_write_b128(at + kZeros + i * 1024 + lane * 16u, u32x4{0u, 0u, 0u, 0u});
 
         uint32_t col[kDma];   // elements from an adapter's B to the lane's rows
 #pragma unroll
@@ -245,59 +243,39 @@ struct LoraExpand {
         }
         const int64_t b_adapter = static_cast<int64_t>(x.cols) * x.rank;
         const Divisor by_rank8(by.rank8);
-        const int parts_chunks = segments(by.rank8) * kSegment;   // of a slot's part, in LDS
-        const int groups = by.slots * kParts * segments(by.rank8);
+        const int planes_part = planes(by.rank8);
         const int steps = (n * by.rank8 + 3) / 4;
 
         const int row0 = wm * S::kWaveM + r16;   // the lane's row of T in row block 0
-        constexpr int kRowBlocks = S::kWaveM / 16;
         // row blocks whose T is in registers at once, one such group ahead
         constexpr int kRows = kRowBlocks > 2 ? 2 / kParts : kRowBlocks;
-        constexpr int kRowGroups = kRowBlocks / kRows;
-        constexpr uint32_t kBelow = 16u * kRowChunks * 16u;   // from one row block to the next
-        const uint32_t t_row = at + kT + static_cast<uint32_t>(row0 * kRowChunks) * 16u;
-        const uint32_t t_part = static_cast<uint32_t>(parts_chunks) * 16u;
+        constexpr int kGroups = kRowBlocks / kRows;
+        const uint32_t t_row = at + kT + row0 * 64u;
+        const uint32_t t_part = static_cast<uint32_t>(planes_part * kPlane);
         const uint32_t b_read = at + kRing + (wn * S::kWaveN + r16) * 64u + ((g ^ swizzle(r16)) * 16u);
 
 #pragma nounroll
         for (int j0 = 0; j0 < x.slots; j0 += by.slots)
 #pragma nounroll
             for (int r0 = 0; r0 < rank8; r0 += by.rank8) {
-                // T: a wave a quarter of the rows, 16 rows by 4 chunks a load; group i is
-                // 4 chunks of one slot's part
+                // T: a wave a quarter of the rows, 16 rows of a plane a load.  (Past the
+                // last slot: past the row, or zeros; never read.)
                 {
-                    constexpr int kLoads = S::BM / 64, kBatch = S::BM == 256 || S::kOccupancy > 1 ? 2 : 4;
-                    const int row = wave * (S::BM / 4) + lane / 4;
-                    const uint32_t from = static_cast<uint32_t>(row * row_bytes) + (lane & 3) * 16u;
-                    const uint32_t to = at + kT + static_cast<uint32_t>(row * kRowChunks) * 16u + (lane & 3) * 16u;
-                    int sp = 0, seg = 0;
+                    const uint32_t from =
+                        static_cast<uint32_t>((wave * (S::BM / 4) + lane / 4) * row_bytes) +
+                        ((lane & 3) ^ swizzle(lane / 4)) * 16u;
+                    SWIGLU_LDS char *to = lds + kT + wave * (kPlane / 4);
 #pragma nounroll
-                    for (int first = 0; first < groups; first += kBatch) {
-                        u32x4 v[kBatch][kLoads];
+                    for (int sp = 0; sp < by.slots * kParts; ++sp)
+#pragma nounroll
+                        for (int i = 0; i < planes_part; ++i) {
+                            const uint32_t soff = static_cast<uint32_t>(
+                                (j0 * kParts + sp) * x.rank * 4 + r0 * 32 + i * 64);
 #pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-                            if (first + i < groups) {
-                                // (past the last slot: past the row, or zeros; never read)
-                                const uint32_t soff = static_cast<uint32_t>(
-                                    (j0 * kParts + sp) * x.rank * 4 + r0 * 32 + seg * (kSegment * 16));
-#pragma unroll
-                                for (int t = 0; t < kLoads; ++t)
-                                    v[i][t] = __builtin_bit_cast(
-                                        u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                   tr, static_cast<int>(from),
-                                                   static_cast<int>(soff + t * 16u * row_bytes), 0));
-                                if (++seg == segments(by.rank8)) {
-                                    seg = 0;
-                                    ++sp;
-                                }
-                            }
-#pragma unroll
-                        for (int i = 0; i < kBatch; ++i)
-                            if (first + i < groups)
-#pragma unroll
-                                for (int t = 0; t < kLoads; ++t)
-                                    asm_write_b128(to + (first + i) * (kSegment * 16) + t * kBelow, v[i][t]);
-                    }
+                            for (int t = 0; t < S::BM / 64; ++t)
+                                dma16(tr, to + t * 1024, from, soff + t * 16u * row_bytes);
+                            to += kPlane;
+                        }
                 }
                 // step s of B to its stage, from the adapter `of` of the lane
                 auto issue_b = [&](int s, uint32_t of) {
@@ -337,48 +315,52 @@ struct LoraExpand {
 #pragma unroll
                 for (int t = 0; t < kRowBlocks; ++t) asm volatile("" : "+v"(where[t]));
 
-                // T of row block t for step s, if the row names the adapter of the lane's
-                // k, else zeros: the LDS address, of part 0
-                uint32_t t_read[kRowBlocks];
-                struct {
-                    uint32_t a0, a1, key0, key1;
-                } look;
+                // Where the lane's k of a step is in T, row block 0 and part 0, for the slots
+                // of a pair, and what a row's `where` holds if it names that adapter.
+                struct Look {
+                    uint32_t at[2], key[2];
+                };
                 auto look_at = [&](int s, int pair) {
                     const int e = 4 * s + g;
                     const int i = by_rank8.quotient(e), k = e - i * by.rank8;
                     const uint32_t key = r0 + k < rank8 ? i + 1 : 0xFFFFu;   // (no index is that far)
-                    look.key0 = 2 * pair >= j0 ? key : 0xFFFFu;
-                    look.key1 = 2 * pair + 1 < j0 + by.slots ? key << 16 : 0xFFFF0000u;
-                    look.a0 = t_row + 32u * k + (2 * pair - j0) * kParts * t_part;
-                    look.a1 = look.a0 + kParts * t_part;
+                    Look l;
+                    l.key[0] = 2 * pair >= j0 ? key : 0xFFFFu;
+                    l.key[1] = 2 * pair + 1 < j0 + by.slots ? key : 0xFFFFu;
+                    l.at[0] = t_row + ((2 * pair - j0) * kParts * planes_part + (k >> 1)) * kPlane +
+                              ((2 * (k & 1)) ^ swizzle(r16)) * 16u;
+                    l.at[1] = l.at[0] + kParts * t_part;
+                    return l;
                 };
-                auto find = [&](int t, uint32_t w, uint32_t otherwise) {
-                    const uint32_t a = (w & 0xFFFF0000u) == look.key1 ? look.a1 + t * kBelow : otherwise;
-                    t_read[t] = (w & 0xFFFFu) == look.key0 ? look.a0 + t * kBelow : a;
+                const uint32_t zeros = at + kZeros;
+                auto match = [&](const Look &l, uint32_t w, uint32_t (&from)[kParts]) {
+                    const bool lo = (w & 0xFFFFu) == l.key[0], hi = (w >> 16) == l.key[1];
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p)
+                        from[p] = lo ? l.at[0] + p * t_part : hi ? l.at[1] + p * t_part : from[p];
                 };
-                // slots past the first two
-                auto find_more = [&](int s) {
+                // T of row block t for the lane's k, all parts, if the row names its adapter,
+                // else zeros
+                auto read_t = [&](u32x4 (&f)[kParts][2], const Look &l, int s, int t) {
+                    uint32_t from[kParts];
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p) from[p] = zeros;
+                    match(l, where[t], from);
+                    if (pair0 + 1 < pairs) {
 #pragma nounroll
-                    for (int pair = pair0 + 1; pair < pairs; ++pair) {
-                        look_at(s, pair);
-                        uint32_t w[kRowBlocks];
-#pragma unroll
-                        for (int t = 0; t < kRowBlocks; ++t)
-                            w[t] = asm_read_b32(at + pair * (kPlanRows * 4) + (row0 + 16 * t) * 4u);
-                        wait_lgkmcnt0();
-#pragma unroll
-                        for (int t = 0; t < kRowBlocks; ++t) {
-                            asm volatile("" : "+v"(w[t]));
-                            find(t, w[t], t_read[t]);
+                        for (int pair = pair0 + 1; pair < pairs; ++pair) {
+                            uint32_t w = asm_read_b32(at + pair * (kPlanRows * 4) + (row0 + 16 * t) * 4u);
+                            w = landed(w);
+                            match(look_at(s, pair), w, from);
                         }
+                    }
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p) {
+                        f[p][0] = read_one(from[p], t * 1024);
+                        f[p][1] = read_one(from[p] ^ 16u, t * 1024);
                     }
                 };
                 u32x4 bf[2][S::TN][2], tf[2][kRows][kParts][2];
-                auto read_t = [&](u32x4 (&f)[kRows][kParts][2], int rb0, int t, int p) {
-                    const uint32_t from = t_read[rb0 + t] + p * t_part;
-                    f[t][p][0] = asm_read_b128<0>(from);
-                    f[t][p][1] = asm_read_b128<16>(from);
-                };
                 auto have = [&](u32x4 (&ft)[kRows][kParts][2], u32x4 (&fb)[S::TN][2]) {
                     asm volatile("s_waitcnt lgkmcnt(0)");
 #pragma unroll
@@ -393,61 +375,51 @@ struct LoraExpand {
                         for (int h = 0; h < 2; ++h) asm volatile("" : "+v"(fb[c][h]));
                 };
                 // step 0
-                look_at(0, pair0);
+                Look look = look_at(0, pair0);
 #pragma unroll
-                for (int t = 0; t < kRowBlocks; ++t) find(t, where[t], at + kZeros);
-                if (pair0 + 1 < pairs) find_more(0);
-                read_b<0>(b_read, bf[0]);
+                for (int w = 0; w < 2 * S::TN; ++w) bf[0][w / 2][w % 2] = read_one(b_read, w * 1024);
 #pragma unroll
-                for (int t = 0; t < kRows; ++t)
-#pragma unroll
-                    for (int p = 0; p < kParts; ++p) read_t(tf[0], 0, t, p);
+                for (int t = 0; t < kRows; ++t) read_t(tf[0][t], look, 0, t);
 
                 // one step with B in bf[BUF]; the next step's B goes to the other buffer
                 auto step = [&](int s, auto buf_) {
                     constexpr int buf = decltype(buf_)::value;
                     constexpr int kMfma = 4 * kRows * S::TN;
                     // T's buffers alternate over the groups of all steps
-                    constexpr int first = kRowGroups % 2 ? buf : 0;
-#pragma unroll
-                    for (int group = 0; group < kRowGroups; ++group) {
+                    constexpr int first = kGroups % 2 ? buf : 0;
+                    uint32_t b_at = b_read;
+                    for_each(std::make_integer_sequence<int, kGroups>{}, [&](auto group_) {
+                        constexpr int group = decltype(group_)::value;
                         have(tf[(first + group) % 2], bf[buf]);
-                        if (group + 1 < kRowGroups) {
-                            constexpr int kEvery = kMfma / (kRows * kParts) / 2;
-                            multiply<kRows>(acc, group * kRows, tf[(first + group) % 2], bf[buf], [&](int i) {
-                                if (i % kEvery == 0 && i / kEvery < kRows * kParts)
-                                    read_t(tf[(first + group + 1) % 2], (group + 1) * kRows,
-                                           i / kEvery / kParts, i / kEvery % kParts);
-                            });
-                            continue;
+                        constexpr bool next = group + 1 == kGroups;   // the next reads are the next step's
+                        if constexpr (next) {
+                            if (s + 1 < steps && (s + 1) % kSteps == 0) {
+                                // the next stage is there, and everyone has read this one
+                                wait_vmcnt<(kStages - 2) * kSteps * kDma>();
+                                block_barrier();
+                                next_stage((s + 1) / kSteps + kStages - 1);
+                            }
+                            b_at += ((s + 1) % (kStages * kSteps)) * kStepBytes;
+                            look = look_at(s + 1, pair0);
                         }
-                        if (s + 1 < steps && (s + 1) % kSteps == 0) {
-                            // the next stage is there, and everyone has read this one
-                            wait_vmcnt<(kStages - 2) * kSteps * kDma>();
-                            block_barrier();
-                            next_stage((s + 1) / kSteps + kStages - 1);
-                        }
-                        const uint32_t b_at = b_read + ((s + 1) % (kStages * kSteps)) * kStepBytes;
-                        look_at(s + 1, pair0);
-                        // between the MFMAs: B of the next step, its addresses of T, its first T
-                        constexpr int kB = 2 * S::TN, kFinds = kB + kRowBlocks,
-                                      kAll = kFinds + kRows * kParts;
+                        // between the MFMAs: T of the next group, B of the next step
+                        constexpr int kB = 2 * S::TN;
+                        constexpr int all = kRows + (next ? kB : 0);
                         multiply<kRows>(acc, group * kRows, tf[(first + group) % 2], bf[buf], [&](int i) {
 #pragma unroll
-                            for (int w = 0; w < kAll; ++w) {
-                                if (w * kMfma / kAll != i) continue;
-                                if (w < kB) {
-                                    bf[buf ^ 1][w / 2][w % 2] = read_b_one(b_at, w);
-                                } else if (w < kFinds) {
-                                    find(w - kB, where[w - kB], at + kZeros);
-                                    if (w + 1 == kFinds && pair0 + 1 < pairs) find_more(s + 1);
-                                } else {
-                                    read_t(tf[(first + group + 1) % 2], 0, (w - kFinds) / kParts,
-                                           (w - kFinds) % kParts);
-                                }
+                            for (int w = 0; w < kB + kRows; ++w) {
+                                if (w >= all || w * kMfma / all != i) continue;
+                                if (next && w < kB)
+                                    bf[buf ^ 1][w / 2][w % 2] = read_one(b_at, w * 1024);
+                                else if (next)
+                                    read_t(tf[(first + group + 1) % 2][w - kB], look, s + 1, w - kB);
+                                else
+                                    read_t(tf[(first + group + 1) % 2][w], look, s,
+                                           (group + 1) * kRows + w);
                             }
                         });
-                    }
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
                 };
                 constexpr std::integral_constant<int, 0> k0{};
                 constexpr std::integral_constant<int, 1> k1{};
@@ -468,17 +440,15 @@ struct LoraExpand {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) asm volatile("" : "+a"(acc[a][c].v[q]));
     }
-    __device__ __forceinline__ static u32x4 read_b_one(uint32_t from, int i) {
-        u32x4 r;
-        asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(r) : "v"(from), "i"((i / 2) * 2048 + (i % 2) * 1024));
-        return r;
+    template <int... I, class F>
+    __device__ __forceinline__ static void for_each(std::integer_sequence<int, I...>, const F &f) {
+        (f(std::integral_constant<int, I>{}), ...);
     }
-    template <int I>
-    __device__ __forceinline__ static void read_b(uint32_t from, u32x4 (&bf)[S::TN][2]) {
-        if constexpr (I < 2 * S::TN) {
-            bf[I / 2][I % 2] = asm_read_b128<(I / 2) * 2048 + (I % 2) * 1024>(from);
-            read_b<I + 1>(from, bf);
-        }
+    // (the offset is a constant once everything is unrolled)
+    __device__ __forceinline__ static u32x4 read_one(uint32_t from, int offset) {
+        u32x4 r;
+        asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(r) : "v"(from), "i"(offset));
+        return r;
     }
 };
 
