@@ -56,9 +56,10 @@ struct LoraTerm {
 };
 
 // Quotients by a small divisor that is the same for all lanes, by its
-// reciprocal: exact while the quotient is below 2^12 and the divisor at most 64
-// (e + 1/2 is at least 1/2 from the next multiple of d, 2^-7 of a quotient, and
-// the two roundings move it by less than 2^-10).
+// reciprocal: exact while e < 2^20, the quotient is below 2^12 and the divisor
+// at most 512 (e + 1/2 is at least 1/2 from the next multiple of d, 2^-10 of a
+// quotient, and the roundings move a quotient below 2^12 by less than 2^-10:
+// three of them, each 2^-24 of it).
 struct Divisor {
     int d;
     float inverse;

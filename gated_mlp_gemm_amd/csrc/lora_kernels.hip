@@ -161,28 +161,32 @@ struct AdapterPanel {
     static_assert(S::kChunksPerRow == 8, "a wave loads 8 rows");
     __amdgpu_buffer_rsrc_t rsrc[S::kDmaA];
     uint32_t voff;
-    int klim, lds_base;
+    int klim, lds_base, last;
 
     __device__ __forceinline__ void init(const ShrinkArgs &x, const SWIGLU_LDS AdapterList &l,
-                                         int first, int total) {
+                                         const Divisor &cols, int first, int total) {
         const int lane = threadIdx.x & 63;
         const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
         const int c = (lane % 8) ^ swz<S>(wave * 8 + lane / 8);
         voff = static_cast<uint32_t>(lane / 8) * static_cast<uint32_t>(x.K) * 2u + c * 16u;
         klim = x.K - c * 8;
+        last = x.K - S::BK;
         lds_base = wave * 1024;
 #pragma unroll
         for (int j = 0; j < S::kDmaA; ++j) {
             const int at = first + 32 * j + 8 * wave;
             const bool in = at < total;
-            const int i = in ? at / x.cols : 0, row = in ? at - i * x.cols : 0;
+            const int i = in ? cols.quotient(at) : 0, row = in ? at - i * x.cols : 0;
             const int id = __builtin_amdgcn_readfirstlane(static_cast<int>(l.list[i]));
             rsrc[j] = make_rsrc(x.A + (static_cast<int64_t>(id) * x.cols + row) * x.K,
                                 in ? 8u * static_cast<uint32_t>(x.K) * 2u : 0u);
         }
     }
+    // kEven: K is a multiple of BK (a step past the end loads the last again)
+    template <bool kEven>
     __device__ __forceinline__ void issue(int k0, SWIGLU_LDS char *dst, int only) const {
-        const uint32_t v = k0 < klim ? voff : kOutOfRange;
+        if constexpr (kEven) k0 = min(k0, last);
+        const uint32_t v = kEven || k0 < klim ? voff : kOutOfRange;
 #pragma unroll
         for (int j = 0; j < S::kDmaA; ++j)
             if (only < 0 || only == j)
@@ -190,24 +194,17 @@ struct AdapterPanel {
     }
 };
 
-__global__ __launch_bounds__(ShapeShrink::kThreads, 1) void lora_shrink_kernel(ShrinkArgs x) {
+template <bool kEven>
+__device__ __forceinline__ void shrink_body(const ShrinkArgs &x, char *smem,
+                                            SWIGLU_LDS AdapterList &list, SWIGLU_LDS unsigned &word) {
     using S = ShapeShrink;
-    __shared__ __attribute__((aligned(16))) char smem[S::kLdsBytes];
-    __shared__ AdapterList list_;
-    __shared__ unsigned word;
     SWIGLU_LDS char *lds = (SWIGLU_LDS char *)smem;
-    SWIGLU_LDS AdapterList &list = *(SWIGLU_LDS AdapterList *)&list_;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / S::WN, wn = wave % S::WN;
     // neighbouring row blocks, which often name the same adapters, on one XCD
     const int G = x.per_rows;
-    const int workers = gridDim.x - x.plan_wgs;
-    if (static_cast<int>(blockIdx.x) >= workers) {
-        write_plan(x, *reinterpret_cast<PlanLists *>(smem), blockIdx.x - workers);
-        return;
-    }
-    const int at_ = xcd_order(blockIdx.x, workers);
+    const int at_ = xcd_order(blockIdx.x, gridDim.x - x.plan_wgs);
     const int rows_at = at_ / G, y = at_ % G;
     const int m0 = rows_at * kShrinkRows;
 
@@ -215,6 +212,7 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 1) void lora_shrink_kernel(S
     __syncthreads();
     const int n = __builtin_amdgcn_readfirstlane(list.n);
     const int total = n * x.cols;
+    const Divisor cols(x.cols);
     const int items = (total + S::BM - 1) / S::BM;
     if (items == 0) return;
     const int splits = max(1, min(G / items, x.most_splits));
@@ -226,15 +224,16 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 1) void lora_shrink_kernel(S
         const int item = job / splits, split = job % splits;
         const int kb = split * nk / splits, len = (split + 1) * nk / splits - kb;
         AdapterPanel ap;
-        ap.init(x, list, item * S::BM, total);
+        ap.init(x, list, cols, item * S::BM, total);
         Pipeline<S> pl;
         pl.init(lds);
         // steps past the range load nothing (K step nk is past the end of K)
         auto issue = [&](int s, int part, SWIGLU_LDS char *dst, int j) {
             const int k0 = (s < len ? kb + s : nk) * S::BK;
-            if (part == 0) ap.issue(k0, dst, j);
-            else xp.issue<false>(k0, dst, j);
+            if (part == 0) ap.issue<kEven>(k0, dst, j);
+            else xp.issue<kEven>(k0, dst, j);
         };
+        pl.prologue_issue(issue);
         // quad q of a lane: rows f .. f + 3 of the item's (8 of them are always of
         // one adapter), and one row of X
         int slot[4], c[4];
@@ -243,7 +242,7 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 1) void lora_shrink_kernel(S
         for (int q = 0; q < 4; ++q) {
             const int f = item * S::BM + 32 * wm + 16 * (q / 2) + 4 * (lane >> 4);
             const int row = 32 * wn + 16 * (q % 2) + (lane & 15);
-            const int i = f < total ? f / x.cols : 0;
+            const int i = f < total ? cols.quotient(f) : 0;
             const int id = f < total ? list.list[i] : -2;
             c[q] = f - i * x.cols;
             // the weights of every slot that names id, the first one's T holding the sum
@@ -257,8 +256,8 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 1) void lora_shrink_kernel(S
             weight[q] *= x.scale[max(id, 0)];
         }
         S::Acc acc[S::TM][S::TN];
-        pl.prologue(issue);
-        pl.run_init0(issue, len, len, acc);
+        pl.prologue_wait();
+        pl.run_init0<kEven>(issue, len, len, acc);
         pl.drain(acc);
 
         f32x4 sum[4];
@@ -306,6 +305,19 @@ __global__ __launch_bounds__(ShapeShrink::kThreads, 1) void lora_shrink_kernel(S
         }
         __syncthreads();   // the ring and `word` are free
     }
+}
+
+__global__ __launch_bounds__(ShapeShrink::kThreads, 1) void lora_shrink_kernel(ShrinkArgs x) {
+    __shared__ __attribute__((aligned(16))) char smem[ShapeShrink::kLdsBytes];
+    __shared__ AdapterList list;
+    __shared__ unsigned word;
+    SWIGLU_LDS AdapterList &l = *(SWIGLU_LDS AdapterList *)&list;
+    SWIGLU_LDS unsigned &w = *(SWIGLU_LDS unsigned *)&word;
+    const int workers = gridDim.x - x.plan_wgs;
+    if (static_cast<int>(blockIdx.x) >= workers)
+        write_plan(x, *reinterpret_cast<PlanLists *>(smem), blockIdx.x - workers);
+    else if (x.K % ShapeShrink::BK == 0) shrink_body<true>(x, smem, l, w);
+    else shrink_body<false>(x, smem, l, w);
 }
 
 int lora_plan_bytes(int count, int slots) {

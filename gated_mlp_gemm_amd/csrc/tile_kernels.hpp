@@ -522,7 +522,7 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
 template <class S, class Epi, int TAIL>
 __global__ __launch_bounds__(S::kThreads, S::kOccupancy) void gemm_tiles_kernel(
     KMajor Ak, KMajor B, int M, int K, Epi epi, Schedule sch) {
-    __shared__ __attribute__((aligned(16))) char smem[S::kLdsBytes];
+    __shared__ __attribute__((aligned(128))) char smem[S::kLdsBytes];
     if (K % S::BK == 0) gemm_tiles_body<S, Epi, TAIL, true>(smem, Ak, B, M, K, epi, sch);
     else gemm_tiles_body<S, Epi, TAIL, false>(smem, Ak, B, M, K, epi, sch);
 }
