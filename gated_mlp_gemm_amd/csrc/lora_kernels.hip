@@ -150,9 +150,9 @@ __device__ __forceinline__ void write_plan(const ShrinkArgs &x, PlanLists &l, in
 // beside.  Both operands stream through LDS (the pipeline of gemm_core.hpp):
 // loaded straight into MFMA registers, 64 bytes of a row an instruction, the
 // same product streamed its operands at less than half the rate.
-// Eight stages, one workgroup a compute unit: a split of up to eight K steps
-// has all its loads in flight at once.
-using ShapeShrink = TileShape<64, 64, 64, 2, 2, 8, 2, 8, 16>;
+// Four stages, two workgroups a compute unit: one lists its adapters or meets
+// the others while the other streams.
+using ShapeShrink = TileShape<64, 64, 64, 2, 2, 4, 2, 4, 16>;
 
 // Panel A of the pipeline: 64 of the listed adapters' rows, 8 of which, always
 // of one adapter, are one load of one wave.
@@ -307,7 +307,7 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs &x, char *smem,
     }
 }
 
-__global__ __launch_bounds__(ShapeShrink::kThreads, 1) void lora_shrink_kernel(ShrinkArgs x) {
+__global__ __launch_bounds__(ShapeShrink::kThreads, 2) void lora_shrink_kernel(ShrinkArgs x) {
     __shared__ __attribute__((aligned(16))) char smem[ShapeShrink::kLdsBytes];
     __shared__ AdapterList list;
     __shared__ unsigned word;
@@ -333,17 +333,17 @@ hipError_t launch_lora_shrink(const uint16_t *X, const LoraTable &t, const int *
     const int64_t tiles = ceil_div(M, kShrinkRows);
     const int64_t named = static_cast<int64_t>(kShrinkRows) * slots;
     const int64_t items = ceil_div((t.count < named ? t.count : named) * cols, S::BM);
-    // a split keeps at least eight K steps, and the last to arrive has its reads
-    // of the others' sums in flight in two goes
+    // a split keeps at least six K steps, and the last to
+    // arrive has its reads of the others' sums in flight in two goes
     const int64_t nk = ceil_div(K, S::BK);
-    int64_t most = nk / 8;
+    int64_t most = nk / 6;
     if (most > 16) most = 16;
     if (most < 1) most = 1;
-    // workgroups a row block: one a compute unit in all (two where that leaves
-    // them 64 K steps and more: row blocks that name one adapter more than
+    // workgroups a row block: two a compute unit in all (four where that leaves
+    // them 24 K steps and more: row blocks that name one adapter more than
     // others would else end last), and no more than there can be work for
-    int64_t G = ws.cus / tiles;
-    if (G * 64 <= nk) G = 2 * ws.cus / tiles;
+    int64_t G = 2 * ws.cus / tiles;
+    if (2 * G * 24 <= nk) G = 4 * ws.cus / tiles;
     if (G > items * most) G = items * most;
     if (G < 1) G = 1;
     if (ws.base == nullptr || ws.counters == nullptr ||

@@ -18,7 +18,11 @@
 // works on 64 / LPR rows at once: the k rounds of arg-max are instructions,
 // not memory, and bound the larger calls, so every lane has to count in them
 // (a row a wave would leave most lanes idle at E <= 64 and run the cross-lane
-// steps once a row instead of once for 64 / LPR of them).
+// steps once a row instead of once for 64 / LPR of them).  A round finds the
+// largest key, then the lowest index that has it; bf16 logits and their index
+// share one word, so that one maximum does both.  What follows from a pick
+// (its exponential, its count, its place in the outputs) is done once, pick j
+// in lane j of the row.
 #include "launch.hpp"
 
 #include "device.hpp"
@@ -26,7 +30,6 @@
 
 namespace swiglu {
 
-constexpr int kRouteThreads = 1024;
 constexpr int kRouteValues = 8;      // logits a lane
 constexpr float kNegInf = -__builtin_inff();
 
@@ -63,16 +66,15 @@ __device__ __forceinline__ float row_sum(float v) {
     if constexpr ((1 << STEP) < LPR) return row_sum<LPR, STEP + 1>(v + partner_f<STEP>(v));
     else return v;
 }
-// The larger key of the row, and of equal keys the lower index.
 template <int LPR, int STEP = 0>
-__device__ __forceinline__ void row_best(uint32_t &key, uint32_t &idx) {
-    if constexpr ((1 << STEP) < LPR) {
-        const uint32_t k = partner<STEP>(key), i = partner<STEP>(idx);
-        const bool take = k > key || (k == key && i < idx);
-        key = take ? k : key;
-        idx = take ? i : idx;
-        row_best<LPR, STEP + 1>(key, idx);
-    }
+__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
+    if constexpr ((1 << STEP) < LPR) return row_max_u32<LPR, STEP + 1>(max(v, partner<STEP>(v)));
+    else return v;
+}
+template <int LPR, int STEP = 0>
+__device__ __forceinline__ uint32_t row_min_u32(uint32_t v) {
+    if constexpr ((1 << STEP) < LPR) return row_min_u32<LPR, STEP + 1>(min(v, partner<STEP>(v)));
+    else return v;
 }
 // Unsigned keys in the order of the floats, and back.
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -157,23 +159,31 @@ struct RouteArgs {
     unsigned *counter;
 };
 
+// Sum over the lanes of a wave, in every lane.
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+    return v;
+}
+
 // The loss and the counts over all rows: workgroup b leaves its sums of p and
 // its picks in partials[b] (device-scope stores), and the last to arrive adds
 // them up in the order of b (so that the sums do not depend on which one that
-// is).
-template <bool kBf16, int LPR>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs x) {
-    constexpr int kRowsPass = kRouteThreads / LPR;
+// is).  THREADS: 1024, or 256 where those take all rows at once (7.3 -> 5 us at
+// M = 1, E = 8: the launch and three memory latencies).
+template <bool kBf16, int LPR, int THREADS>
+__global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs x) {
+    constexpr int kRowsPass = THREADS / LPR;
     constexpr int kMaxE = LPR * kRouteValues;
-    constexpr int kWaves = kRouteThreads / 64;
+    constexpr int kWaves = THREADS / 64;
     constexpr int kHeld = (kMaxRouteK + LPR - 1) / LPR;
     __shared__ unsigned hist[kMaxE + 1];
     __shared__ float psum[kWaves][kMaxE];
-    __shared__ double terms[kRouteThreads];
+    __shared__ double sums[kMaxE];   // of p over all rows
     __shared__ unsigned arrived;
     const int tid = threadIdx.x, li = tid % LPR, group = tid / LPR;
     const int e0 = li * kRouteValues;
-    for (int e = tid; e <= kMaxE; e += kRouteThreads) hist[e] = 0u;
+    for (int e = tid; e <= kMaxE; e += THREADS) hist[e] = 0u;
     __syncthreads();
 
     float mine[kRouteValues] = {};
@@ -181,60 +191,72 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs x) {
          first += static_cast<int64_t>(gridDim.x) * kRowsPass) {
         const int64_t row = first + group;
         const bool here = row < x.M;
+        const bool wanted = here && (x.valid == nullptr || x.valid[row] != 0);
         float v[kRouteValues];
         load_logits<kBf16>(x.logits, here ? row : 0, x.E, e0, x.vec != 0, v);
-        if (x.vec && e0 >= x.E) {
-#pragma unroll
-            for (int i = 0; i < kRouteValues; ++i) v[i] = kNegInf;
-        }
+        // (bf16: the key above, 0xFFFF minus the index below)
         uint32_t key[kRouteValues];
 #pragma unroll
-        for (int i = 0; i < kRouteValues; ++i) key[i] = order_key(v[i]);
+        for (int i = 0; i < kRouteValues; ++i) {
+            key[i] = order_key(v[i]);
+            if constexpr (kBf16) key[i] = (key[i] & 0xFFFF0000u) | (0xFFFFu - (e0 + i));
+        }
         float top, inv;
-        const bool live =
-            row_softmax<LPR>(v, here && (x.valid == nullptr || x.valid[row] != 0), top, inv);
+        const bool live = row_softmax<LPR>(v, wanted, top, inv);
 #pragma unroll
         for (int i = 0; i < kRouteValues; ++i) mine[i] += v[i];
         if (live && li == 0) atomicAdd(&hist[kMaxE], 1u);
 
-        int id[kHeld];
-        float w[kHeld];
-        float total = 0.0f;
+        // pick j = h LPR + li of the row
+        uint32_t picked[kHeld], at[kHeld];
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h) {
-            id[h] = -1;
-            w[h] = 0.0f;
-        }
+        for (int h = 0; h < kHeld; ++h) picked[h] = at[h] = 0u;
 #pragma nounroll
         for (int j = 0; j < x.k; ++j) {
-            uint32_t best = key[0], at = e0;
+            uint32_t best = key[0];
 #pragma unroll
-            for (int i = 1; i < kRouteValues; ++i)
-                if (key[i] > best) {
-                    best = key[i];
-                    at = e0 + i;
-                }
-            row_best<LPR>(best, at);
+            for (int i = 1; i < kRouteValues; ++i) best = max(best, key[i]);
+            best = row_max_u32<LPR>(best);
+            uint32_t index;
+            if constexpr (kBf16) {
+                index = 0xFFFFu - (best & 0xFFFFu);
 #pragma unroll
-            for (int i = 0; i < kRouteValues; ++i)
-                if (at == static_cast<uint32_t>(e0 + i)) key[i] = 0u;
-            const bool pick = live && best > kNegInfKey;
-            const float e = pick ? expf(key_value(best) - top) : 0.0f;
-            total += e;
+                for (int i = 0; i < kRouteValues; ++i) key[i] = key[i] == best ? 0u : key[i];
+            } else {
+                index = 0xFFFFu;
+#pragma unroll
+                for (int i = kRouteValues - 1; i >= 0; --i)
+                    index = key[i] == best ? static_cast<uint32_t>(e0 + i) : index;
+                index = row_min_u32<LPR>(index);
+                const uint32_t d = index - e0;
+#pragma unroll
+                for (int i = 0; i < kRouteValues; ++i) key[i] = d == static_cast<uint32_t>(i) ? 0u : key[i];
+            }
 #pragma unroll
             for (int h = 0; h < kHeld; ++h)
                 if (j == h * LPR + li) {
-                    id[h] = pick ? static_cast<int>(at) : -1;
-                    w[h] = e;
+                    picked[h] = kBf16 ? best & 0xFFFF0000u : best;
+                    at[h] = index;
                 }
-            if (pick && li == 0) atomicAdd(&hist[at], 1u);
         }
+        float w[kHeld], total = 0.0f;
+        bool pick[kHeld];
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            // (a negative logit's key ends in ones)
+            if (kBf16 && !(picked[h] >> 31)) picked[h] |= 0xFFFFu;
+            pick[h] = live && picked[h] > kNegInfKey;
+            w[h] = pick[h] ? expf(key_value(picked[h]) - top) : 0.0f;
+            total += w[h];
+            if (pick[h]) atomicAdd(&hist[at[h]], 1u);
+        }
+        total = row_sum<LPR>(total);
         const float scale = x.normalize ? (total > 0.0f ? 1.0f / total : 0.0f) : inv;
 #pragma unroll
         for (int h = 0; h < kHeld; ++h) {
             const int j = h * LPR + li;
             if (here && j < x.k) {
-                x.ids[row * x.k + j] = id[h];
+                x.ids[row * x.k + j] = pick[h] ? static_cast<int>(at[h]) : -1;
                 x.weights[row * x.k + j] = w[h] * scale;
             }
         }
@@ -250,21 +272,17 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs x) {
     __syncthreads();
     auto block_sum = [&](int e) {
         float s = 0.0f;
+#pragma unroll
         for (int w = 0; w < kWaves; ++w) s += psum[w][e];
         return s;
     };
 
-    double term = 0.0;
     if (gridDim.x == 1) {
-        for (int e = tid; e < x.E; e += kRouteThreads) {
-            x.counts[e] = static_cast<int>(hist[e]);
-            term += static_cast<double>(hist[e]) * block_sum(e);
-        }
-        if (tid == 0) x.counts[x.E] = static_cast<int>(hist[kMaxE]);
+        for (int e = tid; e < x.E; e += THREADS) sums[e] = block_sum(e);
     } else {
         const int width = x.E + 1;
         uint64_t *own = x.partials + static_cast<int64_t>(blockIdx.x) * width;
-        for (int e = tid; e < width; e += kRouteThreads) {
+        for (int e = tid; e < width; e += THREADS) {
             const uint64_t c = e < x.E ? hist[e] : hist[kMaxE];
             const uint32_t s = e < x.E ? __builtin_bit_cast(uint32_t, block_sum(e)) : 0u;
             __hip_atomic_store(own + e, (static_cast<uint64_t>(s) << 32) | c, __ATOMIC_RELAXED,
@@ -279,59 +297,59 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs x) {
         if (arrived + 1 != gridDim.x) return;
         if (tid == 0)
             __hip_atomic_store(x.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        // `parts` threads an expert, each its own run of workgroups
-        constexpr int kParts = kRouteThreads / (2 * kMaxE) > 0 ? kRouteThreads / (2 * kMaxE) : 1;
-        __shared__ double part_p[kParts][kMaxE + 1];
-        __shared__ unsigned part_c[kParts][kMaxE + 1];
+        // as many threads an expert as there are, each its own run of workgroups
+        __shared__ double part_p[THREADS];
+        __shared__ unsigned part_c[THREADS];
+        static_assert(THREADS > kMaxRouteE || THREADS == 256, "256: one workgroup");
+        const int parts = min(32, THREADS / width);
+        constexpr int kBatch = 20;
         const int G = gridDim.x;
-        for (int i = tid; i < kParts * width; i += kRouteThreads) {
-            const int part = i / width, e = i % width;
-            const int b0 = part * G / kParts, b1 = (part + 1) * G / kParts;
+        if (tid < parts * width) {
+            const int part = tid / width, e = tid - part * width;
+            const int b0 = part * G / parts, b1 = (part + 1) * G / parts;
             double s = 0.0;
             unsigned c = 0;
-#pragma unroll 16
-            for (int b = b0; b < b1; ++b) {
-                const uint64_t q = __hip_atomic_load(x.partials + static_cast<int64_t>(b) * width + e,
-                                                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                s += __builtin_bit_cast(float, static_cast<uint32_t>(q >> 32));
-                c += static_cast<uint32_t>(q);
+            for (int b = b0; b < b1; b += kBatch) {   // kBatch loads in flight
+                uint64_t q[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    q[i] = b + i < b1 ? __hip_atomic_load(x.partials + static_cast<int64_t>(b + i) * width + e,
+                                                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                                      : 0u;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    s += __builtin_bit_cast(float, static_cast<uint32_t>(q[i] >> 32));
+                    c += static_cast<uint32_t>(q[i]);
+                }
             }
-            part_p[part][e] = s;
-            part_c[part][e] = c;
+            part_p[tid] = s;
+            part_c[tid] = c;
         }
         __syncthreads();
-        for (int e = tid; e < width; e += kRouteThreads) {
+        for (int e = tid; e < width; e += THREADS) {
             double s = 0.0;
             unsigned c = 0;
-            for (int p = 0; p < kParts; ++p) {
-                s += part_p[p][e];
-                c += part_c[p][e];
+            for (int p = 0; p < parts; ++p) {
+                s += part_p[p * width + e];
+                c += part_c[p * width + e];
             }
-            x.counts[e] = static_cast<int>(c);
-            if (e < x.E) term += s * c;
+            if (e < x.E) sums[e] = s;
             hist[e < x.E ? e : kMaxE] = c;
         }
     }
-    // sum of the terms and the total of the picks, over the threads in a tree
-    terms[tid] = term;
     __syncthreads();
-    for (int d = kRouteThreads / 2; d > 0; d /= 2) {
-        if (tid < d) terms[tid] += terms[tid + d];
-        __syncthreads();
-    }
-    const double sum = terms[0];
-    __syncthreads();
-    double picks = 0.0;
-    for (int e = tid; e < x.E; e += kRouteThreads) picks += hist[e];
-    terms[tid] = picks;
-    __syncthreads();
-    for (int d = kRouteThreads / 2; d > 0; d /= 2) {
-        if (tid < d) terms[tid] += terms[tid + d];
-        __syncthreads();
-    }
-    if (tid == 0) {
-        const double C = terms[0], n = hist[kMaxE];
-        *x.loss = static_cast<float>(C > 0.0 ? x.E * sum / (C * n) : 0.0);
+    for (int e = tid; e <= x.E; e += THREADS)
+        x.counts[e] = static_cast<int>(hist[e < x.E ? e : kMaxE]);
+    if (tid < 64) {
+        double term = 0.0, picks = 0.0;
+        for (int e = tid; e < x.E; e += 64) {
+            term += hist[e] * sums[e];
+            picks += hist[e];
+        }
+        term = wave_sum(term);
+        picks = wave_sum(picks);
+        const double n = hist[kMaxE];
+        if (tid == 0) *x.loss = static_cast<float>(picks > 0.0 ? x.E * term / (picks * n) : 0.0);
     }
 }
 
@@ -354,6 +372,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs x
     constexpr int kThreads = 256, kRowsPass = kThreads / LPR;
     constexpr int kHeld = (kMaxRouteK + LPR - 1) / LPR;
     __shared__ int total_picks;
+    __shared__ __attribute__((aligned(16))) float shares_[kThreads * kRouteValues];
+    SWIGLU_LDS float *shares = (SWIGLU_LDS float *)shares_;
     const int tid = threadIdx.x, li = tid % LPR, group = tid / LPR;
     const int e0 = li * kRouteValues;
     if (tid == 0) total_picks = 0;
@@ -377,10 +397,6 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs x
         const int64_t at = here ? row : 0;
         float p[kRouteValues];
         load_logits<kBf16>(x.logits, at, x.E, e0, x.vec != 0, p);
-        if (x.vec && e0 >= x.E) {
-#pragma unroll
-            for (int i = 0; i < kRouteValues; ++i) p[i] = kNegInf;
-        }
         // pick j = h LPR + li of the row
         int id[kHeld];
         float w[kHeld], dw[kHeld];
@@ -390,6 +406,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs x
             const int j = h * LPR + li;
             const bool held = j < x.k;
             id[h] = held ? x.ids[at * x.k + j] : -1;
+            if (id[h] >= x.E) id[h] = -1;   // (the caller's: not to write past the row)
             w[h] = held && id[h] >= 0 ? x.weights[at * x.k + j] : 0.0f;
             dw[h] = held && id[h] >= 0 && x.d_weights ? x.d_weights[at * x.k + j] : 0.0f;
             wdw += w[h] * dw[h];
@@ -402,21 +419,20 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs x
 #pragma unroll
             for (int h = 0; h < kHeld; ++h) dw[h] = w[h] * (dw[h] - wdw);
         }
-        // each pick's share, at its expert
-        float share[kRouteValues] = {};
+        // each pick's share, at its expert: through the row's own LDS (a wave's LDS
+        // accesses are in order, and its rows are its own)
+        SWIGLU_LDS float *row_shares = shares + (group * LPR + li) * kRouteValues;
+        *reinterpret_cast<SWIGLU_LDS f32x4 *>(row_shares) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        *reinterpret_cast<SWIGLU_LDS f32x4 *>(row_shares + 4) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int h = 0; h < kHeld; ++h) {
-            const int held = min(LPR, x.k - h * LPR);
-#pragma nounroll
-            for (int j = 0; j < held; ++j) {
-                const int from = (tid & 63) / LPR * LPR + j;
-                const int e = __shfl(id[h], from);
-                const float d = __shfl(dw[h], from);
+        for (int h = 0; h < kHeld; ++h)
+            if (id[h] >= 0) shares[group * LPR * kRouteValues + id[h]] = dw[h];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        float share[kRouteValues];
 #pragma unroll
-                for (int i = 0; i < kRouteValues; ++i)
-                    if (e == e0 + i) share[i] += d;
-            }
-        }
+        for (int i = 0; i < kRouteValues; ++i) share[i] = row_shares[i];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < kRouteValues; ++i)
@@ -461,10 +477,11 @@ static int lanes_per_row(int64_t E) {
     return lpr;
 }
 
-// Workgroups of the forward kernel: one per pass of rows, at most one a
-// compute unit.
+// Threads of the forward kernel, and its workgroups: one per pass of rows, at
+// most one a compute unit.
+static int route_threads(int64_t M, int64_t E) { return M * lanes_per_row(E) <= 256 ? 256 : 1024; }
 static int route_grid(int64_t M, int64_t E, int cus) {
-    const int64_t per = kRouteThreads / lanes_per_row(E);
+    const int64_t per = route_threads(M, E) / lanes_per_row(E);
     const int64_t passes = (M + per - 1) / per;
     return static_cast<int>(passes < cus ? passes : cus);
 }
@@ -474,15 +491,15 @@ uint64_t route_partials_bytes(int64_t M, int64_t E, int cus) {
     return grid > 1 ? static_cast<uint64_t>(grid) * (E + 1) * 8 : 0;
 }
 
-template <bool kBf16>
+template <bool kBf16, int THREADS>
 static void run_route(int lpr, int grid, const RouteArgs &a, hipStream_t stream) {
-    const dim3 g(grid), t(kRouteThreads);
+    const dim3 g(grid), t(THREADS);
     switch (lpr) {
-        case 4: hipLaunchKernelGGL((route_kernel<kBf16, 4>), g, t, 0, stream, a); break;
-        case 8: hipLaunchKernelGGL((route_kernel<kBf16, 8>), g, t, 0, stream, a); break;
-        case 16: hipLaunchKernelGGL((route_kernel<kBf16, 16>), g, t, 0, stream, a); break;
-        case 32: hipLaunchKernelGGL((route_kernel<kBf16, 32>), g, t, 0, stream, a); break;
-        default: hipLaunchKernelGGL((route_kernel<kBf16, 64>), g, t, 0, stream, a); break;
+        case 4: hipLaunchKernelGGL((route_kernel<kBf16, 4, THREADS>), g, t, 0, stream, a); break;
+        case 8: hipLaunchKernelGGL((route_kernel<kBf16, 8, THREADS>), g, t, 0, stream, a); break;
+        case 16: hipLaunchKernelGGL((route_kernel<kBf16, 16, THREADS>), g, t, 0, stream, a); break;
+        case 32: hipLaunchKernelGGL((route_kernel<kBf16, 32, THREADS>), g, t, 0, stream, a); break;
+        default: hipLaunchKernelGGL((route_kernel<kBf16, 64, THREADS>), g, t, 0, stream, a); break;
     }
 }
 template <bool kBf16>
@@ -514,8 +531,14 @@ hipError_t launch_route(const void *logits, bool bf16, const uint8_t *valid, int
     const RouteArgs a{logits, valid, ids, weights, counts, loss, M, E, k, normalize ? 1 : 0,
                       vector_rows(E, logits, nullptr) ? 1 : 0, static_cast<uint64_t *>(partials),
                       counter};
-    if (bf16) run_route<true>(lanes_per_row(E), grid, a, stream);
-    else run_route<false>(lanes_per_row(E), grid, a, stream);
+    const int lpr = lanes_per_row(E);
+    if (route_threads(M, E) == 256) {
+        if (bf16) run_route<true, 256>(lpr, grid, a, stream);
+        else run_route<false, 256>(lpr, grid, a, stream);
+    } else {
+        if (bf16) run_route<true, 1024>(lpr, grid, a, stream);
+        else run_route<false, 1024>(lpr, grid, a, stream);
+    }
     return hipGetLastError();
 }
 

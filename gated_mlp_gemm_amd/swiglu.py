@@ -463,6 +463,7 @@ def swiglu_fused_gemm_fp8(A8: torch.Tensor, W_fused8: torch.Tensor, a_exp: int, 
 # router
 # ---------------------------------------------------------------------------
 _LOGITS_TYPES = {torch.float32: SWIGLU_F32, torch.bfloat16: SWIGLU_BF16}
+_ROUTE_ROWS = 4   # so many rows are one workgroup's whatever E is: no scratch
 
 
 def _dev_typed(t: torch.Tensor, name: str, dtype, shape) -> torch.Tensor:
@@ -520,22 +521,31 @@ def swiglu_route(logits: torch.Tensor, k: int, valid: Optional[torch.Tensor] = N
             valid = valid.view(torch.uint8)
         _dev_typed(valid, "valid", torch.uint8, (M,))
     rows = (M, max(k, 0))
-    ids = torch.empty(rows, dtype=torch.int32, device=dev) if ids is None else ids
-    weights = torch.empty(rows, dtype=torch.float32, device=dev) if weights is None else weights
-    counts = torch.empty(E + 1, dtype=torch.int32, device=dev) if counts is None else counts
-    loss = torch.empty((), dtype=torch.float32, device=dev) if loss is None else loss
-    _dev_typed(ids, "ids", torch.int32, rows)
-    _dev_typed(weights, "weights", torch.float32, rows)
-    _dev_typed(counts, "counts", torch.int32, (E + 1,))
-    _dev_typed(loss, "loss", torch.float32, ())
+    # (what is allocated here needs no check: host time counts in a small call)
+    if ids is None:
+        ids = torch.empty(rows, dtype=torch.int32, device=dev)
+    else:
+        _dev_typed(ids, "ids", torch.int32, rows)
+    if weights is None:
+        weights = torch.empty(rows, dtype=torch.float32, device=dev)
+    else:
+        _dev_typed(weights, "weights", torch.float32, rows)
+    if counts is None:
+        counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+    else:
+        _dev_typed(counts, "counts", torch.int32, (E + 1,))
+    if loss is None:
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+    else:
+        _dev_typed(loss, "loss", torch.float32, ())
     with _on_device(dev):
-        if workspace is None:
+        if workspace is None and M > _ROUTE_ROWS:
             n = swiglu_route_workspace_size(M, E)
             workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
         ws, wsb = _ws(workspace)
-        _check(lib.swiglu_route(_ptr(logits), kind, _ptr(valid), _ptr(ids), _ptr(weights),
-                                _ptr(counts), _ptr(loss), M, E, k, int(bool(normalize)), ws, wsb,
-                                _stream(dev)), "swiglu_route")
+        _check(lib.swiglu_route(logits.data_ptr(), kind, _ptr(valid), ids.data_ptr(),
+                                weights.data_ptr(), counts.data_ptr(), loss.data_ptr(), M, E, k,
+                                1 if normalize else 0, ws, wsb, _stream(dev)), "swiglu_route")
     return ids, weights, counts, loss
 
 
@@ -567,7 +577,8 @@ def swiglu_route_backward(logits: torch.Tensor, ids: torch.Tensor, weights: torc
         _dev_typed(d_loss, "d_loss", torch.float32, ())
     if d_logits is None:
         d_logits = torch.empty_like(logits)
-    _dev_typed(d_logits, "d_logits", logits.dtype, (M, E))
+    else:
+        _dev_typed(d_logits, "d_logits", logits.dtype, (M, E))
     with _on_device(logits.device):
         _check(lib.swiglu_route_backward(_ptr(logits), kind, _ptr(valid), _ptr(ids), _ptr(weights),
                                          _ptr(counts), _ptr(d_weights), _ptr(d_loss),
@@ -650,7 +661,8 @@ def swiglu_fused_gemm_lora(A: torch.Tensor, W_fused: torch.Tensor, lora: SwigluL
     table = lora._beside("lora", 2, 2 * N, K)
     if Y is None:
         Y = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
-    _dev_tensor(Y, "Y", (M, N))
+    else:
+        _dev_tensor(Y, "Y", (M, N))
     with _on_device(A.device):
         if workspace is None:
             workspace = make_lora_workspace(M, N, K, J, lora.rank, A.device)
