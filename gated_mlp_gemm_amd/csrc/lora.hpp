@@ -41,10 +41,11 @@ constexpr int kPlanRows = 256;
 constexpr int kPlanWhere = 16;                            // byte offsets in a plan
 constexpr int kPlanIds = kPlanWhere + 4 * kPlanRows * 4;
 
-// How an expansion walks T: `slots` slots and 8 rank8 elements of each part's
-// rank at a time, as much as fits its LDS.
+// How an expansion walks T: `slots` slots and 8 << shift elements of each part's
+// rank at a time, as much as fits its LDS.  (A power of two: with any count the
+// quotients by it were a third of the instructions of a step.)
 struct LoraChunks {
-    int slots, rank8;
+    int slots, shift;
 };
 struct LoraTerm {
     const uint16_t *T;   // [M][slots][parts * rank / 8][2][8]: rounded, then the rest
@@ -115,7 +116,7 @@ __device__ __forceinline__ void gdma16(const uint16_t *p, SWIGLU_LDS char *lds) 
 // Expand into the accumulators of an S tile at (m0, n0) (16x16 MFMAs; the
 // accumulators are settled before and after, the tile's LDS is idle).
 //
-// K runs over the adapters of the tile's plan, rank8 chunks of 8 elements each,
+// K runs over the adapters of the tile's plan, 1 << shift chunks of 8 elements each,
 // 32 k a step.  LDS holds T of the tile's rows (only the slots that there are;
 // a lane whose row does not name the adapter of its 8 k reads zeros from beside
 // it) and a ring of B's rows, kSteps steps a stage, both loaded straight to
@@ -152,13 +153,15 @@ struct LoraExpand {
     static constexpr int kPlanes = (kRing - kT) / kPlane;
     static_assert(kPlanes >= kParts, "T fits");
 
-    static constexpr int planes(int rank8) { return (rank8 + 1) / 2; }   // of a slot's part
+    static constexpr int planes(int shift) { return shift > 1 ? 1 << (shift - 1) : 1; }   // of a slot's part
+    // All slots and the whole rank (rounded up to a power of two) if they fit,
+    // else as much of the rank as does, else one plane and as many slots as do.
     static LoraChunks chunks(int slots, int rank) {
-        const int rank8 = rank / 8, most = kPlanes / kParts;
-        if (slots > most) return {most, rank8 < 2 ? rank8 : 2};
-        const int r = most / slots * 2 < rank8 ? most / slots * 2 : rank8;
-        const int n = (rank8 + r - 1) / r;   // as even as they can be
-        return {slots, (rank8 + n - 1) / n};
+        const int most = kPlanes / kParts;
+        int shift = 0;
+        while ((8 << shift) < rank) ++shift;
+        while (shift > 1 && planes(shift) * slots > most) --shift;
+        return {slots < most ? slots : most, shift};
     }
 
     int n;                 // adapters of the plan
@@ -183,11 +186,11 @@ struct LoraExpand {
         // (uniform: a scalar load)
         n = *reinterpret_cast<const __attribute__((address_space(4))) int *>(
             reinterpret_cast<uintptr_t>(plan));
-        const Divisor rank8(kQuarter ? x.quarter.rank8 : x.whole.rank8);
+        const int shift = kQuarter ? x.quarter.shift : x.whole.shift;
         const uint16_t *ids = reinterpret_cast<const uint16_t *>(plan + kPlanIds);
 #pragma unroll
         for (int s = 0; s < kEarly; ++s)
-            id[s] = n > 0 ? ids[min(rank8.quotient(4 * s + b_chunk(tid)), n - 1)] : 0u;
+            id[s] = n > 0 ? ids[min((4 * s + b_chunk(tid)) >> shift, n - 1)] : 0u;
     }
 
     // after MFMA i of 4 kRows S::TN: hook(i)
@@ -243,9 +246,8 @@ struct LoraExpand {
             col[j] = static_cast<uint32_t>(min(n0 + (kGated ? pair_row(r) : r), x.cols - 1)) * x.rank;
         }
         const int64_t b_adapter = static_cast<int64_t>(x.cols) * x.rank;
-        const Divisor by_rank8(by.rank8);
-        const int planes_part = planes(by.rank8);
-        const int steps = (n * by.rank8 + 3) / 4;
+        const int planes_part = planes(by.shift), mask = (1 << by.shift) - 1;
+        const int steps = ((n << by.shift) + 3) / 4;
 
         const int row0 = wm * S::kWaveM + r16;   // the lane's row of T in row block 0
         // row blocks whose T is in registers at once, one such group ahead
@@ -258,7 +260,7 @@ struct LoraExpand {
 #pragma nounroll
         for (int j0 = 0; j0 < x.slots; j0 += by.slots)
 #pragma nounroll
-            for (int r0 = 0; r0 < rank8; r0 += by.rank8) {
+            for (int r0 = 0; r0 < rank8; r0 += mask + 1) {
                 // T: a wave a quarter of the rows, 16 rows of a plane a load.  (Past the
                 // last slot: past the row, or zeros; never read.)
                 {
@@ -282,7 +284,7 @@ struct LoraExpand {
                 auto issue_b = [&](int s, uint32_t of) {
                     const int e = 4 * s + b_chunk(tid);
                     // past the end: something there is, multiplied with zeros
-                    const int element = min(r0 + e - by_rank8.quotient(e) * by.rank8, rank8 - 1);
+                    const int element = min(r0 + (e & mask), rank8 - 1);
                     const uint16_t *p = x.B + (of * b_adapter + 8 * element);
                     SWIGLU_LDS char *to =
                         lds + kRing + (s % (kStages * kSteps)) * kStepBytes + wave * 1024;
@@ -295,7 +297,7 @@ struct LoraExpand {
                     for (int q = 0; q < kSteps; ++q)
                         of[q] = asm_read_u16(
                             at + kIds +
-                            min(by_rank8.quotient(4 * (stage * kSteps + q) + b_chunk(tid)), n - 1) * 2);
+                            min((4 * (stage * kSteps + q) + b_chunk(tid)) >> by.shift, n - 1) * 2);
 #pragma unroll
                     for (int q = 0; q < kSteps; ++q) issue_b(stage * kSteps + q, landed(of[q]));
                 };
@@ -323,7 +325,7 @@ struct LoraExpand {
                 };
                 auto look_at = [&](int s, int pair) {
                     const int e = 4 * s + g;
-                    const int i = by_rank8.quotient(e), k = e - i * by.rank8;
+                    const int i = e >> by.shift, k = e & mask;
                     const uint32_t key = r0 + k < rank8 ? i + 1 : 0xFFFFu;   // (no index is that far)
                     Look l;
                     l.key[0] = 2 * pair >= j0 ? key : 0xFFFFu;

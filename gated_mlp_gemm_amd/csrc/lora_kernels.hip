@@ -333,10 +333,10 @@ hipError_t launch_lora_shrink(const uint16_t *X, const LoraTable &t, const int *
     const int64_t tiles = ceil_div(M, kShrinkRows);
     const int64_t named = static_cast<int64_t>(kShrinkRows) * slots;
     const int64_t items = ceil_div((t.count < named ? t.count : named) * cols, S::BM);
-    // a split keeps at least six K steps, and the last to
-    // arrive has its reads of the others' sums in flight in two goes
+    // a split keeps at least six K steps (meeting costs as much as ten), and the
+    // last to arrive has its reads of the others' sums in flight in two goes
     const int64_t nk = ceil_div(K, S::BK);
-    int64_t most = nk / 6;
+    int64_t most = nk <= 16 ? 1 : nk / 6;
     if (most > 16) most = 16;
     if (most < 1) most = 1;
     // workgroups a row block: two a compute unit in all (four where that leaves
