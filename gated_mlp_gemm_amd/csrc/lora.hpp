@@ -123,11 +123,13 @@ __device__ __forceinline__ void gdma16(const uint16_t *p, SWIGLU_LDS char *lds) 
 // LDS; so every byte is read once a tile.  Both lie in planes of 64 bytes a
 // row, the 16-byte chunks swizzled by the row (16 rows on 16 different banks).
 // One wave a SIMD issues an instruction about every 6 clocks, so what bounds
-// this is the instructions around the MFMAs, not bytes: the addresses and LDS
-// reads of a group of row blocks stand between the MFMAs of the group before.
-// (256 x 256 tile, Gate and Up, 2 slots of rank 16: 4500 clocks a step with
-// addresses and MFMAs one after the other, of which the MFMAs are 2048, and
-// 5100 before the first with rows of T of any length in LDS.)  The first
+// the steps is the instructions around the MFMAs, not bytes: the addresses and
+// LDS reads of a group of row blocks stand between the MFMAs of the group
+// before.  256 x 256 tile, Gate and Up, 2 slots of rank 16, in clocks: T's 64
+// KiB 3400 (what a compute unit takes in), B and the wait 1600, a step 3300, of
+// which the MFMAs are 2048 (4500 with addresses and MFMAs one after the other).
+// Loaded by each wave straight into its MFMA operands, T and B took as long as
+// that: 16-byte pieces of many cache lines, each row by two waves.  The first
 // stages' adapters are looked up before the tile's K steps (begin).
 template <class S, bool kGated, bool kQuarter>
 struct LoraExpand {

@@ -144,12 +144,18 @@ __device__ __forceinline__ void write_plan(const ShrinkArgs &x, PlanLists &l, in
 // split K where there are fewer items than workgroups (their sums meet in the
 // workspace as in split_tail.hpp: device-scope stores and an arrival count, the
 // last to arrive adds them up in order, nobody waits).  Every row of X is
-// multiplied with every adapter listed: T takes the ones that it names.  Bound
-// by the bytes of X and A, and where those are few by the latency of a handful
-// of dependent memory accesses; the products that no row takes cost nothing
-// beside.  Both operands stream through LDS (the pipeline of gemm_core.hpp):
-// loaded straight into MFMA registers, 64 bytes of a row an instruction, the
-// same product streamed its operands at less than half the rate.
+// multiplied with every adapter listed: T takes the ones that it names (the
+// products that no row takes cost nothing beside the loads).  Both operands
+// stream through LDS (the pipeline of gemm_core.hpp); loaded straight into MFMA
+// registers, 64 bytes of a row an instruction, they streamed at half the rate.
+//
+// What bounds it: where rows are many, the bytes of X and A (M=8192 K=13824,
+// one adapter of rank 64: 57 us, X at 4.0 TB/s).  Where they are few, what one
+// compute unit takes in, about 26 bytes a clock, and a chain of dependent
+// accesses; M=33 K=8960, 16 adapters of rank 8, in clocks: the list 2100, the
+// first loads 4700, nine K steps 6100, the store and the arrival 2400, the 15
+// others' sums 7900, T 1200 (11.6 us with the launch).  Eight stages instead of
+// four, or half the splits, moved that by less than 5 %.
 // Four stages, two workgroups a compute unit: one lists its adapters or meets
 // the others while the other streams.
 using ShapeShrink = TileShape<64, 64, 64, 2, 2, 4, 2, 4, 16>;
