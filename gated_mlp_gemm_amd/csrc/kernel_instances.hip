@@ -120,6 +120,11 @@ template struct TilesLaunch<ShapeQuad, StoreLora, kTailSplit>;
 template struct TilesLaunch<ShapeSplitK, PairMulLora, kTailReduceInKernel>;
 template struct TilesLaunch<ShapeSmallLora, PairMulLora, kTailSplit>;
 template struct TilesLaunch<ShapeSmallLora, StoreLora, kTailSplit>;
+#elif SWIGLU_INSTANCE == 22
+template struct TilesLaunch<ShapeThinLora, PairMulLora, kTailSplit>;
+template struct TilesLaunch<ShapeThinLora, StoreLora, kTailSplit>;
+template struct ReduceLaunch<ShapeThinLora, PairMulEpilogue>;
+template struct ReduceLaunch<ShapeThinLora, StoreEpilogue>;
 template struct ReduceLaunch<ShapeSmallLora, PairMulEpilogue>;
 template struct ReduceLaunch<ShapeSmallLora, StoreEpilogue>;
 #else

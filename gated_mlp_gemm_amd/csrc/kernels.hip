@@ -630,6 +630,8 @@ static hipError_t launch_lora_gemm(const KMajor &A, KMajor B, int M, int cols, i
 template <class Epi, class Base>
 static hipError_t launch_lora(const KMajor &A, const KMajor &B, int M, int cols, int K, Epi epi,
                               const GemmWorkspace &ws, hipStream_t stream) {
+    if (M <= ShapeThinLora::BM && cdiv(cols, ShapeThinLora::BN) >= ws.cus)
+        return launch_lora_gemm<ShapeThinLora, Epi, Base>(A, B, M, cols, K, epi, ws, stream);
     if (M <= 128) {
         if constexpr (std::is_same<Epi, PairMulLora>::value) {
             const Schedule fx = make_fixup_schedule<ShapeSplitK>(M, cols, K, ws);

@@ -142,10 +142,10 @@ struct LoraExpand {
     static constexpr int kZeros = kIds + kPlanRows * kMaxLoraSlots * 2;
     static constexpr int kRowBlocks = S::kWaveM / 16;
     static constexpr int kT = kZeros + kRowBlocks * 1024;   // (a wave's rows, 64 bytes each)
-    // a stage of few columns takes four steps: its barrier and its latency are
-    // most of its time
-    static constexpr int kSteps = S::BN <= 64 ? 4 : 1;
-    static constexpr int kStages = S::BN <= 64 ? 3 : S::kLdsBytes > 65536 && S::BN <= 128 ? 4 : 2;
+    // a stage of a small tile takes several steps: its barrier and its latency
+    // are most of its time
+    static constexpr int kSteps = S::BN <= 64 ? 4 : S::BM <= 64 ? 2 : 1;
+    static constexpr int kStages = kSteps > 1 ? 3 : S::kLdsBytes > 65536 && S::BN <= 128 ? 4 : 2;
     static constexpr int kStepBytes = S::BN * 64;
     static constexpr int kRing = S::kLdsBytes - kStages * kSteps * kStepBytes;
     static constexpr int kDma = kStepBytes / 4096;   // loads a wave and step

@@ -931,6 +931,14 @@ using ShapeSmall = TileShape<128, 64, 64, 2, 2, 4>;
 // 16x16x32 MFMAs, and waves of 32 rows by all 64 columns, so that Gate and Up
 // are blocks of their own.
 using ShapeSmallLora = TileShape<128, 64, 64, 4, 1, 4, 2, 4, 16>;
+// ... and of at most 64 rows: twice the columns, so that all four waves have
+// rows, and the expansion's steps, bound by a wave's instructions, are half as
+// many a column.  M=64 K=3584 N=18944: 84 against 99 us with 28 adapters of rank
+// 16 named, 61 against 70 with none (three stages, two workgroups a compute
+// unit: 90 and 72; six stages: as four).  Where it leaves compute units without
+// a tile the smaller one is faster (M=33 K=8960, 1536 columns: 27.4 against
+// 29.5 us).
+using ShapeThinLora = TileShape<64, 128, 64, 2, 2, 4, 2, 4, 16>;
 // Variant I on FP8 operands: the same three shapes with K steps of 128 FP8
 // values, so every tile row of a stage is 128 bytes and the LDS rings, load
 // counts and swizzles are those of the bf16 shapes (the 256x256 one with a

@@ -364,3 +364,27 @@ def test_graph_and_side_stream(dev, M):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, static))
+
+
+@pytest.mark.parametrize("kind,M,K,N,L,r,J,pattern", [
+    ("gated", 5, 72, 16400, 3, 16, 1, "mixed"), ("gated", 64, 128, 16392, 20, 8, 2, "mixed"),
+    ("down", 33, 200, 32776, 6, 24, 1, "mixed"), ("down", 64, 64, 32800, 4, 256, 8, "mixed"),
+    ("gated", 40, 64, 16384, 5, 136, 3, "twice"), ("down", 1, 8, 40000, 2, 8, 1, "mixed")])
+def test_few_rows_of_a_wide_weight(dev, kind, M, K, N, L, r, J, pattern):
+    """A tile for every compute unit: the 64-row tiles."""
+    check(dev, kind, M, K, N, L, r, J, pattern, J > 1, seed=M + K + r)
+
+
+@pytest.mark.parametrize("tile,tail,M,K,N,r,J", [
+    ("256", "fixup", 100, 520, 1400, 16, 2), ("256", "fixup", 7, 1024, 264, 64, 1),
+    ("256", "fixup", 128, 600, 4600, 24, 4), ("128", "split", 100, 520, 1400, 16, 2),
+    ("128", "whole", 128, 320, 9000, 64, 8), ("256", "split", 90, 1024, 1400, 256, 1)])
+def test_every_schedule_of_few_rows(dev, tile, tail, M, K, N, r, J, monkeypatch):
+    monkeypatch.setenv("SWIGLU_I_TILE", tile)
+    monkeypatch.setenv("SWIGLU_TAIL", tail)
+    check(dev, "gated", M, K, N, 6, r, J, "mixed", True, seed=3)
+    check(dev, "down", M, K, N, 6, r, J, "mixed", True, seed=4)
+
+
+def test_reduced_in_the_kernel_by_its_own_choice(dev):
+    check(dev, "gated", 100, 3584, 4864, 8, 16, 1, "mixed", False, seed=5)
