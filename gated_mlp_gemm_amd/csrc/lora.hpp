@@ -195,9 +195,11 @@ struct LoraExpand {
             id[s] = n > 0 ? ids[min((4 * s + b_chunk(tid)) >> shift, n - 1)] : 0u;
     }
 
-    // after MFMA i of 4 kRows S::TN: hook(i)
+    // after MFMA i of 4 kRows S::TN: hook(i); with the first row block, zeros times B
+    // onto `met`
     template <int kRows, class Hook>
-    __device__ __forceinline__ static void multiply(typename S::Acc (&acc)[S::TM][S::TN], int rb0,
+    __device__ __forceinline__ static void multiply(typename S::Acc (&acc)[S::TM][S::TN], f32x4 &met,
+                                                    const u32x4 &nothing, int rb0,
                                                     const u32x4 (&tf)[kRows][kParts][2],
                                                     const u32x4 (&bf)[S::TN][2], const Hook &hook) {
         asm volatile("s_nop 1");
@@ -212,13 +214,18 @@ struct LoraExpand {
                         const int rb = rb0 + t;
                         mfma_16x16x32_acc(acc[rb / 2][c].v[2 * (rb % 2) + h],
                                           tf[t][kGated ? c % 2 : 0][rest], bf[c][h]);
+                        if (rb == 0 && rest == 0)
+                            asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0"
+                                         : "+v"(met)
+                                         : "v"(nothing), "v"(bf[c][h]));
                         hook(((rest * kRows + t) * S::TN + c) * 2 + h);
                     }
     }
 
-    __device__ __forceinline__ void run(SWIGLU_LDS char *lds, const LoraTerm &x,
+    // Whether the wave's columns met an infinity or NaN in B (then mend()).
+    __device__ __forceinline__ bool run(SWIGLU_LDS char *lds, const LoraTerm &x,
                                         typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0) const {
-        if (n == 0) return;
+        if (n == 0) return false;
         const int tid = thread(), lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / S::WN, wn = wave % S::WN;
@@ -257,6 +264,10 @@ struct LoraExpand {
         constexpr int kGroups = kRowBlocks / kRows;
         const uint32_t t_row = at + kT + row0 * 64u;
         const uint32_t t_part = static_cast<uint32_t>(planes_part * kPlane);
+        // (in vector registers: the accumulators may hold all others)
+        f32x4 met = {0.0f, 0.0f, 0.0f, 0.0f};
+        u32x4 nothing = {0u, 0u, 0u, 0u};
+        asm volatile("" : "+v"(nothing), "+v"(met));
         const uint32_t b_read = at + kRing + (wn * S::kWaveN + r16) * 64u + ((g ^ swizzle(r16)) * 16u);
 
 #pragma nounroll
@@ -410,7 +421,7 @@ struct LoraExpand {
                         // between the MFMAs: T of the next group, B of the next step
                         constexpr int kB = 2 * S::TN;
                         constexpr int all = kRows + (next ? kB : 0);
-                        multiply<kRows>(acc, group * kRows, tf[(first + group) % 2], bf[buf], [&](int i) {
+                        multiply<kRows>(acc, met, nothing, group * kRows, tf[(first + group) % 2], bf[buf], [&](int i) {
 #pragma unroll
                             for (int w = 0; w < kB + kRows; ++w) {
                                 if (w >= all || w * kMfma / all != i) continue;
@@ -444,6 +455,75 @@ struct LoraExpand {
             for (int c = 0; c < S::TN; ++c)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) asm volatile("" : "+a"(acc[a][c].v[q]));
+        asm volatile("" : "+v"(met));
+        // (all rows of zeros: one tells of its column)
+        return __builtin_amdgcn_ballot_w64(met[0] != met[0]) != 0;
+    }
+
+    // The NaN among the wave's results again, from the formula: K elements [k0, k1) of the
+    // shared product, then the row's own adapters.  (A lane an element, from memory: for
+    // adapters that are broken, so that they break no row but their own.)
+    __device__ __forceinline__ static void mend(const LoraTerm &x, const KMajor &X, const KMajor &W,
+                                                int K, int k0, int k1,
+                                                typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0) {
+        constexpr int kQuads = S::TM * S::TN * 4;
+        const int tid = thread(), lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int wm = wave / S::WN, wn = wave % S::WN;
+        const char *plan = x.plans + static_cast<int64_t>(m0 / kPlanRows) * x.plan_bytes;
+        const uint32_t *where = reinterpret_cast<const uint32_t *>(plan + kPlanWhere);
+        const uint16_t *ids = reinterpret_cast<const uint16_t *>(plan + kPlanIds);
+        auto value = [](uint16_t v) {
+            return __builtin_bit_cast(float, static_cast<uint32_t>(v) << 16);
+        };
+#pragma nounroll
+        for (int i = 0; i < kQuads; ++i) {
+            const int block = i / 4 % S::TN;
+            const int pc = wn * S::kWaveN + block * 32 + (i & 1) * 16 + (lane & 15);
+            const int col = n0 + (kGated ? pair_row(pc) : pc);
+            int row = m0 + wm * S::kWaveM + i / (4 * S::TN) * 32 + (i >> 1 & 1) * 16 + (lane >> 4) * 4;
+            f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q)
+                if (q == i) {
+                    v = acc[q / (4 * S::TN)][q / 4 % S::TN].v[q % 4];
+                    asm volatile("" : "+v"(v));
+                }
+#pragma nounroll
+            for (int e = 0; e < 4; ++e, ++row) {
+                float sum = v[0];
+                if (sum != sum && row < x.M && col < x.cols) {
+                    const uint16_t *xr = static_cast<const uint16_t *>(X.base) +
+                                         (static_cast<int64_t>(row) * X.stride + X.offset) * (X.ld ? X.ld : K);
+                    const uint16_t *wr = static_cast<const uint16_t *>(W.base) +
+                                         (static_cast<int64_t>(col) * W.stride + W.offset) * (W.ld ? W.ld : K);
+                    sum = 0.0f;
+                    for (int k = k0; k < k1; ++k) sum = fmaf(value(xr[k]), value(wr[k]), sum);
+                    for (int j = 0; j < x.slots; ++j) {
+                        const uint32_t at =
+                            where[j / 2 * kPlanRows + row % kPlanRows] >> (16 * (j % 2)) & 0xFFFFu;
+                        if (at == 0) continue;
+                        const uint16_t *b =
+                            x.B + (static_cast<int64_t>(ids[at - 1]) * x.cols + col) * x.rank;
+                        const uint16_t *t =
+                            x.T + ((static_cast<int64_t>(row) * x.slots + j) * kParts +
+                                   (kGated ? block % 2 : 0)) * x.rank * 2;
+                        for (int r = 0; r < x.rank; ++r) {
+                            const uint16_t *h = t + (r & ~7) * 2 + (r & 7);
+                            sum = fmaf(value(h[0]) + value(h[8]), value(b[r]), sum);
+                        }
+                    }
+                }
+                v = f32x4{v[1], v[2], v[3], sum};
+            }
+#pragma unroll
+            for (int q = 0; q < kQuads; ++q)
+                if (q == i) {
+                    f32x4 &to = acc[q / (4 * S::TN)][q / 4 % S::TN].v[q % 4];
+                    to = v;
+                    asm volatile("" : "+a"(to));
+                }
+        }
     }
     template <int... I, class F>
     __device__ __forceinline__ static void for_each(std::integer_sequence<int, I...>, const F &f) {

@@ -284,12 +284,12 @@ struct WithLora : Base {
 };
 using PairMulLora = WithLora<PairMulEpilogue>;
 using StoreLora = WithLora<StoreEpilogue>;
-// begin() before a tile's K steps, run() behind them.
+// begin() before a tile's K steps [kb, ke) of BK elements, run() behind them.
 template <class S, class Epi, bool kQuarter = false>
 struct Adapters {
     __device__ __forceinline__ void begin(const Epi &, int) {}
-    __device__ __forceinline__ void run(SWIGLU_LDS char *, const Epi &,
-                                        typename S::Acc (&)[S::TM][S::TN], int, int) {}
+    __device__ __forceinline__ void run(SWIGLU_LDS char *, const Epi &, const KMajor &, const KMajor &,
+                                        int, int, int, typename S::Acc (&)[S::TM][S::TN], int, int) {}
 };
 template <class S, class Base, bool kQuarter>
 struct Adapters<S, WithLora<Base>, kQuarter> {
@@ -298,8 +298,10 @@ struct Adapters<S, WithLora<Base>, kQuarter> {
         expand.begin(epi.lora, m0);
     }
     __device__ __forceinline__ void run(SWIGLU_LDS char *lds, const WithLora<Base> &epi,
+                                        const KMajor &A, const KMajor &B, int K, int kb, int ke,
                                         typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0) {
-        expand.run(lds, epi.lora, acc, m0, n0);
+        if (expand.run(lds, epi.lora, acc, m0, n0))
+            expand.mend(epi.lora, A, B, K, kb * S::BK, min(ke * S::BK, K), acc, m0, n0);
     }
 };
 
@@ -409,7 +411,7 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
                 pl.prologue_wait();
                 run_tile<S, kEven>(pl, issue, nk, acc);
                 pl.drain(acc);
-                adapters.run(lds, epi, acc, m0, n0);
+                adapters.run(lds, epi, Ak, B, K, 0, nk, acc, m0, n0);
                 if (j + grid < sch.dp) {
                     tile_coords(xcd_order(j + grid, sch.dp), sch.tiles_m, sch.tiles_n, sch.group_m, tm,
                                 tn);
@@ -440,7 +442,7 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             Adapters<Q, Epi, true> adapters;
             adapters.begin(epi, m0);
             tile_mainloop<Q, kEven>(lds, Ak, B, M, K, m0, n0, 0, sch.nk, sch.nk, acc);
-            adapters.run(lds, epi, acc, m0, n0);
+            adapters.run(lds, epi, Ak, B, K, 0, sch.nk, acc, m0, n0);
             epi.template apply<Q>(acc, m0, n0, threadIdx.x);
         }
         whole_tiles();
@@ -466,7 +468,7 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
             // (the adapters' terms once a tile)
             if (piece == sch.pieces - 1)
-                adapters.run(lds, epi, acc, tm * S::BM, tn * S::BN);
+                adapters.run(lds, epi, Ak, B, K, kb, ke, acc, tm * S::BM, tn * S::BN);
             const float *slots = sch.partials + static_cast<int64_t>(i) * sch.pieces * S::BM * S::BN;
             store_partial_coherent<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN,
                                       acc, threadIdx.x);
@@ -513,7 +515,7 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
             // (the adapters' terms once a tile)
             if (piece == sch.pieces - 1)
-                adapters.run(lds, epi, acc, tm * S::BM, tn * S::BN);
+                adapters.run(lds, epi, Ak, B, K, kb, ke, acc, tm * S::BM, tn * S::BN);
             store_partial<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN, acc,
                              threadIdx.x);
         }

@@ -388,3 +388,68 @@ def test_every_schedule_of_few_rows(dev, tile, tail, M, K, N, r, J, monkeypatch)
 
 def test_reduced_in_the_kernel_by_its_own_choice(dev):
     check(dev, "gated", 100, 3584, 4864, 8, 16, 1, "mixed", False, seed=5)
+
+
+def one_after_the_other(x, w, t, part, parts, ids, weights):
+    """projected() with sums that go one after the other: K + J r roundings."""
+    D, err = projected(x, w, t, part, parts, ids, weights)
+    size = x.double().abs() @ w[part::parts].double().abs().t()
+    T = (x.double().abs() @ t["A"].double().abs().flatten(0, 1).t()).max() * 8 * t["scale"].abs().max()
+    size += T * t["B"][:, part::parts].double().abs().sum(2).max()
+    return D, err + (x.shape[1] + ids.shape[1] * t["B"].shape[2]) * 2.0 ** -24 * size
+
+
+@pytest.mark.parametrize("kind", ["gated", "down"])
+@pytest.mark.parametrize("M,K,N,r,J,tile,tail", [
+    (1, 200, 264, 8, 2, None, None), (30, 200, 264, 16, 2, None, None),
+    (50, 72, 16400, 24, 1, None, None), (100, 520, 1400, 40, 3, "256", "fixup"),
+    (128, 520, 1400, 16, 2, "128", "split"), (300, 328, 1400, 16, 2, "256", "split"),
+    (300, 328, 1400, 128, 8, "256", "quarter"), (520, 136, 1400, 16, 1, "256", "whole"),
+    (520, 136, 1400, 8, 4, "128", "whole"), (300, 520, 520, 24, 2, "128", "split")])
+def test_a_broken_adapter_is_its_rows_own(dev, kind, M, K, N, r, J, tile, tail, monkeypatch):
+    """Infinities and NaN in the B of an adapter stay in the rows that name it, and
+    are there what the formula makes of them."""
+    print(f"\n[case] lora broken {kind} M={M} K={K} N={N} r={r} J={J} {tile} {tail}", flush=True)
+    if tile:
+        monkeypatch.setenv("SWIGLU_I_TILE", tile)
+        monkeypatch.setenv("SWIGLU_TAIL", tail)
+    x, w, t, ids, weights = case_of(kind, M, K, N, 5, r, J, "mixed", True, seed=M + r)
+    weights += 0.25
+    if M > 1:
+        ids[ids == 2] = 1
+        ids[::7, J - 1] = 2
+    else:
+        ids[0, 0], ids[0, 1] = 2, 1
+    parts = 2 if kind == "gated" else 1
+    bad = {n: v.clone() for n, v in t.items()}
+    cols = parts * N
+    inf_at = sorted({0, cols // 3 // parts * parts, cols - parts})
+    for c in inf_at:
+        bad["B"][2, c, c % r] = float("-inf") if c else float("inf")
+    nan_at = sorted({parts * 5, cols // 2 // parts * parts})
+    for c in nan_at:
+        bad["B"][2, c, r - 1] = float("nan")
+    touched = torch.zeros(N, dtype=torch.bool)
+    touched[[c // parts for c in inf_at + nan_at]] = True
+    named = (ids == 2).any(1)
+
+    ref = run(kind, dev, x, w, t, ids, weights).cpu()
+    got = run(kind, dev, x, w, bad, ids, weights).cpu()
+    assert torch.equal(ref[:, ~touched], got[:, ~touched])
+    if kind == "gated":
+        g, ge = one_after_the_other(x, w, t, 0, 2, ids, weights)
+        u, ue = one_after_the_other(x, w, t, 1, 2, ids, weights)
+        s = g * torch.sigmoid(g)
+        want, se = s * u, 1.1 * ge + s.abs() * 2.0 ** -20
+        tol = (se * u.abs() + s.abs() * ue + se * ue) * (1 + 2.0 ** -8) + want.abs() * 2.0 ** -8
+    else:
+        want, tol = rounded(*one_after_the_other(x, w, t, 0, 1, ids, weights))
+    if not named.all():
+        within(got[~named], want[~named], tol[~named] + 2.0 ** -126, "the other rows")
+    assert torch.isnan(got[named][:, [c // parts for c in nan_at]]).all()
+    if kind == "down":
+        a = x.double() @ t["A"][2].double().t()
+        share = torch.where(ids == 2, weights.double(), 0.0).sum(1) * t["scale"][2].double()
+        for c in inf_at:
+            toward = (a[:, c % r] * share * float(bad["B"][2, c, c % r]))[named]
+            assert torch.equal(got[named][:, c].double(), toward)
