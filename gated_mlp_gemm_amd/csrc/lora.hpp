@@ -167,6 +167,7 @@ struct LoraExpand {
     }
 
     int n;                 // adapters of the plan
+    int first, steps;      // the piece's steps of 32 k
     uint32_t id[kEarly];   // the lane's adapter in each of the first steps
 
     __device__ __forceinline__ static int swizzle(int row) { return ((row >> 1) ^ (row >> 3)) & 3; }
@@ -182,17 +183,23 @@ struct LoraExpand {
         return tid;
     }
 
-    __device__ __forceinline__ void begin(const LoraTerm &x, int m0) {
+    // Piece `piece` of `pieces` of a tile split along K takes its share of the steps.
+    // (All by the last piece: M=525 K=3360 N=3384, 30 adapters of rank 32, 87 against
+    // 60 us; M=99 K=4656 N=1256, 23 of rank 40, 26 against 13.5.)
+    __device__ __forceinline__ void begin(const LoraTerm &x, int m0, int piece, int pieces) {
         const int tid = thread();
         const char *plan = x.plans + static_cast<int64_t>(m0 / kPlanRows) * x.plan_bytes;
         // (uniform: a scalar load)
         n = *reinterpret_cast<const __attribute__((address_space(4))) int *>(
             reinterpret_cast<uintptr_t>(plan));
         const int shift = kQuarter ? x.quarter.shift : x.whole.shift;
+        const int all = ((n << shift) + 3) / 4;
+        first = all * piece / pieces;
+        steps = all * (piece + 1) / pieces - first;
         const uint16_t *ids = reinterpret_cast<const uint16_t *>(plan + kPlanIds);
 #pragma unroll
         for (int s = 0; s < kEarly; ++s)
-            id[s] = n > 0 ? ids[min((4 * s + b_chunk(tid)) >> shift, n - 1)] : 0u;
+            id[s] = n > 0 ? ids[min((4 * (first + s) + b_chunk(tid)) >> shift, n - 1)] : 0u;
     }
 
     // after MFMA i of 4 kRows S::TN: hook(i); with the first row block, zeros times B
@@ -225,7 +232,7 @@ struct LoraExpand {
     // Whether the wave's columns met an infinity or NaN in B (then mend()).
     __device__ __forceinline__ bool run(SWIGLU_LDS char *lds, const LoraTerm &x,
                                         typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0) const {
-        if (n == 0) return false;
+        if (steps == 0) return false;
         const int tid = thread(), lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / S::WN, wn = wave % S::WN;
@@ -256,7 +263,6 @@ struct LoraExpand {
         }
         const int64_t b_adapter = static_cast<int64_t>(x.cols) * x.rank;
         const int planes_part = planes(by.shift), mask = (1 << by.shift) - 1;
-        const int steps = ((n << by.shift) + 3) / 4;
 
         const int row0 = wm * S::kWaveM + r16;   // the lane's row of T in row block 0
         // row blocks whose T is in registers at once, one such group ahead
@@ -295,7 +301,7 @@ struct LoraExpand {
                 }
                 // step s of B to its stage, from the adapter `of` of the lane
                 auto issue_b = [&](int s, uint32_t of) {
-                    const int e = 4 * s + b_chunk(tid);
+                    const int e = 4 * (first + s) + b_chunk(tid);
                     // past the end: something there is, multiplied with zeros
                     const int element = min(r0 + (e & mask), rank8 - 1);
                     const uint16_t *p = x.B + (of * b_adapter + 8 * element);
@@ -310,7 +316,7 @@ struct LoraExpand {
                     for (int q = 0; q < kSteps; ++q)
                         of[q] = asm_read_u16(
                             at + kIds +
-                            min((4 * (stage * kSteps + q) + b_chunk(tid)) >> by.shift, n - 1) * 2);
+                            min((4 * (first + stage * kSteps + q) + b_chunk(tid)) >> by.shift, n - 1) * 2);
 #pragma unroll
                     for (int q = 0; q < kSteps; ++q) issue_b(stage * kSteps + q, landed(of[q]));
                 };
@@ -337,7 +343,7 @@ struct LoraExpand {
                     uint32_t at[2], key[2];
                 };
                 auto look_at = [&](int s, int pair) {
-                    const int e = 4 * s + g;
+                    const int e = 4 * (first + s) + g;
                     const int i = e >> by.shift, k = e & mask;
                     const uint32_t key = r0 + k < rank8 ? i + 1 : 0xFFFFu;   // (no index is that far)
                     Look l;
@@ -461,12 +467,13 @@ struct LoraExpand {
     }
 
     // The NaN among the wave's results again, from the formula: K elements [k0, k1) of the
-    // shared product, then the row's own adapters.  (A lane an element, from memory: for
+    // shared product, then what the piece's steps take of the row's own adapters.  (A lane an element, from memory: for
     // adapters that are broken, so that they break no row but their own.)
-    __device__ __forceinline__ static void mend(const LoraTerm &x, const KMajor &X, const KMajor &W,
-                                                int K, int k0, int k1,
-                                                typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0) {
+    __device__ __forceinline__ void mend(const LoraTerm &x, const KMajor &X, const KMajor &W, int K,
+                                         int k0, int k1, typename S::Acc (&acc)[S::TM][S::TN], int m0,
+                                         int n0) const {
         constexpr int kQuads = S::TM * S::TN * 4;
+        const int shift = kQuarter ? x.quarter.shift : x.whole.shift;
         const int tid = thread(), lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / S::WN, wn = wave % S::WN;
@@ -500,7 +507,7 @@ struct LoraExpand {
                     sum = 0.0f;
                     for (int k = k0; k < k1; ++k) sum = fmaf(value(xr[k]), value(wr[k]), sum);
                     for (int j = 0; j < x.slots; ++j) {
-                        const uint32_t at =
+                        const int at =
                             where[j / 2 * kPlanRows + row % kPlanRows] >> (16 * (j % 2)) & 0xFFFFu;
                         if (at == 0) continue;
                         const uint16_t *b =
@@ -509,6 +516,8 @@ struct LoraExpand {
                             x.T + ((static_cast<int64_t>(row) * x.slots + j) * kParts +
                                    (kGated ? block % 2 : 0)) * x.rank * 2;
                         for (int r = 0; r < x.rank; ++r) {
+                            const int step = (((at - 1) << shift) | (r / 8 & ((1 << shift) - 1))) / 4 - first;
+                            if (step < 0 || step >= steps) continue;
                             const uint16_t *h = t + (r & ~7) * 2 + (r & 7);
                             sum = fmaf(value(h[0]) + value(h[8]), value(b[r]), sum);
                         }

@@ -287,15 +287,16 @@ using StoreLora = WithLora<StoreEpilogue>;
 // begin() before a tile's K steps [kb, ke) of BK elements, run() behind them.
 template <class S, class Epi, bool kQuarter = false>
 struct Adapters {
-    __device__ __forceinline__ void begin(const Epi &, int) {}
+    __device__ __forceinline__ void begin(const Epi &, int, int = 0, int = 1) {}
     __device__ __forceinline__ void run(SWIGLU_LDS char *, const Epi &, const KMajor &, const KMajor &,
                                         int, int, int, typename S::Acc (&)[S::TM][S::TN], int, int) {}
 };
 template <class S, class Base, bool kQuarter>
 struct Adapters<S, WithLora<Base>, kQuarter> {
     LoraExpand<S, std::is_same<Base, PairMulEpilogue>::value, kQuarter> expand;
-    __device__ __forceinline__ void begin(const WithLora<Base> &epi, int m0) {
-        expand.begin(epi.lora, m0);
+    __device__ __forceinline__ void begin(const WithLora<Base> &epi, int m0, int piece = 0,
+                                          int pieces = 1) {
+        expand.begin(epi.lora, m0, piece, pieces);
     }
     __device__ __forceinline__ void run(SWIGLU_LDS char *lds, const WithLora<Base> &epi,
                                         const KMajor &A, const KMajor &B, int K, int kb, int ke,
@@ -464,11 +465,9 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             tile_coords(sch.dp + i, sch.tiles_m, sch.tiles_n, sch.group_m, tm, tn);
             typename S::Acc acc[S::TM][S::TN];
             Adapters<S, Epi> adapters;
-            adapters.begin(epi, tm * S::BM);
+            adapters.begin(epi, tm * S::BM, piece, sch.pieces);
             tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
-            // (the adapters' terms once a tile)
-            if (piece == sch.pieces - 1)
-                adapters.run(lds, epi, Ak, B, K, kb, ke, acc, tm * S::BM, tn * S::BN);
+            adapters.run(lds, epi, Ak, B, K, kb, ke, acc, tm * S::BM, tn * S::BN);
             const float *slots = sch.partials + static_cast<int64_t>(i) * sch.pieces * S::BM * S::BN;
             store_partial_coherent<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN,
                                       acc, threadIdx.x);
@@ -511,11 +510,9 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             tile_coords(t, sch.tiles_m, sch.tiles_n, sch.group_m, tm, tn);
             typename S::Acc acc[S::TM][S::TN];
             Adapters<S, Epi> adapters;
-            adapters.begin(epi, tm * S::BM);
+            adapters.begin(epi, tm * S::BM, piece, sch.pieces);
             tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
-            // (the adapters' terms once a tile)
-            if (piece == sch.pieces - 1)
-                adapters.run(lds, epi, Ak, B, K, kb, ke, acc, tm * S::BM, tn * S::BN);
+            adapters.run(lds, epi, Ak, B, K, kb, ke, acc, tm * S::BM, tn * S::BN);
             store_partial<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN, acc,
                              threadIdx.x);
         }
