@@ -602,17 +602,17 @@ hipError_t launch_down_proj(const uint16_t *H, const uint16_t *W3t, uint16_t *Ou
 }
 
 // The tile kernels with adapters: the same schedules, the adapters' terms
-// expanded before each tile's epilogue (or before a split tile's last piece
-// stores its partial).  The kernels without tail work are those with a tail,
+// expanded before each tile's epilogue (or before the pieces of a split tile store
+// their partials, each its share).  The kernels without tail work are those with a tail,
 // given none.
 template <class S, class Epi, class Base>
 static hipError_t launch_lora_gemm(const KMajor &A, KMajor B, int M, int cols, int K, Epi epi,
-                                   const GemmWorkspace &ws, hipStream_t stream) {
+                                   int count, const GemmWorkspace &ws, hipStream_t stream) {
     constexpr bool kGated = std::is_same<Epi, PairMulLora>::value;
-    epi.lora.whole = LoraExpand<S, kGated, false>::chunks(epi.lora.slots, epi.lora.rank);
+    epi.lora.whole = LoraExpand<S, kGated, false>::chunks(M, epi.lora.slots, epi.lora.rank, count);
     if constexpr (kQuarterable<S>)
         epi.lora.quarter = LoraExpand<typename QuarterOf<S>::type, kGated, true>::chunks(
-            epi.lora.slots, epi.lora.rank);
+            M, epi.lora.slots, epi.lora.rank, count);
     Schedule sch = make_schedule<S>(M, cols, K, ws);
     sch.grid = launch_grid<S>(sch, ws.cus);
     B.pairs = Epi::template paired<S>() ? 1 : 0;   // de-interleaved weight panels
@@ -629,25 +629,25 @@ static hipError_t launch_lora_gemm(const KMajor &A, KMajor B, int M, int cols, i
 
 template <class Epi, class Base>
 static hipError_t launch_lora(const KMajor &A, const KMajor &B, int M, int cols, int K, Epi epi,
-                              const GemmWorkspace &ws, hipStream_t stream) {
+                              int count, const GemmWorkspace &ws, hipStream_t stream) {
     if (M <= ShapeThinLora::BM && cdiv(cols, ShapeThinLora::BN) >= ws.cus)
-        return launch_lora_gemm<ShapeThinLora, Epi, Base>(A, B, M, cols, K, epi, ws, stream);
+        return launch_lora_gemm<ShapeThinLora, Epi, Base>(A, B, M, cols, K, epi, count, ws, stream);
     if (M <= 128) {
         if constexpr (std::is_same<Epi, PairMulLora>::value) {
             const Schedule fx = make_fixup_schedule<ShapeSplitK>(M, cols, K, ws);
             if (fx.pieces) {
                 epi.lora.whole =
-                    LoraExpand<ShapeSplitK, true, false>::chunks(epi.lora.slots, epi.lora.rank);
+                    LoraExpand<ShapeSplitK, true, false>::chunks(M, epi.lora.slots, epi.lora.rank, count);
                 return launch_reduce_in_kernel<ShapeSplitK>(A, B, M, K, epi, fx, stream);
             }
             if (small_m_quad_tiles(M, cols, ws))
-                return launch_lora_gemm<ShapeQuad, Epi, Base>(A, B, M, cols, K, epi, ws, stream);
+                return launch_lora_gemm<ShapeQuad, Epi, Base>(A, B, M, cols, K, epi, count, ws, stream);
         }
-        return launch_lora_gemm<ShapeSmallLora, Epi, Base>(A, B, M, cols, K, epi, ws, stream);
+        return launch_lora_gemm<ShapeSmallLora, Epi, Base>(A, B, M, cols, K, epi, count, ws, stream);
     }
     if (quad_tiles_faster(M, cols, K, ws))
-        return launch_lora_gemm<ShapeQuad, Epi, Base>(A, B, M, cols, K, epi, ws, stream);
-    return launch_lora_gemm<ShapeWide, Epi, Base>(A, B, M, cols, K, epi, ws, stream);
+        return launch_lora_gemm<ShapeQuad, Epi, Base>(A, B, M, cols, K, epi, count, ws, stream);
+    return launch_lora_gemm<ShapeWide, Epi, Base>(A, B, M, cols, K, epi, count, ws, stream);
 }
 
 hipError_t launch_lora_project(const uint16_t *X, const uint16_t *W, uint16_t *Y, int M, int cols,
@@ -658,9 +658,9 @@ hipError_t launch_lora_project(const uint16_t *X, const uint16_t *W, uint16_t *Y
     const LoraTerm lora{T, t.B, plans, lora_plan_bytes(t.count, slots), M, slots, t.rank, cols, {}, {}};
     if (gated)
         return launch_lora<PairMulLora, PairMulEpilogue>(
-            A, B, M, cols, K, PairMulLora{{Y, M, cols / 2, cols / 2, 1.0f}, lora}, ws, stream);
-    return launch_lora<StoreLora, StoreEpilogue>(A, B, M, cols, K, StoreLora{{Y, M, cols}, lora}, ws,
-                                                 stream);
+            A, B, M, cols, K, PairMulLora{{Y, M, cols / 2, cols / 2, 1.0f}, lora}, t.count, ws, stream);
+    return launch_lora<StoreLora, StoreEpilogue>(A, B, M, cols, K, StoreLora{{Y, M, cols}, lora},
+                                                 t.count, ws, stream);
 }
 
 // One 256x256 fp32 slot per CU: a split schedule has at most one piece per

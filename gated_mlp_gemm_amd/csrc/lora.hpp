@@ -37,6 +37,7 @@
 
 namespace swiglu {
 
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int kPlanRows = 256;
 constexpr int kPlanWhere = 16;                            // byte offsets in a plan
 constexpr int kPlanIds = kPlanWhere + 4 * kPlanRows * 4;
@@ -44,8 +45,9 @@ constexpr int kPlanIds = kPlanWhere + 4 * kPlanRows * 4;
 // How an expansion walks T: `slots` slots and 8 << shift elements of each part's
 // rank at a time, as much as fits its LDS.  (A power of two: with any count the
 // quotients by it were a third of the instructions of a step.)
+// `plane`: bytes of a plane of T, 64 for each row there is.
 struct LoraChunks {
-    int slots, shift;
+    int slots, shift, plane;
 };
 struct LoraTerm {
     const uint16_t *T;   // [M][slots][parts * rank / 8][2][8]: rounded, then the rest
@@ -150,20 +152,37 @@ struct LoraExpand {
     static constexpr int kRing = S::kLdsBytes - kStages * kSteps * kStepBytes;
     static constexpr int kDma = kStepBytes / 4096;   // loads a wave and step
     static constexpr int kEarly = (kStages - 1) * kSteps;
-    // a plane of T: 16 elements (4 chunks, rounded and rest) of a slot's part
+    // A plane of T: 16 elements (4 chunks, rounded and rest) of a slot's part.  In
+    // tiles for few rows, of the rows that there are, so that more of the slots and
+    // the rank goes at once (M=8 K=928 N=7112, 3 slots of rank 40: 20.7
+    // -> 17.3 us).
     static constexpr int kPlane = S::BM * 64;
-    static constexpr int kPlanes = (kRing - kT) / kPlane;
-    static_assert(kPlanes >= kParts, "T fits");
+    static constexpr bool kFewRows = kSteps > 1;
+    static_assert((kRing - kT) / kPlane >= kParts, "T fits");
+    __device__ __forceinline__ static int plane(const LoraChunks &by) {
+        return kFewRows ? by.plane : kPlane;
+    }
 
     static constexpr int planes(int shift) { return shift > 1 ? 1 << (shift - 1) : 1; }   // of a slot's part
     // All slots and the whole rank (rounded up to a power of two) if they fit,
     // else as much of the rank as does, else one plane and as many slots as do.
-    static LoraChunks chunks(int slots, int rank) {
-        const int most = kPlanes / kParts;
+    // Where requests of their own adapters make many of them (few rows), less of the
+    // rank at a time if that leaves out so much padding that it pays for the further
+    // passes, each about 3 steps (M=21 K=536 N=1024, 17 adapters of rank 48, two a row:
+    // the tile kernel 20.1 us 16 at a time, 21.4 with all 64).
+    static LoraChunks chunks(int M, int slots, int rank, int count) {
+        const int plane = kFewRows && M < S::BM ? (M + 15) / 16 * 1024 : kPlane;
+        const int most = (kRing - kT) / plane / kParts;
         int shift = 0;
         while ((8 << shift) < rank) ++shift;
         while (shift > 1 && planes(shift) * slots > most) --shift;
-        return {slots < most ? slots : most, shift};
+        if (kFewRows) {
+            const int64_t named = static_cast<int64_t>(M) * slots, n = named < count ? named : count;
+            auto steps = [&](int by) { return ceil_div(rank, 8 << by) * (ceil_div(n << by, 4) + 3); };
+            for (int by = shift - 1; by >= 0; --by)
+                if (steps(by) < steps(shift)) shift = by;
+        }
+        return {slots < most ? slots : most, shift, plane};
     }
 
     int n;                 // adapters of the plan
@@ -269,7 +288,8 @@ struct LoraExpand {
         constexpr int kRows = kRowBlocks > 2 ? 2 / kParts : kRowBlocks;
         constexpr int kGroups = kRowBlocks / kRows;
         const uint32_t t_row = at + kT + row0 * 64u;
-        const uint32_t t_part = static_cast<uint32_t>(planes_part * kPlane);
+        const int t_plane = plane(by);
+        const uint32_t t_part = static_cast<uint32_t>(planes_part * t_plane);
         // (in vector registers: the accumulators may hold all others)
         f32x4 met = {0.0f, 0.0f, 0.0f, 0.0f};
         u32x4 nothing = {0u, 0u, 0u, 0u};
@@ -283,20 +303,26 @@ struct LoraExpand {
                 // T: a wave a quarter of the rows, 16 rows of a plane a load.  (Past the
                 // last slot: past the row, or zeros; never read.)
                 {
+                    const int row16 = kFewRows ? wave : wave * (S::BM / 64);   // of the first load
                     const uint32_t from =
-                        static_cast<uint32_t>((wave * (S::BM / 4) + lane / 4) * row_bytes) +
+                        static_cast<uint32_t>((row16 * 16 + lane / 4) * row_bytes) +
                         ((lane & 3) ^ swizzle(lane / 4)) * 16u;
-                    SWIGLU_LDS char *to = lds + kT + wave * (kPlane / 4);
+                    SWIGLU_LDS char *to = lds + kT + row16 * 1024;
 #pragma nounroll
                     for (int sp = 0; sp < by.slots * kParts; ++sp)
 #pragma nounroll
                         for (int i = 0; i < planes_part; ++i) {
                             const uint32_t soff = static_cast<uint32_t>(
                                 (j0 * kParts + sp) * x.rank * 4 + r0 * 32 + i * 64);
+                            if constexpr (kFewRows) {
+                                for (int t = 0; (row16 + t) * 1024 < t_plane; t += 4)
+                                    dma16(tr, to + t * 1024, from, soff + t * 16u * row_bytes);
+                            } else {
 #pragma unroll
-                            for (int t = 0; t < S::BM / 64; ++t)
-                                dma16(tr, to + t * 1024, from, soff + t * 16u * row_bytes);
-                            to += kPlane;
+                                for (int t = 0; t < S::BM / 64; ++t)
+                                    dma16(tr, to + t * 1024, from, soff + t * 16u * row_bytes);
+                            }
+                            to += t_plane;
                         }
                 }
                 // step s of B to its stage, from the adapter `of` of the lane
@@ -349,7 +375,7 @@ struct LoraExpand {
                     Look l;
                     l.key[0] = 2 * pair >= j0 ? key : 0xFFFFu;
                     l.key[1] = 2 * pair + 1 < j0 + by.slots ? key : 0xFFFFu;
-                    l.at[0] = t_row + ((2 * pair - j0) * kParts * planes_part + (k >> 1)) * kPlane +
+                    l.at[0] = t_row + ((2 * pair - j0) * kParts * planes_part + (k >> 1)) * t_plane +
                               ((2 * (k & 1)) ^ swizzle(r16)) * 16u;
                     l.at[1] = l.at[0] + kParts * t_part;
                     return l;

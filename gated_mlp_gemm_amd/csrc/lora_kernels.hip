@@ -7,8 +7,6 @@
 
 namespace swiglu {
 
-static inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 constexpr int kShrinkRows = 64;
 
 // The adapters that 64 rows from row m0 on name: their slots' ids (-1: none)
