@@ -14,8 +14,10 @@
 #include <cmath>
 #include <cstring>
 #include <atomic>
+#include <chrono>
 #include <mutex>
 
+#include "arrivals.hpp"
 #include "launch.hpp"
 
 namespace {
@@ -135,31 +137,14 @@ int tail_override() {
     return swiglu::kTailAuto;
 }
 
-// Arrival counters of the split GEMM tiles that are reduced in the kernel
-// (split_tail.hpp): library-owned device memory, zero when the library is
-// loaded and left zero by every call that completes.  Each call takes the
-// next of kCounterBlocks blocks of its device's array in turn, so up to
-// kCounterBlocks such calls may run at once on one device (on different
-// streams).  Host code uses the per-device address from hipGetSymbolAddress.
-constexpr int kCounterBlocks = 64;
-constexpr int kCountersPerBlock = 1024;
-static __device__ __align__(256) unsigned split_counters[kCounterBlocks * kCountersPerBlock] = {};
-unsigned *g_counters_ptr[256];   // per device, guarded by g_dev_mutex
-unsigned g_counter_next[256];    // next block per device, guarded by g_dev_mutex
-
-// The current device's next counter block, or nullptr (then no call reduces
-// in the kernel).
-unsigned *next_counter_block() {
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 256) return nullptr;
-    std::lock_guard<std::mutex> lock(g_dev_mutex);
-    if (g_counters_ptr[dev] == nullptr) {
-        void *p = nullptr;
-        if (hipGetSymbolAddress(&p, HIP_SYMBOL(split_counters)) != hipSuccess) return nullptr;
-        g_counters_ptr[dev] = static_cast<unsigned *>(p);
-    }
-    const unsigned block = g_counter_next[dev]++ % kCounterBlocks;
-    return g_counters_ptr[dev] + static_cast<size_t>(block) * kCountersPerBlock;
+// The tag of a launch whose workgroups meet (arrivals.hpp): a number of its upper 52
+// bits that no other launch of this process has, spread over all of them (the step is odd),
+// from a start that other processes hardly share.
+uint64_t next_arrival_tag() {
+    static std::atomic<uint64_t> next{
+        static_cast<uint64_t>(std::chrono::system_clock::now().time_since_epoch().count()) ^
+        (static_cast<uint64_t>(reinterpret_cast<uintptr_t>(&g_dev_mutex)) << 20)};
+    return next.fetch_add(0x9E3779B97F4A7C15u, std::memory_order_relaxed) << swiglu::kArrivalBits;
 }
 
 swiglu::GemmWorkspace make_ws(void *workspace, uint64_t bytes, int cus) {
@@ -169,8 +154,7 @@ swiglu::GemmWorkspace make_ws(void *workspace, uint64_t bytes, int cus) {
     ws.cus = cus;
     ws.tile = tile_override();
     ws.tail = tail_override();
-    ws.counters = ws.base ? next_counter_block() : nullptr;
-    ws.max_counters = ws.counters ? kCountersPerBlock : 0;
+    ws.tag = next_arrival_tag();
     return ws;
 }
 
@@ -287,12 +271,12 @@ hipError_t lora_projection(const uint16_t *X, const uint16_t *W, uint16_t *Y, in
     const uint64_t state = lora_state_bytes(M, slots, parts * t.rank, t.count);
     uint16_t *T = static_cast<uint16_t *>(workspace);
     char *plans = static_cast<char *>(workspace) + lora_t_bytes(M, slots, parts * t.rank);
-    // the two launches run in stream order: they share scratch and counters
-    const swiglu::GemmWorkspace ws =
-        make_ws(static_cast<char *>(workspace) + state, bytes - state, cus);
+    // the two launches run in stream order: they share scratch
+    swiglu::GemmWorkspace ws = make_ws(static_cast<char *>(workspace) + state, bytes - state, cus);
     const hipError_t e = swiglu::launch_lora_shrink(X, t, ids, weights, (int)slots, T, plans,
                                                     (int)M, (int)K, parts, ws, s);
     if (e != hipSuccess) return e;
+    ws.tag = next_arrival_tag();
     return swiglu::launch_lora_project(X, W, Y, (int)M, (int)cols, (int)K, gated, t,
                                        (int)slots, T, plans, ws, s);
 }
@@ -734,7 +718,7 @@ int swiglu_route_workspace_size(int64_t M, int64_t E, uint64_t *bytes) {
     int cus = 0;
     st = check_device(&cus);
     if (st != SWIGLU_OK) return st;
-    *bytes = swiglu::route_partials_bytes(M, E, cus);
+    *bytes = swiglu::route_workspace_bytes(M, E, cus);
     return ok();
 }
 
@@ -760,11 +744,9 @@ int swiglu_route(const void *logits, int logits_type, const uint8_t *valid, int3
     int cus = 0;
     st = check_device(&cus);
     if (st != SWIGLU_OK) return st;
-    const bool part = workspace != nullptr && workspace_bytes > 0;
     return launched(swiglu::launch_route(logits, bf16, valid, ids, weights, counts, loss, M, (int)E,
-                                         (int)k, normalize != 0, part ? workspace : nullptr,
-                                         workspace_bytes, part ? next_counter_block() : nullptr,
-                                         cus, (hipStream_t)stream),
+                                         (int)k, normalize != 0, workspace, workspace_bytes,
+                                         next_arrival_tag(), cus, (hipStream_t)stream),
                     "route");
 }
 

@@ -360,7 +360,7 @@ static bool small_m_quad_tiles(int M, int cols, const GemmWorkspace &ws) {
 // M <= 128 (one tile row): every tile split into s = min(G / T, nk) pieces
 // along K and reduced in the kernel, when 3 <= s <= kMaxFixupPieces and each
 // piece has at least 16 K steps, or when SWIGLU_TAIL=fixup forces it (s
-// capped); needs the workspace for the partials and a counter block.
+// capped); needs the workspace for the partials and a word per tile behind them.
 // Otherwise a schedule with pieces == 0.  Each piece writes a 64 KiB fp32
 // partial and the last reads s - 1 of them, so short pieces lose: against the
 // 128x64 tiles run whole (same box, M=128): K=8192 N=4864 44.2 against
@@ -371,7 +371,7 @@ static bool small_m_quad_tiles(int M, int cols, const GemmWorkspace &ws) {
 template <class S>
 static Schedule make_fixup_schedule(int M, int cols, int K, const GemmWorkspace &ws) {
     Schedule none{};
-    if (M > S::BM || ws.cus <= 0 || ws.base == nullptr || ws.counters == nullptr) return none;
+    if (M > S::BM || ws.cus <= 0 || ws.base == nullptr) return none;
     if (ws.tail != kTailAuto && ws.tail != kTailFixup) return none;
     Schedule sch{};
     sch.tiles_m = 1;
@@ -382,13 +382,15 @@ static Schedule make_fixup_schedule(int M, int cols, int K, const GemmWorkspace 
     int s = ws.cus / T < sch.nk ? ws.cus / T : sch.nk;
     if (ws.tail == kTailAuto && (s < 3 || s > kMaxFixupPieces || sch.nk < 16 * s)) return none;
     if (s > kMaxFixupPieces) s = kMaxFixupPieces;
-    if (s < 2 || T > ws.max_counters) return none;
-    if (static_cast<uint64_t>(T) * s * S::BM * S::BN * sizeof(float) > ws.bytes) return none;
+    if (s < 2) return none;
+    const uint64_t partials = static_cast<uint64_t>(T) * s * S::BM * S::BN * sizeof(float);
+    if (partials + static_cast<uint64_t>(T) * sizeof(uint64_t) > ws.bytes) return none;
     sch.dp = 0;
     sch.split_tiles = T;
     sch.pieces = s;
     sch.partials = reinterpret_cast<float *>(ws.base);
-    sch.counters = ws.counters;
+    sch.arrivals = reinterpret_cast<uint64_t *>(static_cast<char *>(ws.base) + partials);
+    sch.tag = ws.tag;
     sch.grid = T * s;
     return sch;
 }

@@ -15,8 +15,7 @@ struct GemmWorkspace {
     int cus;          // compute units of the device
     int tile;         // variant I / ablation GEMM tile: 0 = by the cost model, 256 or 128 = forced
     int tail;         // partly idle last round: 0 = by the cost model, else a TailChoice
-    unsigned *counters;   // arrival counters for a split reduced in the kernel (zero between calls)
-    int max_counters;     // counters available at `counters`
+    uint64_t tag;     // of the meetings of one launch's workgroups (arrivals.hpp)
 };
 // How the tiles of a partly idle last round run (GemmWorkspace::tail).
 enum TailChoice { kTailAuto = 0, kTailWhole = 1, kTailPieces = 2, kTailQuarters = 3, kTailFixup = 4 };
@@ -68,11 +67,12 @@ hipError_t launch_fused_sequential_fp8(const uint8_t *A8, const uint8_t *Wf8, ui
 int describe_gemm_fp8(int M, int cols, int K, const GemmWorkspace &ws, char *buf, size_t n);
 // The router and its gradient (route_kernels.hip).
 constexpr int kMaxRouteE = 512, kMaxRouteK = 16;
-uint64_t route_partials_bytes(int64_t M, int64_t E, int cus);
-// partials / counter: without them (or too few bytes) one workgroup does it all.
+uint64_t route_workspace_bytes(int64_t M, int64_t E, int cus);
+// workspace: without it (or too few bytes) one workgroup does it all; tag: of the
+// workgroups' meeting (arrivals.hpp).
 hipError_t launch_route(const void *logits, bool bf16, const uint8_t *valid, int *ids,
                         float *weights, int *counts, float *loss, int64_t M, int E, int k,
-                        bool normalize, void *partials, uint64_t partial_bytes, unsigned *counter,
+                        bool normalize, void *workspace, uint64_t workspace_bytes, uint64_t tag,
                         int cus, hipStream_t stream);
 hipError_t launch_route_backward(const void *logits, bool bf16, const uint8_t *valid,
                                  const int *ids, const float *weights, const int *counts,

@@ -70,7 +70,7 @@ struct ShrinkArgs {
     int plan_bytes, plan_wgs;   // the last workgroups of the grid write the plans
     int M, K, slots, cols, count;   // cols = parts * rank
     float *partials;
-    unsigned *counters;
+    uint64_t *arrivals, tag;   // a word an item of a row block (arrivals.hpp)
     int most_splits, per_rows;   // workgroups a row block
 };
 
@@ -140,8 +140,8 @@ __device__ __forceinline__ void write_plan(const ShrinkArgs &x, PlanLists &l, in
 // name; the rows of A of those, one after the other, make the columns of
 // T^T = A . X^T in items of 64, shared out over per_rows workgroups, which
 // split K where there are fewer items than workgroups (their sums meet in the
-// workspace as in split_tail.hpp: device-scope stores and an arrival count, the
-// last to arrive adds them up in order, nobody waits).  Every row of X is
+// workspace as in split_tail.hpp: device-scope stores and arrivals, the last to
+// arrive adds them up in order, nobody waits).  Every row of X is
 // multiplied with every adapter listed: T takes the ones that it names (the
 // products that no row takes cost nothing beside the loads).  Both operands
 // stream through LDS (the pipeline of gemm_core.hpp); loaded straight into MFMA
@@ -259,8 +259,12 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs &x, char *smem,
                 }
             weight[q] *= x.scale[max(id, 0)];
         }
+        // (two workgroups an item at least: G / 2 items)
+        uint64_t *arrivals = x.arrivals + static_cast<int64_t>(rows_at) * (G / 2) + item;
+        Arrival meeting{};
         S::Acc acc[S::TM][S::TN];
         pl.prologue_wait();
+        if (splits > 1 && tid == 0) meeting.announce(arrivals, x.tag);
         pl.run_init0<kEven>(issue, len, len, acc);
         pl.drain(acc);
 
@@ -270,6 +274,7 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs &x, char *smem,
 #pragma unroll
             for (int i = 0; i < 4; ++i) sum[q][i] = read_acc(acc[0][0].v[q][i]);
         if (splits > 1) {
+            if (tid == 0) meeting.settle(arrivals, x.tag);
             constexpr uint32_t kSlot = 4 * S::kThreads * 16;
             const __amdgpu_buffer_rsrc_t pr = make_rsrc(
                 x.partials + (static_cast<int64_t>(rows_at) * G + item * splits) * (kSlot / 4),
@@ -281,15 +286,11 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs &x, char *smem,
                     static_cast<int>(split * kSlot + (q * S::kThreads + tid) * 16), 0, kDeviceScope);
             wait_vmcnt<0>();   // this wave's sums are visible device-wide
             __syncthreads();   // ... and every wave's
-            unsigned *counter = x.counters + rows_at * (G / 2) + item;
-            if (tid == 0)
-                word = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED,
-                                              __HIP_MEMORY_SCOPE_AGENT);
+            if (tid == 0) word = arrive(arrivals);
             __syncthreads();
             // (a workgroup has one job where K is split)
             if (word + 1 != static_cast<unsigned>(splits)) return;
-            if (tid == 0)
-                __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (tid == 0) arrivals_done(arrivals);
 #pragma unroll
             for (int q = 0; q < 4; ++q) sum[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 8
@@ -350,13 +351,13 @@ hipError_t launch_lora_shrink(const uint16_t *X, const LoraTable &t, const int *
     if (2 * G * 24 <= nk) G = 4 * ws.cus / tiles;
     if (G > items * most) G = items * most;
     if (G < 1) G = 1;
-    if (ws.base == nullptr || ws.counters == nullptr ||
-        static_cast<uint64_t>(tiles) * G * (S::BM * S::BN * 4) > ws.bytes ||
-        tiles * G > 2 * ws.max_counters)
-        most = 1;
+    const uint64_t partials = static_cast<uint64_t>(tiles) * G * (S::BM * S::BN * 4);
+    const uint64_t words = static_cast<uint64_t>(tiles) * (G / 2);
+    if (ws.base == nullptr || partials + words * sizeof(uint64_t) > ws.bytes) most = 1;
     const int64_t plan_wgs = ceil_div(M, kPlanRows);
     const ShrinkArgs a{X, t.A, t.scale, weights, ids, T, plans, lora_plan_bytes(t.count, slots),
-                       static_cast<int>(plan_wgs), M, K, slots, cols, t.count, static_cast<float *>(ws.base), ws.counters,
+                       static_cast<int>(plan_wgs), M, K, slots, cols, t.count, static_cast<float *>(ws.base),
+                       reinterpret_cast<uint64_t *>(static_cast<char *>(ws.base) + partials), ws.tag,
                        static_cast<int>(most), static_cast<int>(G)};
     hipLaunchKernelGGL(lora_shrink_kernel, dim3((unsigned)(tiles * G + plan_wgs)), dim3(S::kThreads), 0, stream, a);
     return hipGetLastError();

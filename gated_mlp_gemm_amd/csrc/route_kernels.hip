@@ -25,6 +25,7 @@
 // in lane j of the row.
 #include "launch.hpp"
 
+#include "arrivals.hpp"
 #include "device.hpp"
 #include "gemm_core.hpp"
 
@@ -156,7 +157,7 @@ struct RouteArgs {
     int E, k;
     int normalize, vec;
     uint64_t *partials;   // [grid][E + 1]: {sum of p, picks}; unused by a grid of one
-    unsigned *counter;
+    uint64_t *arrivals, tag;   // (arrivals.hpp)
 };
 
 // Sum over the lanes of a wave, in every lane.
@@ -186,6 +187,7 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs x) {
     for (int e = tid; e <= kMaxE; e += THREADS) hist[e] = 0u;
     __syncthreads();
 
+    Arrival meeting{};
     float mine[kRouteValues] = {};
     for (int64_t first = static_cast<int64_t>(blockIdx.x) * kRowsPass; first < x.M;
          first += static_cast<int64_t>(gridDim.x) * kRowsPass) {
@@ -203,6 +205,9 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs x) {
         }
         float top, inv;
         const bool live = row_softmax<LPR>(v, wanted, top, inv);
+        // (in flight beside the picks, not before the logits)
+        if (tid == 0 && gridDim.x > 1 && first == static_cast<int64_t>(blockIdx.x) * kRowsPass)
+            meeting.announce(x.arrivals, x.tag);
 #pragma unroll
         for (int i = 0; i < kRouteValues; ++i) mine[i] += v[i];
         if (live && li == 0) atomicAdd(&hist[kMaxE], 1u);
@@ -280,6 +285,7 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs x) {
     if (gridDim.x == 1) {
         for (int e = tid; e < x.E; e += THREADS) sums[e] = block_sum(e);
     } else {
+        if (tid == 0) meeting.settle(x.arrivals, x.tag);
         const int width = x.E + 1;
         uint64_t *own = x.partials + static_cast<int64_t>(blockIdx.x) * width;
         for (int e = tid; e < width; e += THREADS) {
@@ -290,13 +296,10 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs x) {
         }
         wait_vmcnt<0>();   // this wave's sums are visible device-wide
         __syncthreads();   // ... and every wave's
-        if (tid == 0)
-            arrived = __hip_atomic_fetch_add(x.counter, 1u, __ATOMIC_RELAXED,
-                                             __HIP_MEMORY_SCOPE_AGENT);
+        if (tid == 0) arrived = arrive(x.arrivals);
         __syncthreads();
         if (arrived + 1 != gridDim.x) return;
-        if (tid == 0)
-            __hip_atomic_store(x.counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (tid == 0) arrivals_done(x.arrivals);
         // as many threads an expert as there are, each its own run of workgroups
         __shared__ double part_p[THREADS];
         __shared__ unsigned part_c[THREADS];
@@ -483,12 +486,18 @@ static int route_threads(int64_t M, int64_t E) { return M * lanes_per_row(E) <= 
 static int route_grid(int64_t M, int64_t E, int cus) {
     const int64_t per = route_threads(M, E) / lanes_per_row(E);
     const int64_t passes = (M + per - 1) / per;
+    if (cus >= 1 << kArrivalBits) cus = (1 << kArrivalBits) - 1;
     return static_cast<int>(passes < cus ? passes : cus);
 }
 
-uint64_t route_partials_bytes(int64_t M, int64_t E, int cus) {
+// The partials, and behind them (in a cache line of its own) the word that the
+// workgroups arrive at.
+static uint64_t partials_words(int grid, int64_t E) {
+    return (static_cast<uint64_t>(grid) * (E + 1) + 31) & ~uint64_t{31};
+}
+uint64_t route_workspace_bytes(int64_t M, int64_t E, int cus) {
     const int grid = route_grid(M, E, cus);
-    return grid > 1 ? static_cast<uint64_t>(grid) * (E + 1) * 8 : 0;
+    return grid > 1 ? (partials_words(grid, E) + 1) * sizeof(uint64_t) : 0;
 }
 
 template <bool kBf16, int THREADS>
@@ -521,16 +530,16 @@ static bool vector_rows(int64_t E, const void *p, const void *q) {
 
 hipError_t launch_route(const void *logits, bool bf16, const uint8_t *valid, int *ids,
                         float *weights, int *counts, float *loss, int64_t M, int E, int k,
-                        bool normalize, void *partials, uint64_t partial_bytes, unsigned *counter,
+                        bool normalize, void *workspace, uint64_t workspace_bytes, uint64_t tag,
                         int cus, hipStream_t stream) {
     int grid = route_grid(M, E, cus);
-    if (grid > 1 && (partials == nullptr || counter == nullptr ||
-                     partial_bytes < route_partials_bytes(M, E, cus)))
+    if (grid > 1 && (workspace == nullptr || workspace_bytes < route_workspace_bytes(M, E, cus)))
         grid = 1;
     if (grid < 1) grid = 1;   // M == 0: the counts and the loss are still written
+    uint64_t *const words = static_cast<uint64_t *>(workspace);
     const RouteArgs a{logits, valid, ids, weights, counts, loss, M, E, k, normalize ? 1 : 0,
-                      vector_rows(E, logits, nullptr) ? 1 : 0, static_cast<uint64_t *>(partials),
-                      counter};
+                      vector_rows(E, logits, nullptr) ? 1 : 0, words,
+                      grid > 1 ? words + partials_words(grid, E) : nullptr, tag};
     const int lpr = lanes_per_row(E);
     if (route_threads(M, E) == 256) {
         if (bf16) run_route<true, 256>(lpr, grid, a, stream);

@@ -29,15 +29,15 @@
 // and few tiles: the reduction launch would cost as much as the GEMM), every
 // piece stores its partial with device-scope stores (cache policy sc1: written
 // through to the level where every XCD sees it), waits for them to complete,
-// and one thread of its workgroup adds 1 to the tile's arrival counter with a
-// device-scope atomic.  The piece that sees s - 1 arrivals before its own is
-// the last: it resets the counter to 0, reads the other pieces' partials with
+// and one thread of its workgroup arrives at the tile's word, behind the
+// partials in the workspace (arrivals.hpp).  The piece that sees s - 1 arrivals
+// before its own is the last: it reads the other pieces' partials with
 // device-scope loads and sums all s in piece order (its own from registers, the
 // same additions as the reduction kernel's), then runs the epilogue.  No
-// workgroup ever waits for another.  The counters are library-owned device
-// memory that starts at zero and that every completed call leaves at zero.
+// workgroup ever waits for another.
 #pragma once
 
+#include "arrivals.hpp"
 #include "gemm_core.hpp"
 
 namespace swiglu {
@@ -52,7 +52,8 @@ struct Schedule {
     int quartered;          // 1: the tail tiles run as four quarter-size tiles instead
     int grid;               // workgroups launched (each loops over its share of the work)
     float *partials;        // one BM*BN slot per piece: slot j = piece j % pieces of split tile j / pieces
-    unsigned *counters;     // fixup: one arrival counter per split tile (zero between calls)
+    uint64_t *arrivals;     // fixup: a word per split tile (arrivals.hpp), and the launch's tag
+    uint64_t tag;
 };
 
 // Cache policy of the fixup's partial stores and loads: device scope (sc1).

@@ -461,6 +461,8 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             const int piece = j % sch.pieces;
             const int kb = piece * sch.nk / sch.pieces;
             const int ke = (piece + 1) * sch.nk / sch.pieces;
+            Arrival meeting{};
+            if (threadIdx.x == 0) meeting.announce(sch.arrivals + i, sch.tag);
             int tm, tn;
             tile_coords(sch.dp + i, sch.tiles_m, sch.tiles_n, sch.group_m, tm, tn);
             typename S::Acc acc[S::TM][S::TN];
@@ -469,20 +471,18 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
             adapters.run(lds, epi, Ak, B, K, kb, ke, acc, tm * S::BM, tn * S::BN);
             const float *slots = sch.partials + static_cast<int64_t>(i) * sch.pieces * S::BM * S::BN;
+            if (threadIdx.x == 0) meeting.settle(sch.arrivals + i, sch.tag);
             store_partial_coherent<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN,
                                       acc, threadIdx.x);
             wait_vmcnt<0>();   // this wave's partial is visible device-wide
             __syncthreads();   // ... and every wave's
             if (threadIdx.x == 0)
-                *arrival = __hip_atomic_fetch_add(sch.counters + i, 1u, __ATOMIC_RELAXED,
-                                                  __HIP_MEMORY_SCOPE_AGENT);
+                *arrival = arrive(sch.arrivals + i);
             __syncthreads();
             const unsigned seen = *arrival;
             __syncthreads();   // read by all before the next item's loads reuse LDS
             if (seen + 1 != static_cast<unsigned>(sch.pieces)) continue;
-            // the last piece: the counter is free for the next call
-            if (threadIdx.x == 0)
-                __hip_atomic_store(sch.counters + i, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (threadIdx.x == 0) arrivals_done(sch.arrivals + i);
             constexpr int kUnitBlocks = Epi::template unit_blocks<S>();
             constexpr int kUnits = S::TM * S::TN / kUnitBlocks;
 #pragma unroll

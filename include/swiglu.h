@@ -50,12 +50,12 @@
  *    transpose inside every call, so the transpose is the pack's job.
  *  - Calls are re-entrant; the only global state is a per-device cache of
  *    the device's architecture and compute-unit count, the static scratch
- *    array of swiglu_fused_gemm_noalloc, and a static array of arrival
- *    counters for the split reduced in the kernel (device memory the library
- *    holds; no call allocates).  The counters start at zero and every call
- *    that completes leaves them at zero; each such call takes the next of 64
- *    counter blocks of its device in turn, so at most 64 of them may run at
- *    once on one device (different streams).
+ *    array of swiglu_fused_gemm_noalloc (device memory the library holds; no
+ *    call allocates), and a count that numbers the calls.  Where workgroups of
+ *    one launch meet, they count arrivals in a word of the caller's workspace,
+ *    beside that number (which makes initialisation unnecessary).  So any number
+ *    of calls may run at once, on different streams or as captured graphs
+ *    replayed beside others, as long as each has a workspace of its own.
  *  - The code object targets gfx950 only: on another device every launching
  *    call returns SWIGLU_ERR_UNSUPPORTED.
  */
@@ -136,8 +136,8 @@ int swiglu_pack_weights(const uint16_t *W1, const uint16_t *W2,
  * epilogue.  At M <= 128 with long K (at least 3 pieces of at least 16 K
  * steps of 64, at most 4 pieces) variant I instead splits every tile along K
  * and sums the partials in the same kernel: the last piece of each tile to
- * finish (counted with a library-owned arrival counter, see the global state
- * below) reads the others' partials from the workspace.  Every schedule gives
+ * finish (see the arrivals above) reads the others' partials from the
+ * workspace.  Every schedule gives
  * bitwise reproducible results for a given (M, N, K, workspace size, device).
  * NULL or too small: no split.  Variant S does not use it.
  */
@@ -331,8 +331,9 @@ int swiglu_fused_gemm_fp8(const uint8_t *A8, const uint8_t *W_fused8,
  * Preconditions: 0 <= M <= 2^31 - 1, 1 <= E <= 512, 1 <= k <= min(E, 16);
  * pointers aligned to their element; outputs overlap nothing.  M == 0: counts
  * and loss are written (zeros).  workspace: at least
- * swiglu_route_workspace_size() bytes, 256-byte aligned, no initialisation;
- * NULL or too small: one workgroup does all rows.
+ * swiglu_route_workspace_size() bytes, 256-byte aligned, no initialisation, not
+ * shared by calls that may run concurrently; NULL or too small: one workgroup
+ * does all rows.
  *
  * swiglu_route_backward: d_logits [M][E] (the logits' type) from d_weights
  * [M][k] (NULL: zeros) and the scalar d_loss (NULL: zero), given what
@@ -378,7 +379,8 @@ int swiglu_route_backward(const void *logits, int logits_type, const uint8_t *va
  * Preconditions: those of the call without adapters; 1 <= slots <= 8; rank a
  * multiple of 8 in [8, 256]; 1 <= count <= 8192; matrices 16-byte, ids,
  * weights and scale 4-byte aligned; outputs and workspace overlap nothing.
- * workspace: required, 256-byte aligned, no initialisation: at least
+ * workspace: required, 256-byte aligned, no initialisation, not shared by calls
+ * that may run concurrently: at least
  * M * slots * (2 * rank) * 4 bytes (gated; rank for the down projection),
  * rounded up to 256, and another ceil(M / 256) * (4112 + 2 c), c being
  * min(count, 256 slots) rounded up to a multiple of 8, rounded up to 256; with
