@@ -374,20 +374,20 @@ template <bool kBf16, int LPR>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackwardArgs x) {
     constexpr int kThreads = 256, kRowsPass = kThreads / LPR;
     constexpr int kHeld = (kMaxRouteK + LPR - 1) / LPR;
-    __shared__ int total_picks;
+    __shared__ unsigned long long total_picks;   // (up to 16 (2^31 - 1))
     __shared__ __attribute__((aligned(16))) float shares_[kThreads * kRouteValues];
     SWIGLU_LDS float *shares = (SWIGLU_LDS float *)shares_;
     const int tid = threadIdx.x, li = tid % LPR, group = tid / LPR;
     const int e0 = li * kRouteValues;
-    if (tid == 0) total_picks = 0;
+    if (tid == 0) total_picks = 0u;
     __syncthreads();
-    int picks = 0;
+    unsigned long long picks = 0u;
     for (int e = tid; e < x.E; e += kThreads) picks += x.counts[e];
     if (picks) atomicAdd(&total_picks, picks);
     __syncthreads();
     const float n = static_cast<float>(max(x.counts[x.E], 1));
     const float d_loss = x.d_loss ? *x.d_loss : 0.0f;
-    const float each = d_loss * x.E / (static_cast<float>(max(total_picks, 1)) * n);
+    const float each = d_loss * x.E / (static_cast<float>(max(total_picks, 1ull)) * n);
     float g[kRouteValues];
 #pragma unroll
     for (int i = 0; i < kRouteValues; ++i)
