@@ -256,13 +256,14 @@ __global__ __launch_bounds__(THREADS) void route_kernel(RouteArgs x) {
             if (pick[h]) atomicAdd(&hist[at[h]], 1u);
         }
         total = row_sum<LPR>(total);
-        const float scale = x.normalize ? (total > 0.0f ? 1.0f / total : 0.0f) : inv;
+        // (a row that routes picks its largest logit: its total is 1 at least, or NaN)
+        const float scale = x.normalize ? 1.0f / total : inv;
 #pragma unroll
         for (int h = 0; h < kHeld; ++h) {
             const int j = h * LPR + li;
             if (here && j < x.k) {
                 x.ids[row * x.k + j] = pick[h] ? static_cast<int>(at[h]) : -1;
-                x.weights[row * x.k + j] = w[h] * scale;
+                x.weights[row * x.k + j] = pick[h] ? w[h] * scale : 0.0f;
             }
         }
     }

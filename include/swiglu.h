@@ -324,8 +324,8 @@ int swiglu_fused_gemm_fp8(const uint8_t *A8, const uint8_t *W_fused8,
  *                    balance loss, 1 when probabilities and picks are even.
  * A row routes if it has a logit above -inf and `valid` (NULL, or one byte a
  * row) is not 0 for it; one that does not gets ids -1 and weights 0 and counts
- * nowhere.  A NaN logit makes its row's weights (and the loss) NaN; its ids are then
- * unspecified picks of [-1, E).  Sums over a
+ * nowhere.  A NaN or +inf logit makes the weights of its row's picks (and the loss)
+ * NaN; where a logit is NaN the ids are unspecified picks of [-1, E).  Sums over a
  * row are fp32, sums over rows fp32 in each workgroup and 64-bit over
  * workgroups, in a fixed order: the same call gives the same bits.
  * Preconditions: 0 <= M <= 2^31 - 1, 1 <= E <= 512, 1 <= k <= min(E, 16);

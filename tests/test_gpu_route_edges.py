@@ -13,6 +13,8 @@ import torch
 from gated_mlp_gemm_amd import swiglu as sw
 
 pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+INF = float("inf")
 
 
 @pytest.fixture(scope="module")
@@ -46,3 +48,65 @@ def test_gradient_with_picks_past_31_bits(dev, each, normalize):
     size = p * (G + (p * G).sum(1, keepdim=True))
     off = (dz.cpu().double() - want).abs()
     assert (off <= 2.0 ** -17 * size).all(), float((off / size).max())
+
+
+def nan_rows(E, dtype, sign):
+    """A NaN of the sign alone, beside -inf, and beside numbers, at several places."""
+    word = {torch.float32: (torch.int32, 0x7FC00001, -0x400000),
+            BF: (torch.int16, 0x7FC0, -0x40)}[dtype]
+    nan = torch.tensor([word[1] if sign > 0 else word[2]], dtype=word[0]).view(dtype)
+    assert torch.isnan(nan).all()
+    rows = []
+    for at in sorted({0, E // 2, E - 1}):
+        for rest in (-INF, 0.5, 3.0e38):
+            row = torch.full((E,), rest).to(dtype)
+            row[at] = nan
+            rows.append(row)
+    rows.append(nan.expand(E).clone())
+    return torch.stack(rows)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("sign", [1], ids=["positive"])
+def test_a_nan_makes_its_rows_picks_nan(dev, sign, dtype):
+    for E, k in ((1, 1), (5, 1), (5, 3), (64, 4), (300, 16)):
+        z = nan_rows(E, dtype, sign)
+        M = z.shape[0]
+        z = torch.cat([z, torch.linspace(-1, 1, E).to(dtype)[None]])   # and a row without
+        for normalize in (True, False):
+            print(f"\n[case] route NaN {dtype} sign={sign} E={E} k={k} normalize={normalize}",
+                  flush=True)
+            ids, w, counts, loss = sw.swiglu_route(z.to(dev), k, normalize=normalize)
+            torch.cuda.synchronize()
+            ids, w = ids.cpu(), w.cpu()
+            assert int(ids.min()) >= -1 and int(ids.max()) < E
+            assert (ids[:M, 0] >= 0).all()
+            assert torch.isnan(w[:M][ids[:M] >= 0]).all(), w[:M]
+            assert (w[ids < 0] == 0).all()
+            assert not torch.isnan(w[M]).any()
+            assert torch.isnan(loss)
+            assert int(counts[E]) == M + 1
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("E,k", [(1, 1), (6, 3), (64, 8), (200, 16)])
+def test_an_infinite_logit_makes_its_rows_weights_nan(dev, E, k, dtype):
+    """softmax takes inf - inf: NaN, for every pick; the picks are what they are."""
+    z = torch.linspace(-2, 2, E).flip(0).repeat(4, 1)
+    z[0, E // 2] = INF
+    z[1, 0] = z[1, E - 1] = INF
+    z[2] = -INF
+    z[2, E - 1] = INF
+    z = z.to(dtype)
+    for normalize in (True, False):
+        print(f"\n[case] route inf {dtype} E={E} k={k} normalize={normalize}", flush=True)
+        ids, w, counts, loss = sw.swiglu_route(z.to(dev), k, normalize=normalize)
+        torch.cuda.synchronize()
+        order = torch.sort(z.float(), dim=1, descending=True, stable=True)
+        want = torch.where(order.values[:, :k] > -INF, order.indices[:, :k], -1)
+        assert torch.equal(ids.cpu().long(), want)
+        w = w.cpu()
+        assert torch.isnan(w[:3][want[:3] >= 0]).all(), w[:3]
+        assert (w[want < 0] == 0).all()
+        assert not torch.isnan(w[3]).any()
+        assert torch.isnan(loss)
