@@ -77,10 +77,11 @@ __device__ __forceinline__ uint32_t row_min_u32(uint32_t v) {
     if constexpr ((1 << STEP) < LPR) return row_min_u32<LPR, STEP + 1>(min(v, partner<STEP>(v)));
     else return v;
 }
-// Unsigned keys in the order of the floats, and back.
+// Unsigned keys in the order of the floats, and back.  NaN, of either sign (0 / 0 is a
+// negative one on many machines), is above all numbers: its row picks it.
 __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);   // (-0 counts as 0)
-    return b ^ (static_cast<uint32_t>(static_cast<int>(b) >> 31) | 0x80000000u);
+    return v != v ? 0xFFFFFFFFu : b ^ (static_cast<uint32_t>(static_cast<int>(b) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
     return __builtin_bit_cast(float, k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));

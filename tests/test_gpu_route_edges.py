@@ -67,8 +67,8 @@ def nan_rows(E, dtype, sign):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, BF], ids=["fp32", "bf16"])
-@pytest.mark.parametrize("sign", [1], ids=["positive"])
-def test_a_nan_makes_its_rows_picks_nan(dev, sign, dtype):
+@pytest.mark.parametrize("sign", [1, -1], ids=["positive", "negative"])
+def test_a_nan_of_either_sign_makes_its_rows_picks_nan(dev, sign, dtype):
     for E, k in ((1, 1), (5, 1), (5, 3), (64, 4), (300, 16)):
         z = nan_rows(E, dtype, sign)
         M = z.shape[0]
