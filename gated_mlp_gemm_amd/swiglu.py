@@ -592,31 +592,59 @@ def swiglu_route_backward(logits: torch.Tensor, ids: torch.Tensor, weights: torc
 # ---------------------------------------------------------------------------
 class SwigluLora:
     """A table of low-rank adapters beside a projection: A [count, parts * rank, K],
-    B [count, columns, rank] (bfloat16) and scale [count] (float32), checked once
-    here.  parts is 2 beside W_fused (columns 2N, Gate and Up rows interleaved as
-    in it; A's first `rank` rows Gate's), 1 beside W3t."""
-    __slots__ = ("A", "B", "scale", "count", "rank", "columns", "a_rows", "K", "_args")
+    B [count, columns, rank] (bfloat16) and scale [count] (float32).  parts is 2
+    beside W_fused (columns 2N, Gate and Up rows interleaved as in it; A's first
+    `rank` rows Gate's), 1 beside W3t.  The tensors may be exchanged later: each call
+    takes, and checks, those that the table holds then."""
+    __slots__ = ("A", "B", "scale")
 
     def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor):
+        self.A, self.B, self.scale = A, B, scale
+        self._checked()
+
+    def _checked(self):
+        """(A, B) once the three fit one another."""
+        A, B = self.A, self.B
         for name, t in (("A", A), ("B", B)):
             if not isinstance(t, torch.Tensor):
                 raise TypeError(f"{name} must be a torch.Tensor")
             if t.dim() != 3:
                 raise ValueError(f"{name} must have three dimensions, got {tuple(t.shape)}")
-        self.count, self.a_rows, self.K = A.shape
-        self.columns, self.rank = B.shape[1], B.shape[2]
-        self.A = _dev_tensor(A, "A", (self.count, self.a_rows, self.K))
-        self.B = _dev_tensor(B, "B", (self.count, self.columns, self.rank))
-        self.scale = _dev_typed(scale, "scale", torch.float32, (self.count,))
-        self._args = (A.data_ptr(), B.data_ptr(), scale.data_ptr(), self.count, self.rank)
+        count = A.shape[0]
+        _dev_tensor(A, "A", A.shape)
+        _dev_tensor(B, "B", (count, B.shape[1], B.shape[2]))
+        _dev_typed(self.scale, "scale", torch.float32, (count,))
+        return A, B
+
+    @property
+    def count(self) -> int:
+        return self.A.shape[0]
+
+    @property
+    def a_rows(self) -> int:
+        return self.A.shape[1]
+
+    @property
+    def K(self) -> int:
+        return self.A.shape[2]
+
+    @property
+    def columns(self) -> int:
+        return self.B.shape[1]
+
+    @property
+    def rank(self) -> int:
+        return self.B.shape[2]
 
     def _beside(self, name: str, parts: int, columns: int, K: int):
         """The C arguments, once the table is one for a [columns, K] weight."""
-        if (self.columns, self.K, self.a_rows) != (columns, K, parts * self.rank):
+        A, B = self._checked()
+        (count, a_rows, a_k), (_, b_columns, rank) = A.shape, B.shape
+        if (b_columns, a_k, a_rows) != (columns, K, parts * rank):
             raise ValueError(
-                f"{name}: A {tuple(self.A.shape)} and B {tuple(self.B.shape)} do not fit a "
+                f"{name}: A {tuple(A.shape)} and B {tuple(B.shape)} do not fit a "
                 f"[{columns}, {K}] weight with {parts} part(s)")
-        return self._args
+        return A.data_ptr(), B.data_ptr(), self.scale.data_ptr(), count, rank
 
 
 def swiglu_lora_workspace_size(M: int, N: int, K: int, slots: int, rank: int) -> int:
