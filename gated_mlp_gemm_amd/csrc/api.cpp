@@ -784,10 +784,13 @@ int swiglu_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t slots, i
                                uint64_t *bytes) {
     if (!bytes) return fail(SWIGLU_ERR_NULL, "bytes is required");
     *bytes = 0;
-    int st = check_gemm_shape(M, N, K);
+    // the sizes of either projection: Gate and Up's K is at most 2^21, the down
+    // projection's N
+    int st = check_down_shape(M, N, K);
+    if (st != SWIGLU_OK) st = check_gemm_shape(M, N, K);
     if (st == SWIGLU_OK) st = check_lora(slots, 1, rank);
     if (st != SWIGLU_OK) return st;
-    if (M == 0 || N == 0) return ok();
+    if (M == 0 || N == 0 || K == 0) return ok();
     int cus = 0;
     st = check_device(&cus);
     if (st != SWIGLU_OK) return st;

@@ -385,7 +385,8 @@ int swiglu_route_backward(const void *logits, int logits_type, const uint8_t *va
  * rounded up to 256, and another ceil(M / 256) * (4112 + 2 c), c being
  * min(count, 256 slots) rounded up to a multiple of 8, rounded up to 256; with
  * swiglu_lora_workspace_size() bytes the calls may also split K, as without
- * adapters.
+ * adapters.  Its M, N and K are the block's: N the hidden width, K the model's
+ * (the down projection's D), each as large as the call that it is for takes.
  */
 int swiglu_lora_workspace_size(int64_t M, int64_t N, int64_t K, int64_t slots, int64_t rank,
                                uint64_t *bytes);

@@ -1,5 +1,5 @@
 """The binding of the calls with low-rank adapters (needs an MI355X): what a table
-holds at the time of the call counts."""
+holds at the time of the call counts, and the sizes that the C calls take."""
 from __future__ import annotations
 
 import pytest
@@ -70,3 +70,26 @@ def test_a_tables_tensors_are_checked_at_the_call(dev):
     grown.A, grown.B = torch.cat([A, A], 1), torch.cat([B, B], 2)
     assert (grown.rank, grown.count, grown.columns, grown.K) == (2 * r, L, D, N)
     assert not sw.swiglu_down_proj_lora(h, w, grown, ids).any()
+
+
+@pytest.mark.parametrize("D", [0, (1 << 21) + 8, 1 << 22])
+def test_down_projection_columns_without_a_workspace(dev, D):
+    """The binding sizes its own workspace for every D that the C call takes."""
+    print(f"\n[case] down projection D={D}", flush=True)
+    M, N, L, r = 3, 16, 2, 8
+    g = torch.Generator(device=dev).manual_seed(5)
+    h = torch.randn(M, N, generator=g, device=dev).to(BF)
+    w = torch.randn(D, N, generator=g, device=dev).to(BF)
+    A, B, scale = tensors(dev, L, D, N, r, 6)
+    ids = torch.tensor([[0], [-1], [1]], dtype=torch.int32, device=dev)
+    out = sw.swiglu_down_proj_lora(h, w, sw.SwigluLora(A, B, scale), ids)
+    torch.cuda.synchronize()
+    assert out.shape == (M, D)
+    x = h.double()
+    want, size = x @ w.double().t(), x.abs() @ w.double().abs().t()
+    for m, n in ((0, 0), (2, 1)):
+        t = (A[n].double() @ x[m]) * scale[n].double()
+        want[m] += B[n].double() @ t
+        size[m] += B[n].double().abs() @ (A[n].double().abs() @ x[m].abs()) * scale[n].double()
+    # sums of 16 and 8 terms in fp32 and T in 16 bits: 2^-15 of the magnitudes; one bf16 rounding
+    assert ((out.double() - want).abs() <= 2.0 ** -14 * size + 2.0 ** -8 * want.abs()).all()
