@@ -867,9 +867,13 @@ struct Pipeline {
         for (; t < t_end; ++t) step(issue, t, total, acc, [](int) {});
     }
 
+    // The fragments read behind the last step are used by nothing, but their
+    // registers have to stay theirs until the reads have landed (wait_frags()
+    // uses them behind its wait: an address in one of them would be overwritten).
     __device__ __forceinline__ void drain() {
+        static_assert(S::kKSub % 2 == 0, "the reads behind a step are into f[0]");
         wait_vmcnt<0>();
-        wait_lgkmcnt0();
+        wait_frags<S>(f[0]);
         block_barrier();
         // the last assembly MFMAs' results are read from here on
         if constexpr (S::MI == 16) wait_mfma_results();

@@ -409,8 +409,7 @@ struct LoraExpand {
                     }
                 };
                 u32x4 bf[2][S::TN][2], tf[2][kRows][kParts][2];
-                auto have = [&](u32x4 (&ft)[kRows][kParts][2], u32x4 (&fb)[S::TN][2]) {
-                    asm volatile("s_waitcnt lgkmcnt(0)");
+                auto keep = [&](u32x4 (&ft)[kRows][kParts][2], u32x4 (&fb)[S::TN][2]) {
 #pragma unroll
                     for (int t = 0; t < kRows; ++t)
 #pragma unroll
@@ -421,6 +420,10 @@ struct LoraExpand {
                     for (int c = 0; c < S::TN; ++c)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) asm volatile("" : "+v"(fb[c][h]));
+                };
+                auto have = [&](u32x4 (&ft)[kRows][kParts][2], u32x4 (&fb)[S::TN][2]) {
+                    asm volatile("s_waitcnt lgkmcnt(0)");
+                    keep(ft, fb);
                 };
                 // step 0
                 Look look = look_at(0, pair0);
@@ -439,6 +442,10 @@ struct LoraExpand {
                     for_each(std::make_integer_sequence<int, kGroups>{}, [&](auto group_) {
                         constexpr int group = decltype(group_)::value;
                         have(tf[(first + group) % 2], bf[buf]);
+                        // Registers that reads are in flight to stay theirs until this wait or
+                        // the one behind the loop, on every path of the compiled code (also
+                        // on those that no number of steps takes: it joins the two exits).
+                        if constexpr (group == 0) keep(tf[(first + 1) % 2], bf[buf ^ 1]);
                         constexpr bool next = group + 1 == kGroups;   // the next reads are the next step's
                         if constexpr (next) {
                             if (s + 1 < steps && (s + 1) % kSteps == 0) {
@@ -477,7 +484,9 @@ struct LoraExpand {
                     if (s + 1 < steps) step(s + 1, k1);
                 }
                 wait_vmcnt<0>();
-                wait_lgkmcnt0();
+                // (the reads of the step behind the last)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) have(tf[i], bf[i]);
                 block_barrier();   // T and the ring are free
             }
         wait_mfma_results();
