@@ -105,6 +105,9 @@ __device__ __forceinline__ uint32_t asm_read_u16(uint32_t addr) {
 __device__ __forceinline__ void asm_write_b128(uint32_t addr, const u32x4 &v) {
     asm volatile("ds_write_b128 %0, %1" ::"v"(addr), "v"(v) : "memory");
 }
+__device__ __forceinline__ void asm_write_b32(uint32_t addr, uint32_t v) {
+    asm volatile("ds_write_b32 %0, %1" ::"v"(addr), "v"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t landed(uint32_t v) {
     asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(v));
     return v;
@@ -248,10 +251,13 @@ struct LoraExpand {
                     }
     }
 
-    // Whether the wave's columns met an infinity or NaN in B (then mend()).
+    // Whether the wave's columns met an infinity or NaN in B: then the accumulators are
+    // worthless, and the tile is done again with `clean` (which returns false).  That one
+    // makes zeros of them in the LDS (each wave of what it loaded) and adds what they are
+    // to the rows that name their adapter (add_broken).
     __device__ __forceinline__ bool run(SWIGLU_LDS char *lds, const LoraTerm &x,
-                                        typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0) const {
-        if (steps == 0) return false;
+                                        typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0,
+                                        bool clean) const {
         const int tid = thread(), lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / S::WN, wn = wave % S::WN;
@@ -267,11 +273,14 @@ struct LoraExpand {
             make_rsrc(x.T + static_cast<int64_t>(m0) * (row_bytes / 2),
                       static_cast<uint32_t>(min(S::BM, x.M - m0) * row_bytes));
         // where of the tile's rows: one of the four planes a wave; ids: 1 KiB a wave
-        dma16(pr, lds + wave * 1024, static_cast<uint32_t>(kPlanWhere + (m0 % kPlanRows) * 4) + lane * 16u,
-              wave * (kPlanRows * 4));
-        dma16(pr, lds + kIds + wave * 1024, kPlanIds + lane * 16u, wave * 1024);
-        for (int i = wave; i < kRowBlocks; i += 4)
-            asm_write_b128(at + kZeros + i * 1024 + lane * 16u, u32x4{0u, 0u, 0u, 0u});
+        if (steps > 0) {
+            dma16(pr, lds + wave * 1024,
+                  static_cast<uint32_t>(kPlanWhere + (m0 % kPlanRows) * 4) + lane * 16u,
+                  wave * (kPlanRows * 4));
+            dma16(pr, lds + kIds + wave * 1024, kPlanIds + lane * 16u, wave * 1024);
+            for (int i = wave; i < kRowBlocks; i += 4)
+                asm_write_b128(at + kZeros + i * 1024 + lane * 16u, u32x4{0u, 0u, 0u, 0u});
+        }
 
         uint32_t col[kDma];   // elements from an adapter's B to the lane's rows
 #pragma unroll
@@ -297,7 +306,8 @@ struct LoraExpand {
         const uint32_t b_read = at + kRing + (wn * S::kWaveN + r16) * 64u + ((g ^ swizzle(r16)) * 16u);
 
 #pragma nounroll
-        for (int j0 = 0; j0 < x.slots; j0 += by.slots)
+        // (no steps: nothing to expand; one way out, so that the accumulators stay in place)
+        for (int j0 = steps > 0 ? 0 : x.slots; j0 < x.slots; j0 += by.slots)
 #pragma nounroll
             for (int r0 = 0; r0 < rank8; r0 += mask + 1) {
                 // T: a wave a quarter of the rows, 16 rows of a plane a load.  (Past the
@@ -336,6 +346,13 @@ struct LoraExpand {
 #pragma unroll
                     for (int j = 0; j < kDma; ++j) gdma16(p + col[j], to + j * 4096);
                 };
+                auto clear_stage = [&](int stage) {   // (what issue_b of this lane brought)
+#pragma nounroll
+                    for (int i = 0; i < kSteps * kDma; ++i)
+                        clear_lds(at + kRing + (stage % kStages) * (kSteps * kStepBytes) +
+                                  i / kDma * kStepBytes + i % kDma * 4096 + wave * 1024 + lane * 16u);
+                    wait_lgkmcnt0();
+                };
                 auto next_stage = [&](int stage) {
                     uint32_t of[kSteps];
 #pragma unroll
@@ -349,6 +366,17 @@ struct LoraExpand {
 #pragma unroll
                 for (int s = 0; s < kEarly; ++s) issue_b(s, id[s]);
                 wait_vmcnt<(kStages - 2) * kSteps * kDma>();
+                if (__builtin_expect(clean, 0)) {
+                    const int row16 = kFewRows ? wave : wave * (S::BM / 64);
+                    uint32_t to = at + kT + row16 * 1024 + lane * 16u;
+#pragma nounroll
+                    for (int sp = 0; sp < by.slots * kParts * planes_part; ++sp, to += t_plane)
+#pragma nounroll
+                        for (int t = 0; kFewRows ? (row16 + t) * 1024 < t_plane : t < S::BM / 64;
+                             t += kFewRows ? 4 : 1)
+                            clear_lds(to + t * 1024);
+                    clear_stage(0);
+                }
                 wait_lgkmcnt0();
                 block_barrier();   // the plan, T and stage 0 are there
                 next_stage(kStages - 1);
@@ -451,6 +479,7 @@ struct LoraExpand {
                             if (s + 1 < steps && (s + 1) % kSteps == 0) {
                                 // the next stage is there, and everyone has read this one
                                 wait_vmcnt<(kStages - 2) * kSteps * kDma>();
+                                if (__builtin_expect(clean, 0)) clear_stage((s + 1) / kSteps);
                                 block_barrier();
                                 next_stage((s + 1) / kSteps + kStages - 1);
                             }
@@ -497,33 +526,108 @@ struct LoraExpand {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) asm volatile("" : "+a"(acc[a][c].v[q]));
         asm volatile("" : "+v"(met));
+        if (__builtin_expect(clean, 0)) {
+            if (steps > 0) add_broken(x, acc, m0, n0);
+            return false;
+        }
         // (all rows of zeros: one tells of its column)
         return __builtin_amdgcn_ballot_w64(met[0] != met[0]) != 0;
     }
 
-    // The NaN among the wave's results again, from the formula: K elements [k0, k1) of the
-    // shared product, then what the piece's steps take of the row's own adapters.  (A lane an element, from memory: for
-    // adapters that are broken, so that they break no row but their own.)
-    __device__ __forceinline__ void mend(const LoraTerm &x, const KMajor &X, const KMajor &W, int K,
-                                         int k0, int k1, typename S::Acc (&acc)[S::TM][S::TN], int m0,
-                                         int n0) const {
+    // Whether run() returned true to any wave of the workgroup, for all of them (whose LDS
+    // is idle; a barrier has to stand before its next use).
+    __device__ __forceinline__ static bool any_wave(SWIGLU_LDS char *lds, bool mine) {
+        if constexpr (S::WN == 1) return mine;   // (all have the same columns)
+        const int tid = thread();
+        const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(lds));
+        if ((tid & 63) == 0) asm_write_b32(at + (tid >> 6) * 4u, mine ? 1u : 0u);
+        wait_lgkmcnt0();
+        block_barrier();
+        u32x4 all = read_one(at, 0);
+        asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(all));
+        return __builtin_amdgcn_readfirstlane(
+                   static_cast<int>(all[0] | all[1] | all[2] | all[3])) != 0;
+    }
+
+    // Infinities and NaN become zeros; whether there were any.
+    __device__ __forceinline__ static bool clear_broken(u32x4 &v) {
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool lo = (v[i] & 0x7F80u) == 0x7F80u, hi = (v[i] & 0x7F800000u) == 0x7F800000u;
+            v[i] &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0x0000FFFFu : ~0u);
+            any = any || lo || hi;
+        }
+        return any;
+    }
+
+    // The same of 16 bytes of LDS.
+    __device__ __forceinline__ static void clear_lds(uint32_t addr) {
+        u32x4 v = read_one(addr, 0);
+        asm volatile("s_waitcnt lgkmcnt(0)" : "+v"(v));
+        clear_broken(v);
+        asm_write_b128(addr, v);
+    }
+
+    // The terms that a clean expansion left out, of the row's own adapters: those with
+    // an infinity or NaN in B or in T.  A lane an element, from memory.
+    __device__ __forceinline__ void add_broken(const LoraTerm &x, S::Acc (&acc)[S::TM][S::TN], int m0,
+                                               int n0) const {
         constexpr int kQuads = S::TM * S::TN * 4;
-        const int shift = kQuarter ? x.quarter.shift : x.whole.shift;
+        static_assert(kRowBlocks <= 8, "a bit a row");
+        const int shift = kQuarter ? x.quarter.shift : x.whole.shift, rank8 = x.rank / 8;
         const int tid = thread(), lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / S::WN, wn = wave % S::WN;
         const char *plan = x.plans + static_cast<int64_t>(m0 / kPlanRows) * x.plan_bytes;
         const uint32_t *where = reinterpret_cast<const uint32_t *>(plan + kPlanWhere);
         const uint16_t *ids = reinterpret_cast<const uint16_t *>(plan + kPlanIds);
-        auto value = [](uint16_t v) {
-            return __builtin_bit_cast(float, static_cast<uint32_t>(v) << 16);
+        const int row0 = m0 + wm * S::kWaveM + (lane >> 4) * 4;   // of row block 0
+        auto adapter = [&](int row, int j) {   // 1 + its list index, 0: none
+            return static_cast<int>(where[j / 2 * kPlanRows + row % kPlanRows] >> (16 * (j % 2)) & 0xFFFFu);
         };
+        auto t_of = [&](int row, int j, int part) {
+            return reinterpret_cast<const u32x4 *>(
+                x.T + ((static_cast<int64_t>(row) * x.slots + j) * kParts + part) * x.rank * 2);
+        };
+        auto column = [&](int i) {   // of 16-column block i
+            const int pc = wn * S::kWaveN + i * 16 + (lane & 15);
+            return n0 + (kGated ? pair_row(pc) : pc);
+        };
+        auto b_of = [&](int at, int col) {
+            return reinterpret_cast<const u32x4 *>(
+                x.B + (static_cast<int64_t>(ids[at]) * x.cols + col) * x.rank);
+        };
+        uint32_t columns = 0u;   // those in which some adapter of the plan has some, a bit each
+#pragma nounroll
+        for (int i = 0; i < 2 * S::TN; ++i) {
+            const int col = column(i);
+            bool any = false;
+            for (int at = 0; at < n && col < x.cols; ++at)
+#pragma unroll 4
+                for (int c = 0; c < rank8; ++c) {
+                    u32x4 b = b_of(at, col)[c];
+                    any |= clear_broken(b);
+                }
+            columns |= static_cast<uint32_t>(any) << i;
+        }
+        uint32_t rows = 0u;   // rows whose T has some, bit 4 (row block) + e
+#pragma nounroll
+        for (int i = 0; i < kRowBlocks * 4; ++i) {
+            const int row = row0 + i / 4 * 16 + i % 4;
+            bool any = false;
+            for (int j = 0; j < x.slots && row < x.M; ++j)
+                for (int c = 0; c < kParts * rank8 && adapter(row, j); ++c) {
+                    u32x4 t = t_of(row, j, 0)[2 * c];
+                    any |= clear_broken(t);
+                }
+            rows |= static_cast<uint32_t>(any) << i;
+        }
 #pragma nounroll
         for (int i = 0; i < kQuads; ++i) {
-            const int block = i / 4 % S::TN;
-            const int pc = wn * S::kWaveN + block * 32 + (i & 1) * 16 + (lane & 15);
-            const int col = n0 + (kGated ? pair_row(pc) : pc);
-            int row = m0 + wm * S::kWaveM + i / (4 * S::TN) * 32 + (i >> 1 & 1) * 16 + (lane >> 4) * 4;
+            const int block = i / 4 % S::TN, rb = i / (4 * S::TN) * 2 + (i >> 1 & 1);
+            const int at_col = 2 * block + (i & 1), col = column(at_col);
+            const uint32_t wanted = columns >> at_col & 1u ? 15u : rows >> (4 * rb) & 15u;
             f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int q = 0; q < kQuads; ++q)
@@ -532,32 +636,33 @@ struct LoraExpand {
                     asm volatile("" : "+v"(v));
                 }
 #pragma nounroll
-            for (int e = 0; e < 4; ++e, ++row) {
+            for (int e = 0; e < 4; ++e) {
+                const int row = row0 + 16 * rb + e;
                 float sum = v[0];
-                if (sum != sum && row < x.M && col < x.cols) {
-                    const uint16_t *xr = static_cast<const uint16_t *>(X.base) +
-                                         (static_cast<int64_t>(row) * X.stride + X.offset) * (X.ld ? X.ld : K);
-                    const uint16_t *wr = static_cast<const uint16_t *>(W.base) +
-                                         (static_cast<int64_t>(col) * W.stride + W.offset) * (W.ld ? W.ld : K);
-                    sum = 0.0f;
-                    for (int k = k0; k < k1; ++k) sum = fmaf(value(xr[k]), value(wr[k]), sum);
+                if ((wanted >> e & 1u) && row < x.M && col < x.cols)
                     for (int j = 0; j < x.slots; ++j) {
-                        const int at =
-                            where[j / 2 * kPlanRows + row % kPlanRows] >> (16 * (j % 2)) & 0xFFFFu;
-                        if (at == 0) continue;
-                        const uint16_t *b =
-                            x.B + (static_cast<int64_t>(ids[at - 1]) * x.cols + col) * x.rank;
-                        const uint16_t *t =
-                            x.T + ((static_cast<int64_t>(row) * x.slots + j) * kParts +
-                                   (kGated ? block % 2 : 0)) * x.rank * 2;
-                        for (int r = 0; r < x.rank; ++r) {
-                            const int step = (((at - 1) << shift) | (r / 8 & ((1 << shift) - 1))) / 4 - first;
-                            if (step < 0 || step >= steps) continue;
-                            const uint16_t *h = t + (r & ~7) * 2 + (r & 7);
-                            sum = fmaf(value(h[0]) + value(h[8]), value(b[r]), sum);
+                        const int at = adapter(row, j) - 1;
+                        if (at < 0) continue;
+                        const u32x4 *b = b_of(at, col), *t = t_of(row, j, kGated ? block % 2 : 0);
+#pragma unroll 4
+                        for (int c = 0; c < rank8; ++c) {
+                            // (of the piece's own steps)
+                            const int step = (at << shift | (c & ((1 << shift) - 1))) / 4 - first;
+                            const u32x4 bv = b[c], hi = t[2 * c], lo = t[2 * c + 1];
+                            u32x4 b0 = bv, t0 = hi;
+                            const bool any = clear_broken(b0) | clear_broken(t0);
+                            if (!any || step < 0 || step >= steps) continue;
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                auto value = [&](const u32x4 &v) {
+                                    return __builtin_bit_cast(
+                                        float, q % 2 ? v[q / 2] & 0xFFFF0000u : v[q / 2] << 16);
+                                };
+                                if (value(bv) != value(b0) || value(hi) != value(t0))
+                                    sum = fmaf(value(hi) + value(lo), value(bv), sum);
+                            }
                         }
                     }
-                }
                 v = f32x4{v[1], v[2], v[3], sum};
             }
 #pragma unroll

@@ -284,25 +284,37 @@ struct WithLora : Base {
 };
 using PairMulLora = WithLora<PairMulEpilogue>;
 using StoreLora = WithLora<StoreEpilogue>;
-// begin() before a tile's K steps [kb, ke) of BK elements, run() behind them.
+// begin() before a tile's K steps, run() behind them.  run() is true where the wave met an
+// infinity or NaN in an adapter's B; if any() wave did, the workgroup does its tiles again
+// with `clean`, where run() keeps them to the rows that name the adapter.
 template <class S, class Epi, bool kQuarter = false>
 struct Adapters {
+    static constexpr bool kThere = false;
+    __device__ __forceinline__ static int thread() { return threadIdx.x; }   // of what stores the tile
+    __device__ __forceinline__ static bool any(SWIGLU_LDS char *, bool) { return false; }
     __device__ __forceinline__ void begin(const Epi &, int, int = 0, int = 1) {}
-    __device__ __forceinline__ void run(SWIGLU_LDS char *, const Epi &, const KMajor &, const KMajor &,
-                                        int, int, int, typename S::Acc (&)[S::TM][S::TN], int, int) {}
+    __device__ __forceinline__ bool run(SWIGLU_LDS char *, const Epi &,
+                                        typename S::Acc (&)[S::TM][S::TN], int, int, bool) {
+        return false;
+    }
 };
 template <class S, class Base, bool kQuarter>
 struct Adapters<S, WithLora<Base>, kQuarter> {
-    LoraExpand<S, std::is_same<Base, PairMulEpilogue>::value, kQuarter> expand;
+    static constexpr bool kThere = true;
+    using Expand = LoraExpand<S, std::is_same<Base, PairMulEpilogue>::value, kQuarter>;
+    Expand expand;
+    __device__ __forceinline__ static int thread() { return Expand::thread(); }
+    __device__ __forceinline__ static bool any(SWIGLU_LDS char *lds, bool mine) {
+        return Expand::any_wave(lds, mine);
+    }
     __device__ __forceinline__ void begin(const WithLora<Base> &epi, int m0, int piece = 0,
                                           int pieces = 1) {
         expand.begin(epi.lora, m0, piece, pieces);
     }
-    __device__ __forceinline__ void run(SWIGLU_LDS char *lds, const WithLora<Base> &epi,
-                                        const KMajor &A, const KMajor &B, int K, int kb, int ke,
-                                        typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0) {
-        if (expand.run(lds, epi.lora, acc, m0, n0))
-            expand.mend(epi.lora, A, B, K, kb * S::BK, min(ke * S::BK, K), acc, m0, n0);
+    __device__ __forceinline__ bool run(SWIGLU_LDS char *lds, const WithLora<Base> &epi,
+                                        typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0,
+                                        bool clean) {
+        return expand.run(lds, epi.lora, acc, m0, n0, clean);
     }
 };
 
@@ -381,14 +393,18 @@ enum TailMode { kTailNone = 0, kTailSplit = 1, kTailQuarter = 2, kTailReduceInKe
 //
 // kEven: K is a multiple of BK (the loads' offsets are fixed per tile, see
 // PanelLoader::issue); the kernel runs the body compiled for its K.
+// Returns whether the wave met a broken adapter: then all of it is done again with `clean`
+// (results and partials that are stored twice are stored by the same lanes; a tile reduced in
+// the kernel is done again before it is).
 template <class S, class Epi, int TAIL, bool kEven>
-__device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, const KMajor &B,
+__device__ __forceinline__ bool gemm_tiles_body(char *smem, const KMajor &Ak, const KMajor &B,
                                                 int M, int K, const Epi &epi,
-                                                const Schedule &sch) {
+                                                const Schedule &sch, bool clean) {
     SWIGLU_LDS char *lds = (SWIGLU_LDS char *)smem;
     const int b = blockIdx.x;
     const int grid = sch.grid;
 
+    bool met = false;   // (adapters only)
     auto whole_tiles = [&] {
         if (b < sch.dp) {
             Pipeline<S> pl;
@@ -412,14 +428,14 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
                 pl.prologue_wait();
                 run_tile<S, kEven>(pl, issue, nk, acc);
                 pl.drain(acc);
-                adapters.run(lds, epi, Ak, B, K, 0, nk, acc, m0, n0);
+                met |= adapters.run(lds, epi, acc, m0, n0, clean);
                 if (j + grid < sch.dp) {
                     tile_coords(xcd_order(j + grid, sch.dp), sch.tiles_m, sch.tiles_n, sch.group_m, tm,
                                 tn);
                     ld.init(Ak, tm * S::BM, B, tn * S::BN, K);
                     pl.prologue_issue(issue);
                 }
-                epi.template apply<S>(acc, m0, n0, threadIdx.x);
+                epi.template apply<S>(acc, m0, n0, adapters.thread());
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -443,8 +459,8 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             Adapters<Q, Epi, true> adapters;
             adapters.begin(epi, m0);
             tile_mainloop<Q, kEven>(lds, Ak, B, M, K, m0, n0, 0, sch.nk, sch.nk, acc);
-            adapters.run(lds, epi, Ak, B, K, 0, sch.nk, acc, m0, n0);
-            epi.template apply<Q>(acc, m0, n0, threadIdx.x);
+            met |= adapters.run(lds, epi, acc, m0, n0, clean);
+            epi.template apply<Q>(acc, m0, n0, adapters.thread());
         }
         whole_tiles();
     } else {
@@ -467,9 +483,15 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             tile_coords(sch.dp + i, sch.tiles_m, sch.tiles_n, sch.group_m, tm, tn);
             typename S::Acc acc[S::TM][S::TN];
             Adapters<S, Epi> adapters;
-            adapters.begin(epi, tm * S::BM, piece, sch.pieces);
-            tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
-            adapters.run(lds, epi, Ak, B, K, kb, ke, acc, tm * S::BM, tn * S::BN);
+            // (the others read its partial once it has arrived: done again before)
+            for (bool again = false;; again = true) {
+                adapters.begin(epi, tm * S::BM, piece, sch.pieces);
+                tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
+                const bool broken = adapters.run(lds, epi, acc, tm * S::BM, tn * S::BN, again);
+                const bool any = adapters.any(lds, broken);
+                if constexpr (adapters.kThere) block_barrier();
+                if (!any) break;
+            }
             const float *slots = sch.partials + static_cast<int64_t>(i) * sch.pieces * S::BM * S::BN;
             if (threadIdx.x == 0) meeting.settle(sch.arrivals + i, sch.tag);
             store_partial_coherent<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN,
@@ -512,9 +534,23 @@ __device__ __forceinline__ void gemm_tiles_body(char *smem, const KMajor &Ak, co
             Adapters<S, Epi> adapters;
             adapters.begin(epi, tm * S::BM, piece, sch.pieces);
             tile_mainloop<S, kEven>(lds, Ak, B, M, K, tm * S::BM, tn * S::BN, kb, ke, sch.nk, acc);
-            adapters.run(lds, epi, Ak, B, K, kb, ke, acc, tm * S::BM, tn * S::BN);
+            met |= adapters.run(lds, epi, acc, tm * S::BM, tn * S::BN, clean);
             store_partial<S>(sch.partials + static_cast<int64_t>(j) * S::BM * S::BN, acc,
-                             threadIdx.x);
+                             adapters.thread());
+        }
+    }
+    return met;
+}
+template <class S, class Epi, int TAIL, bool kEven>
+__device__ __forceinline__ void gemm_tiles_run(char *smem, const KMajor &Ak, const KMajor &B, int M,
+                                               int K, const Epi &epi, const Schedule &sch) {
+    if constexpr (!Adapters<S, Epi>::kThere || TAIL == kTailReduceInKernel) {
+        gemm_tiles_body<S, Epi, TAIL, kEven>(smem, Ak, B, M, K, epi, sch, false);
+    } else {
+        for (bool clean = false;; clean = true) {
+            const bool met = gemm_tiles_body<S, Epi, TAIL, kEven>(smem, Ak, B, M, K, epi, sch, clean);
+            if (__builtin_expect(!Adapters<S, Epi>::any((SWIGLU_LDS char *)smem, met), 1)) break;
+            block_barrier();
         }
     }
 }
@@ -522,8 +558,8 @@ template <class S, class Epi, int TAIL>
 __global__ __launch_bounds__(S::kThreads, S::kOccupancy) void gemm_tiles_kernel(
     KMajor Ak, KMajor B, int M, int K, Epi epi, Schedule sch) {
     __shared__ __attribute__((aligned(128))) char smem[S::kLdsBytes];
-    if (K % S::BK == 0) gemm_tiles_body<S, Epi, TAIL, true>(smem, Ak, B, M, K, epi, sch);
-    else gemm_tiles_body<S, Epi, TAIL, false>(smem, Ak, B, M, K, epi, sch);
+    if (K % S::BK == 0) gemm_tiles_run<S, Epi, TAIL, true>(smem, Ak, B, M, K, epi, sch);
+    else gemm_tiles_run<S, Epi, TAIL, false>(smem, Ak, B, M, K, epi, sch);
 }
 
 // The split tiles' epilogue: one single-wave workgroup per (split tile, GEMM

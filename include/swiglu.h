@@ -373,9 +373,10 @@ int swiglu_route_backward(const void *logits, int logits_type, const uint8_t *va
  * X . A^T times weight and scale is held as two bf16 numbers (16 bits of its
  * value) for the product with B; all sums are fp32, Y, H and Out are rounded
  * once.  Results are bitwise
- * reproducible for the same arguments and workspace size.  A row's result does
- * not depend on other rows' ids (infinities and NaN in an adapter stay in the
- * rows that name it; elements beside them may differ in the sums' order).
+ * reproducible for the same arguments and workspace size.  A row's result is its
+ * formula's whatever other rows name (infinities and NaN in an adapter stay in the
+ * rows that name it), but the order of its sums, and so its last bits, may depend on
+ * which adapters they are.
  * Preconditions: those of the call without adapters; 1 <= slots <= 8; rank a
  * multiple of 8 in [8, 256]; 1 <= count <= 8192; matrices 16-byte, ids,
  * weights and scale 4-byte aligned; outputs and workspace overlap nothing.
