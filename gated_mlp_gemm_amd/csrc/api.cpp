@@ -281,6 +281,28 @@ hipError_t lora_projection(const uint16_t *X, const uint16_t *W, uint16_t *Y, in
                                        (int)slots, T, plans, ws, s);
 }
 
+// Sizes of the training calls: rows of any count are contracted by the weights'
+// gradients, and N is also a contraction (2N columns of GU).
+constexpr int64_t kMaxTrainM = int64_t(1) << 30;
+constexpr int64_t kMaxTrainN = int64_t(1) << 20;
+int check_train_shape(int64_t M, int64_t N, int64_t K) {
+    int st = check_gemm_shape(M, N, K);
+    if (st != SWIGLU_OK) return st;
+    if (M > kMaxTrainM || N > kMaxTrainN)
+        return fail(SWIGLU_ERR_SHAPE, "size beyond limits (M<=2^30, N<=2^20)");
+    if (swiglu::max_tiles(2 * N, K) > 2147483647 || swiglu::max_tiles(M, K) > 2147483647)
+        return fail(SWIGLU_ERR_SHAPE, "tile grid too large");
+    return SWIGLU_OK;
+}
+int check_grad_type(int grad_type) {
+    if (grad_type != SWIGLU_F32 && grad_type != SWIGLU_BF16)
+        return fail(SWIGLU_ERR_UNSUPPORTED, "unknown gradient type %d", grad_type);
+    return SWIGLU_OK;
+}
+int grad_size(int grad_type) { return grad_type == SWIGLU_F32 ? 4 : 2; }
+// A sum that a weight's gradient is added to may be the gradient itself.
+const void *add_operand(const void *add, const void *dW) { return add == dW ? nullptr : add; }
+
 int launched(hipError_t e, const char *what) {
     if (e != hipSuccess) return fail(SWIGLU_ERR_HIP, "%s launch: %s", what, hipGetErrorString(e));
     return ok();
@@ -916,6 +938,190 @@ int swiglu_gated_mlp_lora(const uint16_t *X, const uint16_t *W_fused, const uint
     return launched(lora_projection(H, W3t, Out, M, K, N, false, down, ids, weights, slots,
                                     workspace, workspace_bytes, cus, s),
                     "gated MLP lora: down projection");
+}
+
+int swiglu_fused_gemm_train(const uint16_t *A, const uint16_t *W_fused, uint16_t *H, uint16_t *GU,
+                            int64_t M, int64_t N, int64_t K, void *workspace,
+                            uint64_t workspace_bytes, void *stream) {
+    int st = check_train_shape(M, N, K);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0 || N == 0) return ok();
+    const Operand ops[] = {
+        {"A", A, M * K * 2, 16, false, false},
+        {"W_fused", W_fused, 2 * N * K * 2, 16, false, false},
+        {"H", H, M * N * 2, 16, true, false},
+        {"GU", GU, 2 * M * N * 2, 16, true, false},
+        {"workspace", workspace, (int64_t)workspace_bytes, 256, true, true},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    return launched(swiglu::launch_fused_train(A, W_fused, H, GU, (int)M, (int)N, (int)K,
+                                               make_ws(workspace, workspace_bytes, cus),
+                                               (hipStream_t)stream),
+                    "fused training forward");
+}
+
+int swiglu_gated_mlp_train(const uint16_t *A, const uint16_t *W_fused, const uint16_t *W3t,
+                           uint16_t *H, uint16_t *GU, uint16_t *Out, int64_t M, int64_t N,
+                           int64_t K, void *workspace, uint64_t workspace_bytes, void *stream) {
+    int st = check_train_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_down_shape(M, N, K);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0) return ok();
+    const Operand ops[] = {
+        {"A", A, M * K * 2, 16, false, false},
+        {"W_fused", W_fused, 2 * N * K * 2, 16, false, false},
+        {"W3t", W3t, K * N * 2, 16, false, false},
+        {"H", H, M * N * 2, 16, true, false},
+        {"GU", GU, 2 * M * N * 2, 16, true, false},
+        {"Out", Out, M * K * 2, 16, true, false},
+        {"workspace", workspace, (int64_t)workspace_bytes, 256, true, true},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    const hipStream_t s = (hipStream_t)stream;
+    const swiglu::GemmWorkspace ws = make_ws(workspace, workspace_bytes, cus);
+    const hipError_t e =
+        swiglu::launch_fused_train(A, W_fused, H, GU, (int)M, (int)N, (int)K, ws, s);
+    if (e != hipSuccess) return launched(e, "gated MLP training forward: fused SwiGLU");
+    return launched(swiglu::launch_down_proj(H, W3t, Out, (int)M, (int)N, (int)K, ws, s),
+                    "gated MLP training forward: down projection");
+}
+
+int swiglu_down_proj_backward(const uint16_t *dOut, const uint16_t *H, const uint16_t *W3t,
+                              uint16_t *dH, void *dW3t, const void *dW3t_add, int grad_type,
+                              int64_t M, int64_t N, int64_t D, void *workspace,
+                              uint64_t workspace_bytes, void *stream) {
+    int st = check_grad_type(grad_type);
+    if (st == SWIGLU_OK) st = check_down_shape(M, N, D);
+    if (st != SWIGLU_OK) return st;
+    if (D < 8) return fail(SWIGLU_ERR_SHAPE, "D=%lld must be >= 8", (long long)D);
+    if (M > kMaxTrainM || D > kMaxK || swiglu::max_tiles(M, N) > 2147483647 ||
+        swiglu::max_tiles(D, N) > 2147483647)
+        return fail(SWIGLU_ERR_SHAPE, "size beyond limits (M<=2^30, D<=2^21, tile grids)");
+    if (!dH && !dW3t) return fail(SWIGLU_ERR_NULL, "dH or dW3t is required");
+    if (dW3t_add && !dW3t) return fail(SWIGLU_ERR_NULL, "dW3t_add without dW3t");
+    const bool none = M == 0;
+    const Operand ops[] = {
+        {"dOut", dOut, M * D * 2, 16, false, none},
+        {"H", H, M * N * 2, 16, false, none || !dW3t},
+        {"W3t", W3t, D * N * 2, 16, false, none || !dH},
+        {"dW3t_add", add_operand(dW3t_add, dW3t), D * N * grad_size(grad_type), 16, false, true},
+        {"dH", dH, M * N * 2, 16, true, true},
+        {"dW3t", dW3t, D * N * grad_size(grad_type), 16, true, true},
+        {"workspace", workspace, (int64_t)workspace_bytes, 256, true, true},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    const hipStream_t s = (hipStream_t)stream;
+    const swiglu::GemmWorkspace ws = make_ws(workspace, workspace_bytes, cus);
+    hipError_t e = hipSuccess;
+    if (dH && M > 0)
+        e = swiglu::launch_grad_input(dOut, W3t, dH, (int)M, (int)N, (int)D, ws, s);
+    if (e == hipSuccess && dW3t)
+        e = swiglu::launch_weight_grad(dOut, H, dW3t, dW3t_add, grad_type == SWIGLU_F32, (int)M,
+                                       (int)D, (int)N, ws, s);
+    return launched(e, "down projection backward");
+}
+
+int swiglu_fused_gemm_backward(const uint16_t *dH, const uint16_t *A, const uint16_t *W_fused,
+                               const uint16_t *GU, uint16_t *dGU, uint16_t *dA, void *dW_fused,
+                               const void *dW_fused_add, int grad_type, int64_t M, int64_t N,
+                               int64_t K, void *workspace, uint64_t workspace_bytes,
+                               void *stream) {
+    int st = check_grad_type(grad_type);
+    if (st == SWIGLU_OK) st = check_train_shape(M, N, K);
+    if (st != SWIGLU_OK) return st;
+    if (N < 8) return fail(SWIGLU_ERR_SHAPE, "N=%lld must be >= 8", (long long)N);
+    if (dW_fused_add && !dW_fused) return fail(SWIGLU_ERR_NULL, "dW_fused_add without dW_fused");
+    const bool none = M == 0;
+    const int64_t weight = 2 * N * K;
+    const Operand ops[] = {
+        {"dH", dH, M * N * 2, 16, false, none},
+        {"A", A, M * K * 2, 16, false, none || !dW_fused},
+        {"W_fused", W_fused, weight * 2, 16, false, none || !dA},
+        {"GU", GU == dGU ? nullptr : GU, 2 * M * N * 2, 16, false, none || GU == dGU},
+        {"dW_fused_add", add_operand(dW_fused_add, dW_fused), weight * grad_size(grad_type), 16,
+         false, true},
+        {"dGU", dGU, 2 * M * N * 2, 16, true, none},
+        {"dA", dA, M * K * 2, 16, true, true},
+        {"dW_fused", dW_fused, weight * grad_size(grad_type), 16, true, true},
+        {"workspace", workspace, (int64_t)workspace_bytes, 256, true, true},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    const hipStream_t s = (hipStream_t)stream;
+    const swiglu::GemmWorkspace ws = make_ws(workspace, workspace_bytes, cus);
+    hipError_t e = hipSuccess;
+    if (M > 0) e = swiglu::launch_gate_grad(dH, GU, dGU, M * N, s);
+    if (e == hipSuccess && dA && M > 0)
+        e = swiglu::launch_grad_input(dGU, W_fused, dA, (int)M, (int)K, (int)(2 * N), ws, s);
+    if (e == hipSuccess && dW_fused)
+        e = swiglu::launch_weight_grad(dGU, A, dW_fused, dW_fused_add, grad_type == SWIGLU_F32,
+                                       (int)M, (int)(2 * N), (int)K, ws, s);
+    return launched(e, "fused SwiGLU backward");
+}
+
+int swiglu_gated_mlp_backward(const uint16_t *dOut, const uint16_t *A, const uint16_t *W_fused,
+                              const uint16_t *W3t, const uint16_t *H, const uint16_t *GU,
+                              uint16_t *dGU, uint16_t *dA, void *dW_fused,
+                              const void *dW_fused_add, void *dW3t, const void *dW3t_add,
+                              int grad_type, int64_t M, int64_t N, int64_t K, void *workspace,
+                              uint64_t workspace_bytes, void *stream) {
+    int st = check_grad_type(grad_type);
+    if (st == SWIGLU_OK) st = check_train_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_down_shape(M, N, K);
+    if (st != SWIGLU_OK) return st;
+    if (dW_fused_add && !dW_fused) return fail(SWIGLU_ERR_NULL, "dW_fused_add without dW_fused");
+    if (dW3t_add && !dW3t) return fail(SWIGLU_ERR_NULL, "dW3t_add without dW3t");
+    const bool none = M == 0;
+    const int64_t weight = 2 * N * K, size = grad_size(grad_type);
+    const Operand ops[] = {
+        {"dOut", dOut, M * K * 2, 16, false, none},
+        {"A", A, M * K * 2, 16, false, none || !dW_fused},
+        {"W_fused", W_fused, weight * 2, 16, false, none || !dA},
+        {"W3t", W3t, weight, 16, false, none},
+        {"H", H, M * N * 2, 16, false, none || !dW3t},
+        {"GU", GU == dGU ? nullptr : GU, 2 * M * N * 2, 16, false, none || GU == dGU},
+        {"dW_fused_add", add_operand(dW_fused_add, dW_fused), weight * size, 16, false, true},
+        {"dW3t_add", add_operand(dW3t_add, dW3t), N * K * size, 16, false, true},
+        {"dGU", dGU, 2 * M * N * 2, 16, true, none},
+        {"dA", dA, M * K * 2, 16, true, true},
+        {"dW_fused", dW_fused, weight * size, 16, true, true},
+        {"dW3t", dW3t, N * K * size, 16, true, true},
+        {"workspace", workspace, (int64_t)workspace_bytes, 256, true, true},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    const hipStream_t s = (hipStream_t)stream;
+    const swiglu::GemmWorkspace ws = make_ws(workspace, workspace_bytes, cus);
+    const bool f32 = grad_type == SWIGLU_F32;
+    hipError_t e = hipSuccess;
+    if (M > 0)
+        e = swiglu::launch_grad_gate_up(dOut, W3t, GU, dGU, (int)M, (int)N, (int)K, ws, s);
+    if (e == hipSuccess && dW3t)
+        e = swiglu::launch_weight_grad(dOut, H, dW3t, dW3t_add, f32, (int)M, (int)K, (int)N, ws, s);
+    if (e == hipSuccess && dA && M > 0)
+        e = swiglu::launch_grad_input(dGU, W_fused, dA, (int)M, (int)K, (int)(2 * N), ws, s);
+    if (e == hipSuccess && dW_fused)
+        e = swiglu::launch_weight_grad(dGU, A, dW_fused, dW_fused_add, f32, (int)M, (int)(2 * N),
+                                       (int)K, ws, s);
+    return launched(e, "gated MLP backward");
 }
 
 }  // extern "C"

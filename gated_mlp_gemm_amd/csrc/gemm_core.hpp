@@ -37,6 +37,13 @@
 // Edges.  Rows past the end of an operand fall outside its buffer range and
 // load as zeros; chunks at k >= K are masked explicitly, so the K tail
 // contributes nothing.
+//
+// Strided operands.  The gradients' products contract along the rows of an
+// operand ([K][columns] in memory: a weight by its rows, or both factors of a
+// weight's gradient).  A shape may take such an operand (kATr, kBTr) with the
+// same rings, loads and MFMAs: its panel lies in LDS in pieces of 4 k x 32
+// columns (256 bytes), and a fragment is two transposing 64-bit reads, each
+// 4 k x 16 columns of one piece (StridedLoader, TrFrag).
 #pragma once
 
 #include <type_traits>
@@ -56,13 +63,14 @@ namespace swiglu {
 // registers of the 32x32 one.  A K step of BK elements moves BK * EB bytes
 // per tile row either way.
 template <int BM_, int BN_, int BK_, int WM_, int WN_, int STAGES_, int EB_ = 2,
-          int BSTAGES_ = STAGES_, int MI_ = 32>
+          int BSTAGES_ = STAGES_, int MI_ = 32, bool ATR_ = false, bool BTR_ = false>
 struct TileShape {
     static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_;
     static constexpr int STAGES = STAGES_;     // A ring
     static constexpr int BSTAGES = BSTAGES_;   // B ring
     static constexpr int MI = MI_;
     static constexpr int EB = EB_;
+    static constexpr bool kATr = ATR_, kBTr = BTR_;   // strided operands
     static constexpr int kWaves = WM * WN;
     static constexpr int kThreads = 64 * kWaves;
     static constexpr int kWaveM = BM / WM;
@@ -102,6 +110,7 @@ struct TileShape {
     static_assert(STAGES >= 2 && STAGES <= 16 && BSTAGES >= 2 && BSTAGES <= 16, "ring depth");
     static_assert(kDmaA * STAGES + kDmaB * BSTAGES < 64, "vmcnt is a 6-bit counter");
     static_assert(kWaves == 4, "4 waves, one per SIMD (the pipeline below)");
+    static_assert((!kATr && !kBTr) || (MI == 16 && BK == 64), "strided operands: bf16, 16x16 MFMAs");
 
     // Row and column, within its 32x32 block, of accumulator register r of
     // lane l: row_l(l) + row_r(r) and col_l(l) + col_r(r) (device.hpp gives
@@ -307,11 +316,70 @@ struct PanelLoader {
     }
 };
 
+// The direct-to-LDS loads of one tile panel of a strided operand: element
+// (k, column r) of the logical row r lies at base + k ld + r, and the panel's
+// NROWS logical rows are that many columns of memory.  LDS holds pieces of
+// 4 k x 32 columns, row by row (256 bytes), the pieces of the same 4 k side by
+// side: a transposing read takes 4 rows x 32 bytes of one piece, which are 64
+// bytes apart and so in different banks, and every read of a lane is an
+// immediate offset from one address.  (64 bytes of a row are the least that
+// four lanes, one step of the load's address unit, cover together.)
+//
+// Load j of a wave fills the 1 KiB LDS block j kWaves + wave, four pieces; the
+// waves' blocks of one load cover whole rows, so load j adds a uniform row
+// distance to the lane's one offset.  Each step's buffer range is that step's
+// rows of the matrix: k past K reads zeros, with no masking, and neither the
+// matrix nor K has to stay below 2^31 bytes.  Columns past the matrix's last
+// read what lies there (the next row), which only reaches results that are
+// not stored.
+template <class S, int NROWS, int NDMA>
+struct StridedLoader {
+    static constexpr int kPieces = NROWS / 32;                      // of the same 4 k
+    static constexpr int kRowsPerLoad = S::kWaves * 1024 / (NROWS * 2);
+    static_assert(kRowsPerLoad % 4 == 0 && kRowsPerLoad * NDMA == S::BK, "loads of whole rows");
+    const char *panel;
+    uint32_t row_bytes;    // uniform: from one k to the next
+    uint32_t before;       // uniform: bytes of a row before the panel
+    uint32_t voff;         // byte offset of this lane's chunk of load 0
+    int lds_base;          // uniform: LDS byte offset of the wave's block of load 0
+    int klen;
+
+    __device__ __forceinline__ void init(const KMajor &op, int r0, int K) {
+        before = static_cast<uint32_t>(r0) * 2u;
+        row_bytes = static_cast<uint32_t>(op.ld) * 2u;
+        panel = static_cast<const char *>(op.base) + before;
+        klen = r0 < op.rows ? K : 0;
+        const int lane = threadIdx.x & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+        const int piece = 4 * wave + lane / 16;
+        const int k = 4 * (piece / kPieces) + (lane % 16) / 4;
+        const int c = 32 * (piece % kPieces) + 8 * (lane % 4);
+        voff = static_cast<uint32_t>(k) * row_bytes + static_cast<uint32_t>(c) * 2u;
+        lds_base = wave * 1024;
+    }
+    // (the scalar arithmetic of a step is the same for all its loads)
+    template <bool kEven = false>
+    __device__ __forceinline__ void issue(int k0, SWIGLU_LDS char *panel_lds, int only = -1) const {
+        const int rows = min(klen - k0, S::BK);
+        const int bytes = rows > 0 ? rows * static_cast<int>(row_bytes) - static_cast<int>(before) : 0;
+        const __amdgpu_buffer_rsrc_t rsrc =
+            make_rsrc(panel + static_cast<int64_t>(k0) * row_bytes, static_cast<uint32_t>(bytes));
+#pragma unroll
+        for (int j = 0; j < NDMA; ++j)
+            if (only < 0 || only == j)
+                dma16(rsrc, panel_lds + lds_base + j * S::kWaves * 1024, voff,
+                      static_cast<uint32_t>(j * kRowsPerLoad) * row_bytes);
+    }
+};
+
 // Loader of one output tile: the A panel and the B panel of each K step.
 template <class S>
 struct TileLoader {
-    PanelLoader<S, S::BM, S::kDmaA> a;
-    PanelLoader<S, S::BN, S::kDmaB> b;
+    typename std::conditional<S::kATr, StridedLoader<S, S::BM, S::kDmaA>,
+                              PanelLoader<S, S::BM, S::kDmaA>>::type a;
+    using PanelB = typename std::conditional<S::kBTr, StridedLoader<S, S::BN, S::kDmaB>,
+                                             PanelLoader<S, S::BN, S::kDmaB>>::type;
+    PanelB b;
     int K;
 
     __device__ __forceinline__ void init(const KMajor &A, int m0, const KMajor &B, int n0,
@@ -326,7 +394,7 @@ struct TileLoader {
     // kstep >= ceil(K/BK) loads nothing.
     template <bool kEven = false>
     __device__ __forceinline__ void issue(int kstep, int part, SWIGLU_LDS char *dst, int only,
-                                          const PanelLoader<S, S::BN, S::kDmaB> &bp) const {
+                                          const PanelB &bp) const {
         const int k0 = kstep * S::BK;
         if (part == 0) a.template issue<kEven>(k0, dst, only);
         else bp.template issue<kEven>(k0, dst, only);
@@ -338,13 +406,27 @@ struct TileLoader {
     }
 };
 
+// A strided operand's fragment: the 8 k of a lane as two transposing reads of
+// 4 k each (kept apart: nothing may touch either before its read has landed).
+struct TrFrag {
+    u32x2 lo, hi;
+};
 // Fragment registers of one k-substep: raw MFMA operands, kFragChunks
 // 16-byte chunks per block.
 template <class S>
 struct Frags {
-    u32x4 a[S::TM][S::kFragChunks];
-    u32x4 b[S::TN][S::kFragChunks];
+    typename std::conditional<S::kATr, TrFrag, u32x4>::type a[S::TM][S::kFragChunks];
+    typename std::conditional<S::kBTr, TrFrag, u32x4>::type b[S::TN][S::kFragChunks];
 };
+__device__ __forceinline__ const u32x4 &operand(const u32x4 &f) { return f; }
+__device__ __forceinline__ u32x4 operand(const TrFrag &f) {
+    return __builtin_shufflevector(f.lo, f.hi, 0, 1, 2, 3);
+}
+__device__ __forceinline__ void landed(u32x4 &f) { asm volatile("" : "+v"(f)); }
+__device__ __forceinline__ void landed(TrFrag &f) {
+    asm volatile("" : "+v"(f.lo));
+    asm volatile("" : "+v"(f.hi));
+}
 
 // LDS reads issued as inline assembly.  The compiler neither tracks their
 // completion nor sees them as LDS accesses; the pipelines wait for them with
@@ -355,6 +437,13 @@ template <int OFF>
 __device__ __forceinline__ u32x4 asm_read_b128(uint32_t addr) {
     u32x4 r;
     asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(r) : "v"(addr), "i"(OFF));
+    return r;
+}
+
+template <int OFF>
+__device__ __forceinline__ u32x2 asm_read_tr(uint32_t addr) {
+    u32x2 r;
+    asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(r) : "v"(addr), "i"(OFF));
     return r;
 }
 
@@ -374,8 +463,22 @@ template <class S>
 struct FragOffsets {
     uint32_t a[S::kKSub][S::kFragChunks];
     uint32_t b[S::kKSub][S::kFragChunks];
+    // A strided operand's reads: lane l = 16 g + i of read h (k 8 g + 4 h on)
+    // addresses row i / 4, columns 4 (i % 4) on of the piece that holds k =
+    // 8 g + 4 h; substep, block, half and h are immediate offsets (tr_offset).
+    uint32_t a_tr, b_tr;
+    __device__ __forceinline__ static uint32_t tr_lane(int rows, int first, int lane) {
+        return static_cast<uint32_t>(2 * (lane >> 4) * rows * 8 + first * 8 +
+                                     ((lane >> 2) & 3) * 64 + (lane & 3) * 8);
+    }
+    // rows: of the panel; block: 32 rows from the wave's first
+    static constexpr int tr_offset(int rows, int ks, int block, int j, int h) {
+        return (8 * ks + h) * rows * 8 + block * 256 + j * 32;
+    }
 
     __device__ __forceinline__ void init(int wm, int wn, int lane) {
+        a_tr = tr_lane(S::BM, wm * S::kWaveM, lane);
+        b_tr = tr_lane(S::BN, wn * S::kWaveN, lane);
 #pragma unroll
         for (int ks = 0; ks < S::kKSub; ++ks)
 #pragma unroll
@@ -395,33 +498,6 @@ struct FragOffsets {
             }
     }
 };
-
-template <class S, int I>
-__device__ __forceinline__ void read_a_blocks(uint32_t p, Frags<S> &f, int j) {
-    if constexpr (I < S::TM) {
-        f.a[I][j] = asm_read_b128<I * 32 * S::kRowBytes>(p);
-        read_a_blocks<S, I + 1>(p, f, j);
-    }
-}
-template <class S, int I>
-__device__ __forceinline__ void read_b_blocks(uint32_t p, Frags<S> &f, int j) {
-    if constexpr (I < S::TN) {
-        f.b[I][j] = asm_read_b128<I * 32 * S::kRowBytes>(p);
-        read_b_blocks<S, I + 1>(p, f, j);
-    }
-}
-
-// Issue the fragment reads of k-substep KS from the A and B ring buffers at
-// LDS addresses `sa` and `sb`.
-template <class S, int KS>
-__device__ __forceinline__ void read_frags(uint32_t sa, uint32_t sb, const FragOffsets<S> &o,
-                                           Frags<S> &f) {
-#pragma unroll
-    for (int j = 0; j < S::kFragChunks; ++j) {
-        read_a_blocks<S, 0>(sa + o.a[KS][j], f, j);
-        read_b_blocks<S, 0>(sb + o.b[KS][j], f, j);
-    }
-}
 
 // Load issue order of the pipeline below, and the vmcnt waits it implies.
 // K step t's panels are loaded in group g = t - STAGES (A) and t - BSTAGES
@@ -475,9 +551,9 @@ __device__ __forceinline__ void wait_frags(Frags<S> &f) {
 #pragma unroll
     for (int j = 0; j < S::kFragChunks; ++j) {
 #pragma unroll
-        for (int tm = 0; tm < S::TM; ++tm) asm volatile("" : "+v"(f.a[tm][j]));
+        for (int tm = 0; tm < S::TM; ++tm) landed(f.a[tm][j]);
 #pragma unroll
-        for (int tn = 0; tn < S::TN; ++tn) asm volatile("" : "+v"(f.b[tn][j]));
+        for (int tn = 0; tn < S::TN; ++tn) landed(f.b[tn][j]);
     }
 }
 
@@ -500,17 +576,29 @@ __device__ __forceinline__ void mma(const Frags<S> &f, typename S::Acc (&acc)[S:
         }
 }
 
-// Fragment read R of k-substep KS (R < kFragChunks (TM + TN), in the order of
-// read_frags: for each read j, the TM A blocks, then the TN B blocks).
-template <class S, int KS, int R>
-__device__ __forceinline__ void read_frag_one(uint32_t sa, uint32_t sb, const FragOffsets<S> &o,
-                                              Frags<S> &f) {
+// Fragment read R of k-substep KS (R < kFragChunks (TM + TN): for each read j,
+// the TM A blocks, then the TN B blocks).  rd.at<part, OFF>(lane) reads at the
+// stage's panel of `part` (0: A, 1: B) + lane + OFF; at_tr the same, transposing.
+template <class S, int KS, int R, class Reads>
+__device__ __forceinline__ void read_frag_one(const Reads &rd, const FragOffsets<S> &o, Frags<S> &f) {
     constexpr int kPer = S::TM + S::TN;
     constexpr int j = R / kPer, b = R % kPer;
-    if constexpr (b < S::TM)
-        f.a[b][j] = asm_read_b128<b * 32 * S::kRowBytes>(sa + o.a[KS][j]);
-    else
-        f.b[b - S::TM][j] = asm_read_b128<(b - S::TM) * 32 * S::kRowBytes>(sb + o.b[KS][j]);
+    if constexpr (b < S::TM) {
+        if constexpr (S::kATr) {
+            f.a[b][j].lo = rd.template at_tr<0, FragOffsets<S>::tr_offset(S::BM, KS, b, j, 0)>(o.a_tr);
+            f.a[b][j].hi = rd.template at_tr<0, FragOffsets<S>::tr_offset(S::BM, KS, b, j, 1)>(o.a_tr);
+        } else {
+            f.a[b][j] = rd.template at<0, b * 32 * S::kRowBytes>(o.a[KS][j]);
+        }
+    } else {
+        constexpr int c = b - S::TM;
+        if constexpr (S::kBTr) {
+            f.b[c][j].lo = rd.template at_tr<1, FragOffsets<S>::tr_offset(S::BN, KS, c, j, 0)>(o.b_tr);
+            f.b[c][j].hi = rd.template at_tr<1, FragOffsets<S>::tr_offset(S::BN, KS, c, j, 1)>(o.b_tr);
+        } else {
+            f.b[c][j] = rd.template at<1, c * 32 * S::kRowBytes>(o.b[KS][j]);
+        }
+    }
 }
 
 // Where a substep's fragment reads find their ring stage.  RuntimeReads: the
@@ -523,30 +611,53 @@ template <class S>
 struct RuntimeReads {
     uint32_t sa, sb;
     const FragOffsets<S> *o;
+    template <int PART, int OFF>
+    __device__ __forceinline__ u32x4 at(uint32_t lane) const {
+        return asm_read_b128<OFF>((PART == 0 ? sa : sb) + lane);
+    }
+    template <int PART, int OFF>
+    __device__ __forceinline__ u32x2 at_tr(uint32_t lane) const {
+        return asm_read_tr<OFF>((PART == 0 ? sa : sb) + lane);
+    }
     template <int KS, int R>
     __device__ __forceinline__ void read(Frags<S> &f) const {
-        read_frag_one<S, KS, R>(sa, sb, *o, f);
+        read_frag_one<S, KS, R>(*this, *o, f);
     }
 };
 template <class S, int OFFA, int OFFB>
 struct FixedReads {
     uint32_t lds_addr;
     const FragOffsets<S> *o;
-    template <int OFF>
-    __device__ __forceinline__ static u32x4 at(uint32_t lane_base) {
-        static_assert((OFF & 0xFFFF) + 16 <= 0x10000, "16-bit immediate offset");
-        return asm_read_b128<(OFF & 0xFFFF)>(lane_base + static_cast<uint32_t>(OFF & ~0xFFFF));
+    template <int PART, int OFF>
+    __device__ __forceinline__ u32x4 at(uint32_t lane) const {
+        constexpr int off = (PART == 0 ? OFFA : OFFB) + OFF;
+        static_assert((off & 0xFFFF) + 16 <= 0x10000, "16-bit immediate offset");
+        return asm_read_b128<(off & 0xFFFF)>(lds_addr + lane + static_cast<uint32_t>(off & ~0xFFFF));
+    }
+    template <int PART, int OFF>
+    __device__ __forceinline__ u32x2 at_tr(uint32_t lane) const {
+        constexpr int off = (PART == 0 ? OFFA : OFFB) + OFF;
+        return asm_read_tr<(off & 0xFFFF)>(lds_addr + lane + static_cast<uint32_t>(off & ~0xFFFF));
     }
     template <int KS, int R>
     __device__ __forceinline__ void read(Frags<S> &f) const {
-        constexpr int kPer = S::TM + S::TN;
-        constexpr int j = R / kPer, b = R % kPer;
-        if constexpr (b < S::TM)
-            f.a[b][j] = at<OFFA + b * 32 * S::kRowBytes>(lds_addr + o->a[KS][j]);
-        else
-            f.b[b - S::TM][j] = at<OFFB + (b - S::TM) * 32 * S::kRowBytes>(lds_addr + o->b[KS][j]);
+        read_frag_one<S, KS, R>(*this, *o, f);
     }
 };
+
+// Issue the fragment reads of k-substep KS from the A and B ring buffers at
+// LDS addresses `sa` and `sb`.
+template <class S, int KS, int... R>
+__device__ __forceinline__ void read_frags_each(const RuntimeReads<S> &rd, Frags<S> &f,
+                                                std::integer_sequence<int, R...>) {
+    (rd.template read<KS, R>(f), ...);
+}
+template <class S, int KS>
+__device__ __forceinline__ void read_frags(uint32_t sa, uint32_t sb, const FragOffsets<S> &o,
+                                           Frags<S> &f) {
+    read_frags_each<S, KS>(RuntimeReads<S>{sa, sb, &o}, f,
+                           std::make_integer_sequence<int, S::kFragChunks *(S::TM + S::TN)>{});
+}
 
 // The 16x16 MFMAs of one k-substep, issued one by one (inline assembly, in
 // program order) on the fragments `cur`, and between them:
@@ -573,8 +684,10 @@ __device__ __forceinline__ void mma16_at(const Frags<S> &cur, Frags<S> &nxt, con
     constexpr int kNReads = sizeof...(R);
     constexpr int tm = I / (4 * S::TN), tn = (I / 4) % S::TN, sm = (I / 2) % 2, sn = I % 2;
     // quad 2 sm + sn of block (tm, tn): rows 16 sm, columns 16 sn
-    if constexpr (kInit) mfma_16x16x32_init(acc[tm][tn].v[2 * sm + sn], cur.a[tm][sm], cur.b[tn][sn]);
-    else mfma_16x16x32_acc(acc[tm][tn].v[2 * sm + sn], cur.a[tm][sm], cur.b[tn][sn]);
+    if constexpr (kInit)
+        mfma_16x16x32_init(acc[tm][tn].v[2 * sm + sn], operand(cur.a[tm][sm]), operand(cur.b[tn][sn]));
+    else
+        mfma_16x16x32_acc(acc[tm][tn].v[2 * sm + sn], operand(cur.a[tm][sm]), operand(cur.b[tn][sn]));
     (
         [&] {
             if constexpr (kReads && kBegin + R * (kSpan / 2) / kNReads == I)

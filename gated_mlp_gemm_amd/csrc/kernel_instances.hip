@@ -127,6 +127,35 @@ template struct ReduceLaunch<ShapeThinLora, PairMulEpilogue>;
 template struct ReduceLaunch<ShapeThinLora, StoreEpilogue>;
 template struct ReduceLaunch<ShapeSmallLora, PairMulEpilogue>;
 template struct ReduceLaunch<ShapeSmallLora, StoreEpilogue>;
+#elif SWIGLU_INSTANCE == 23
+template struct TilesLaunch<ShapeWideDx, GateGradEpilogue, kTailSplit>;
+#elif SWIGLU_INSTANCE == 24
+template struct TilesLaunch<ShapeWideDx, StoreEpilogue, kTailSplit>;
+#elif SWIGLU_INSTANCE == 25
+template struct TilesLaunch<ShapeWideDw, WeightGradEpilogue, kTailSplit>;
+#elif SWIGLU_INSTANCE == 26
+template struct TilesLaunch<ShapeWide, PairMulKeep, kTailSplit>;
+#elif SWIGLU_INSTANCE == 27
+template struct TilesLaunch<ShapeQuadDx, GateGradEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeQuadDx, StoreEpilogue, kTailSplit>;
+#elif SWIGLU_INSTANCE == 28
+template struct TilesLaunch<ShapeQuadDw, WeightGradEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeQuad, PairMulKeep, kTailSplit>;
+#elif SWIGLU_INSTANCE == 29
+template struct TilesLaunch<ShapeSmallDx, GateGradEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeSmallDx, StoreEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeSmallLora, PairMulKeep, kTailSplit>;
+template struct ReduceLaunch<ShapeWideDx, GateGradEpilogue>;
+template struct ReduceLaunch<ShapeWideDx, StoreEpilogue>;
+template struct ReduceLaunch<ShapeWideDw, WeightGradEpilogue>;
+template struct ReduceLaunch<ShapeWide, PairMulKeep>;
+template struct ReduceLaunch<ShapeQuadDx, GateGradEpilogue>;
+template struct ReduceLaunch<ShapeQuadDx, StoreEpilogue>;
+template struct ReduceLaunch<ShapeQuadDw, WeightGradEpilogue>;
+template struct ReduceLaunch<ShapeQuad, PairMulKeep>;
+template struct ReduceLaunch<ShapeSmallDx, GateGradEpilogue>;
+template struct ReduceLaunch<ShapeSmallDx, StoreEpilogue>;
+template struct ReduceLaunch<ShapeSmallLora, PairMulKeep>;
 #else
 #error "SWIGLU_INSTANCE is past the end of the instance list"
 #endif

@@ -235,7 +235,7 @@ constexpr double quarter_step_us() {
 //    ceil(nk / s) steps plus the reduction.
 // ws.tail forces one of them where it applies.  `us`, if given, receives the
 // predicted time of the whole schedule.
-template <class S>
+template <class S, bool kQuarters = kQuarterable<S>>
 static Schedule make_schedule(int M, int cols, int K, const GemmWorkspace &ws,
                               double *us = nullptr) {
     Schedule sch{};
@@ -258,7 +258,7 @@ static Schedule make_schedule(int M, int cols, int K, const GemmWorkspace &ws,
     if (L == 0) return sch;
     const bool forced = ws.tail != kTailAuto;
     double best = round;                            // tail tiles whole
-    if (kQuarterable<S> && (!forced || ws.tail == kTailQuarters)) {
+    if (kQuarters && (!forced || ws.tail == kTailQuarters)) {
         const double t = cdiv(4 * L, G) * (kRoundUs + sch.nk * quarter_step_us<S>());
         if (forced || t < best) {
             best = t;
@@ -663,6 +663,120 @@ hipError_t launch_lora_project(const uint16_t *X, const uint16_t *W, uint16_t *Y
             A, B, M, cols, K, PairMulLora{{Y, M, cols / 2, cols / 2, 1.0f}, lora}, t.count, ws, stream);
     return launch_lora<StoreLora, StoreEpilogue>(A, B, M, cols, K, StoreLora{{Y, M, cols}, lora},
                                                  t.count, ws, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Training: the forward pass that keeps Gate and Up, and the gradients' products.
+// The kernels without tail work are those with a split tail, given none.
+// ---------------------------------------------------------------------------
+template <class S, class Epi>
+static hipError_t launch_split_gemm(const KMajor &A, KMajor B, int M, int cols, int K,
+                                    const Epi &epi, const GemmWorkspace &ws, hipStream_t stream) {
+    Schedule sch = make_schedule<S, false>(M, cols, K, ws);
+    sch.grid = launch_grid<S>(sch, ws.cus);
+    B.pairs = Epi::template paired<S>() ? 1 : 0;   // de-interleaved weight panels
+    if (sch.grid <= 0) return hipSuccess;
+    const hipError_t e =
+        TilesLaunch<S, Epi, kTailSplit>::run(sch.grid, A, B, M, K, epi, sch, stream);
+    if (e != hipSuccess || sch.pieces == 0) return e;
+    constexpr int kWavesPerTile = S::kWaves * S::TM * S::TN / Epi::template unit_blocks<S>();
+    return ReduceLaunch<S, Epi>::run(sch.split_tiles * kWavesPerTile, epi, sch, stream);
+}
+template <class Wide, class Quad>
+static bool quad_split_faster(int M, int cols, int K, const GemmWorkspace &ws) {
+    if (ws.tile == 256) return false;
+    if (ws.tile == 128) return true;
+    if (ws.cus <= 0) return false;
+    double wide = 0.0, quad = 0.0;
+    make_schedule<Wide, false>(M, cols, K, ws, &wide);
+    make_schedule<Quad, false>(M, cols, K, ws, &quad);
+    return quad < wide;
+}
+
+hipError_t launch_fused_train(const uint16_t *A, const uint16_t *Wf, uint16_t *H, uint16_t *GU,
+                              int M, int N, int K, const GemmWorkspace &ws, hipStream_t stream) {
+    const KMajor Ak{A, M, 1, 0, 0, 0};
+    const KMajor B{Wf, 2 * N, 1, 0, 0, 0};
+    PairMulKeep epi;
+    epi.Y = H;
+    epi.M = M;
+    epi.N = N;
+    epi.ldy = N;
+    epi.scale = 1.0f;
+    epi.GU = GU;
+    if (M <= 128 && !small_m_quad_tiles(M, 2 * N, ws))
+        return launch_split_gemm<ShapeSmallLora>(Ak, B, M, 2 * N, K, epi, ws, stream);
+    if (M <= 128 || quad_split_faster<ShapeWide, ShapeQuad>(M, 2 * N, K, ws))
+        return launch_split_gemm<ShapeQuad>(Ak, B, M, 2 * N, K, epi, ws, stream);
+    return launch_split_gemm<ShapeWide>(Ak, B, M, 2 * N, K, epi, ws, stream);
+}
+
+// D [M][cols] = dY [M][C] . W [C][cols], with a weight contracted by its rows.
+template <class Epi>
+static hipError_t launch_dx(const uint16_t *dY, const uint16_t *W, int M, int cols, int C,
+                            const Epi &epi, const GemmWorkspace &ws, hipStream_t stream) {
+    const KMajor A{dY, M, 1, 0, 0, 0};
+    const KMajor B{W, cols, 1, 0, 0, cols};
+    if (M <= 128) return launch_split_gemm<ShapeSmallDx>(A, B, M, cols, C, epi, ws, stream);
+    if (quad_split_faster<ShapeWideDx, ShapeQuadDx>(M, cols, C, ws))
+        return launch_split_gemm<ShapeQuadDx>(A, B, M, cols, C, epi, ws, stream);
+    return launch_split_gemm<ShapeWideDx>(A, B, M, cols, C, epi, ws, stream);
+}
+hipError_t launch_grad_input(const uint16_t *dY, const uint16_t *W, uint16_t *dX, int M, int cols,
+                             int C, const GemmWorkspace &ws, hipStream_t stream) {
+    return launch_dx(dY, W, M, cols, C, StoreEpilogue{dX, M, cols}, ws, stream);
+}
+hipError_t launch_grad_gate_up(const uint16_t *dOut, const uint16_t *W3t, const uint16_t *GU,
+                               uint16_t *dGU, int M, int N, int D, const GemmWorkspace &ws,
+                               hipStream_t stream) {
+    GateGradEpilogue epi;
+    epi.GU = GU;
+    epi.dGU = dGU;
+    epi.M = M;
+    epi.N = N;
+    return launch_dx(dOut, W3t, M, N, D, epi, ws, stream);
+}
+
+hipError_t launch_weight_grad(const uint16_t *dY, const uint16_t *X, void *dW, const void *add,
+                              bool f32, int M, int rows, int cols, const GemmWorkspace &ws_,
+                              hipStream_t stream) {
+    const KMajor A{dY, rows, 1, 0, 0, rows};
+    const KMajor B{X, cols, 1, 0, 0, cols};
+    const WeightGradEpilogue epi{dW, add, rows, cols, f32 ? 1 : 0};
+    GemmWorkspace ws = ws_;
+    if (M == 0) ws.tail = kTailWhole;   // no K step to split: the tiles store zeros (+ add)
+    if (quad_split_faster<ShapeWideDw, ShapeQuadDw>(rows, cols, M, ws))
+        return launch_split_gemm<ShapeQuadDw>(A, B, rows, cols, M, epi, ws, stream);
+    return launch_split_gemm<ShapeWideDw>(A, B, rows, cols, M, epi, ws, stream);
+}
+
+// dGU of a given dH: the epilogue's arithmetic, 8 outputs of H a lane.
+__global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t *__restrict__ dH,
+                                                        const uint16_t *GU, uint16_t *dGU,
+                                                        int64_t nchunks) {
+    for (int64_t c = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; c < nchunks;
+         c += (int64_t)gridDim.x * blockDim.x) {
+        const u32x4 d = gload16(dH + c * 8);
+        const u32x4 lo = gload16(GU + c * 16), hi = gload16(GU + c * 16 + 8);
+        u32x4 olo, ohi;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const u32x4 &src = i < 2 ? lo : hi;
+            u32x4 &dst = i < 2 ? olo : ohi;
+            dst[(i & 1) * 2] = gate_grad(bf16_lo(d[i]), src[(i & 1) * 2]);
+            dst[(i & 1) * 2 + 1] = gate_grad(bf16_hi(d[i]), src[(i & 1) * 2 + 1]);
+        }
+        gstore16(dGU + c * 16, olo);
+        gstore16(dGU + c * 16 + 8, ohi);
+    }
+}
+hipError_t launch_gate_grad(const uint16_t *dH, const uint16_t *GU, uint16_t *dGU, int64_t count,
+                            hipStream_t stream) {
+    const int64_t chunks = count / 8;
+    const int64_t blocks = (chunks + 255) / 256;
+    const int grid = static_cast<int>(blocks < 65536 ? blocks : 65536);
+    hipLaunchKernelGGL(gate_grad_kernel, dim3(grid), dim3(256), 0, stream, dH, GU, dGU, chunks);
+    return hipGetLastError();
 }
 
 // One 256x256 fp32 slot per CU: a split schedule has at most one piece per

@@ -55,6 +55,23 @@ hipError_t launch_gemm_store(const uint16_t *A, const uint16_t *Wf, int phase, u
 // Out [M][D] = bf16(H [M][N] . W3), W3 given K-contiguous as W3t [D][N].
 hipError_t launch_down_proj(const uint16_t *H, const uint16_t *W3t, uint16_t *Out, int M, int N,
                             int D, const GemmWorkspace &ws, hipStream_t stream);
+// Training.  H and GU [M][2N] (Gate and Up, bf16, interleaved) of one pass over A.
+hipError_t launch_fused_train(const uint16_t *A, const uint16_t *Wf, uint16_t *H, uint16_t *GU,
+                              int M, int N, int K, const GemmWorkspace &ws, hipStream_t stream);
+// dX [M][cols] = bf16(dY [M][C] . W), W [C][cols] as the forward pass holds it.
+hipError_t launch_grad_input(const uint16_t *dY, const uint16_t *W, uint16_t *dX, int M, int cols,
+                             int C, const GemmWorkspace &ws, hipStream_t stream);
+// dGU [M][2N] of dH = dOut [M][D] . W3 (W3t [D][N]), which stays in registers; dGU may be GU.
+hipError_t launch_grad_gate_up(const uint16_t *dOut, const uint16_t *W3t, const uint16_t *GU,
+                               uint16_t *dGU, int M, int N, int D, const GemmWorkspace &ws,
+                               hipStream_t stream);
+// ... of a given dH, count = M N (a multiple of 8).
+hipError_t launch_gate_grad(const uint16_t *dH, const uint16_t *GU, uint16_t *dGU, int64_t count,
+                            hipStream_t stream);
+// dW [rows][cols] = dY [M][rows]^T . X [M][cols] (+ add), fp32 (f32) or bf16; add may be dW.
+hipError_t launch_weight_grad(const uint16_t *dY, const uint16_t *X, void *dW, const void *add,
+                              bool f32, int M, int rows, int cols, const GemmWorkspace &ws,
+                              hipStream_t stream);
 // FP8 (E4M3) path: q = fp8(x * 2^-scale_exp); variant I on FP8 operands with
 // the epilogue scaling Gate and Up by `scale` (= 2^(a_exp + w_exp)).
 hipError_t launch_quantize_fp8(const uint16_t *x, uint8_t *q, int64_t count, int scale_exp,

@@ -276,6 +276,279 @@ struct StoreEpilogue {
     __device__ __forceinline__ static int unit_block(int u, int) { return u; }
 };
 
+// Byte offset of lane `lane`'s first element of block (tm, tn) of a wave in a
+// row-major matrix of 4-byte elements, ld a row, as lane_offsets' (the block's row
+// 32 tm aside, which is uniform).
+template <class S>
+__device__ __forceinline__ void lane_offsets4(uint32_t (&voff)[2], int tn, int cols_valid, int n0,
+                                              int ld, int tid) {
+    const int lane = tid & 63, wave = tid >> 6;
+    lane_offsets(voff, static_cast<uint32_t>((wave / S::WN) * S::kWaveM + S::row_l(lane)),
+                 (wave % S::WN) * S::kWaveN + tn * 32 + S::col_l(lane), cols_valid, n0, ld);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) voff[h] = voff[h] == kOutOfRange ? kOutOfRange : 2u * voff[h];
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc4(const void *base, int m0, int rows, int ld) {
+    return make_rsrc(static_cast<const char *>(base) + static_cast<int64_t>(m0) * ld * 4,
+                     static_cast<uint32_t>(rows) * static_cast<uint32_t>(ld) * 4u);
+}
+
+// The training forward pass: variant I's epilogue, which also stores Gate and Up
+// as bf16, interleaved as W_fused's columns: GU [M][2N], one 4-byte store a pair
+// (Y is computed from the fp32 sums, bit for bit as without).  Paired layouts only.
+struct PairMulKeep : PairMulEpilogue {
+    uint16_t *GU;
+
+    template <class S, bool kFromAcc = true>
+    __device__ __forceinline__ void unit(const typename S::Acc &g, const typename S::Acc &up, int u,
+                                         int m0, int n0, int tid) const {
+        static_assert(S::TN % 2 == 0 && S::MI == 16, "paired layout");
+        const int lane = tid & 63, wave = tid >> 6;
+        const int tm = u / (S::TN / 2), tp = u % (S::TN / 2);
+        const int y0 = n0 / 2, ycols_valid = min(S::BN / 2, N - y0);
+        const int rows_valid = min(S::BM, M - m0);
+        const __amdgpu_buffer_rsrc_t ry = out_rsrc(Y, m0, rows_valid, ldy);
+        const __amdgpu_buffer_rsrc_t rg = rsrc4(GU, m0, rows_valid, N);
+        const uint32_t lrow = static_cast<uint32_t>((wave / S::WN) * S::kWaveM + S::row_l(lane));
+        uint32_t voff[2], goff[2];
+        lane_offsets(voff, lrow, (wave % S::WN) * (S::kWaveN / 2) + tp * 32 + S::col_l(lane),
+                     ycols_valid, y0, N);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) goff[h] = voff[h] == kOutOfRange ? kOutOfRange : 2u * voff[h];
+        const uint32_t pitch = static_cast<uint32_t>(N) * 2u;   // of Y (ldy = N here); GU: twice
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float g0 = acc_value<kFromAcc>(g.get(i)), g1 = acc_value<kFromAcc>(g.get(i + 1));
+            const float u0 = acc_value<kFromAcc>(up.get(i)), u1 = acc_value<kFromAcc>(up.get(i + 1));
+            const uint32_t v = pack_bf16x2(silu(g0) * u0, silu(g1) * u1);
+            const uint32_t row = static_cast<uint32_t>(tm * 32 + S::row_r(i)) * pitch;
+            const int h = S::col_r(i) / 16;
+            store_b16(ry, voff[h], row, static_cast<uint16_t>(v));
+            store_b16_hi(ry, voff[h], row + pitch, v);
+            __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(g0, u0), rg, static_cast<int>(goff[h]),
+                                                  static_cast<int>(2u * row), 0);
+            __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(g1, u1), rg, static_cast<int>(goff[h]),
+                                                  static_cast<int>(2u * row + 2u * pitch), 0);
+        }
+    }
+    template <class S>
+    __device__ __forceinline__ void apply(const typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0,
+                                          int tid) const {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < S::TM * S::TN / 2; ++u) {
+            unit<S>(acc[u / (S::TN / 2)][2 * (u % (S::TN / 2))],
+                    acc[u / (S::TN / 2)][2 * (u % (S::TN / 2)) + 1], u, m0, n0, tid);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+};
+
+// Epilogues that read a matrix of the output's shape beside the accumulators:
+// D::load fetches a block's 16 values a lane and D::finish uses them.  A block's
+// loads go out kAhead blocks before its use, so that a tile waits for memory about
+// once and not once a block.
+template <class D>
+struct ReadingEpilogue {
+    static constexpr int kAhead = 3;
+    template <class S>
+    static constexpr bool paired() { return false; }
+    template <class S>
+    static constexpr int unit_blocks() { return 1; }
+    template <class S>
+    __device__ __forceinline__ static int unit_block(int u, int) { return u; }
+
+    template <class S, bool kFromAcc = true>
+    __device__ __forceinline__ void unit(const typename S::Acc &a0, const typename S::Acc &, int u,
+                                         int m0, int n0, int tid) const {
+        const D &d = static_cast<const D &>(*this);
+        uint32_t x[16];
+        d.template load<S>(x, u, m0, n0, tid);
+        d.template finish<S, kFromAcc>(a0, x, u, m0, n0, tid);
+    }
+    template <class S>
+    __device__ __forceinline__ void apply(const typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0,
+                                          int tid) const {
+        const D &d = static_cast<const D &>(*this);
+        constexpr int kUnits = S::TM * S::TN;
+        uint32_t x[kUnits][16];   // (kAhead + 1 of them live)
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < kUnits + kAhead; ++u) {
+            if (u < kUnits) d.template load<S>(x[u], u, m0, n0, tid);
+            __builtin_amdgcn_sched_barrier(0);
+            if (u >= kAhead) {
+                const int f = u - kAhead;
+                d.template finish<S, true>(acc[f / S::TN][f % S::TN], x[f], f, m0, n0, tid);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+};
+
+// D is the gradient by H of the gated MLP; with what the forward pass kept
+// (g = Gate, u = Up, bf16 in GU [M][2N]) and s = 1 / (1 + e^-g), H = g s u, so
+//     dGate = D u s (1 + g (1 - s)),   dUp = D g s,
+// stored as dGU [M][2N], interleaved as GU.  D is never stored, and both halves are
+// rounded to bf16 here: they are an operand of the MFMAs of two more products.
+__device__ __forceinline__ uint32_t gate_grad(float d, uint32_t gu) {
+    const float g = __builtin_bit_cast(float, gu << 16);
+    const float u = __builtin_bit_cast(float, gu & 0xFFFF0000u);
+    const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
+    return pack_bf16x2(d * u * (s * (1.0f + g * (1.0f - s))), d * (g * s));
+}
+struct GateGradEpilogue : ReadingEpilogue<GateGradEpilogue> {
+    const uint16_t *GU;
+    uint16_t *dGU;
+    int M, N;
+
+    template <class S>
+    __device__ __forceinline__ void load(uint32_t (&x)[16], int u, int m0, int n0, int tid) const {
+        const int tm = u / S::TN, tn = u % S::TN;
+        const __amdgpu_buffer_rsrc_t r = rsrc4(GU, m0, min(S::BM, M - m0), N);
+        uint32_t voff[2];
+        lane_offsets4<S>(voff, tn, min(S::BN, N - n0), n0, N, tid);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            x[i] = __builtin_amdgcn_raw_buffer_load_b32(
+                r, static_cast<int>(voff[S::col_r(i) / 16]),
+                static_cast<int>(static_cast<uint32_t>(tm * 32 + S::row_r(i)) *
+                                 static_cast<uint32_t>(N) * 4u), 0);
+    }
+    template <class S, bool kFromAcc>
+    __device__ __forceinline__ void finish(const typename S::Acc &a, const uint32_t (&x)[16], int u,
+                                           int m0, int n0, int tid) const {
+        const int tm = u / S::TN, tn = u % S::TN;
+        const __amdgpu_buffer_rsrc_t r = rsrc4(dGU, m0, min(S::BM, M - m0), N);
+        uint32_t voff[2];
+        lane_offsets4<S>(voff, tn, min(S::BN, N - n0), n0, N, tid);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            __builtin_amdgcn_raw_buffer_store_b32(
+                gate_grad(acc_value<kFromAcc>(a.get(i)), x[i]), r,
+                static_cast<int>(voff[S::col_r(i) / 16]),
+                static_cast<int>(static_cast<uint32_t>(tm * 32 + S::row_r(i)) *
+                                 static_cast<uint32_t>(N) * 4u), 0);
+    }
+};
+
+// A weight's gradient C [M][N] = D (+ add), rounded once, bf16 or fp32 (f32);
+// add: NULL, or a matrix of C's type and shape, C itself among them (each element
+// is read by the lane that stores it).
+struct WeightGradEpilogue {
+    void *C;
+    const void *add;
+    int M, N;
+    int f32;
+
+    template <bool kF32, bool kAdd>
+    struct Mode : ReadingEpilogue<Mode<kF32, kAdd>> {
+        void *C;
+        const void *add;
+        int M, N;
+        static constexpr uint32_t kSize = kF32 ? 4 : 2;
+
+        template <class S>
+        __device__ __forceinline__ void offsets(uint32_t (&voff)[2], int tn, int n0, int tid) const {
+            if constexpr (kF32) {
+                lane_offsets4<S>(voff, tn, min(S::BN, N - n0), n0, N, tid);
+            } else {
+                const int lane = tid & 63, wave = tid >> 6;
+                lane_offsets(voff, static_cast<uint32_t>((wave / S::WN) * S::kWaveM + S::row_l(lane)),
+                             (wave % S::WN) * S::kWaveN + tn * 32 + S::col_l(lane),
+                             min(S::BN, N - n0), n0, N);
+            }
+        }
+        __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, int m0, int rows) const {
+            return make_rsrc(static_cast<const char *>(p) + static_cast<int64_t>(m0) * N * kSize,
+                             static_cast<uint32_t>(rows) * static_cast<uint32_t>(N) * kSize);
+        }
+        template <class S>
+        __device__ __forceinline__ void load(uint32_t (&x)[16], int u, int m0, int n0, int tid) const {
+            if constexpr (kAdd) {
+                const int tm = u / S::TN, tn = u % S::TN;
+                const __amdgpu_buffer_rsrc_t r = rsrc(add, m0, min(S::BM, M - m0));
+                uint32_t voff[2];
+                offsets<S>(voff, tn, n0, tid);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int v = static_cast<int>(voff[S::col_r(i) / 16]);
+                    const int s = static_cast<int>(static_cast<uint32_t>(tm * 32 + S::row_r(i)) *
+                                                   static_cast<uint32_t>(N) * kSize);
+                    if constexpr (kF32) x[i] = __builtin_amdgcn_raw_buffer_load_b32(r, v, s, 0);
+                    else x[i] = __builtin_amdgcn_raw_buffer_load_b16(r, v, s, 0);
+                }
+            }
+        }
+        template <class S, bool kFromAcc>
+        __device__ __forceinline__ void finish(const typename S::Acc &a, const uint32_t (&x)[16],
+                                               int u, int m0, int n0, int tid) const {
+            const int tm = u / S::TN, tn = u % S::TN;
+            const __amdgpu_buffer_rsrc_t r = rsrc(C, m0, min(S::BM, M - m0));
+            uint32_t voff[2];
+            offsets<S>(voff, tn, n0, tid);
+            const uint32_t pitch = static_cast<uint32_t>(N) * kSize;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                float c0 = acc_value<kFromAcc>(a.get(i)), c1 = acc_value<kFromAcc>(a.get(i + 1));
+                if constexpr (kAdd) {
+                    c0 += __builtin_bit_cast(float, kF32 ? x[i] : x[i] << 16);
+                    c1 += __builtin_bit_cast(float, kF32 ? x[i + 1] : x[i + 1] << 16);
+                }
+                const uint32_t v = voff[S::col_r(i) / 16];
+                const uint32_t row = static_cast<uint32_t>(tm * 32 + S::row_r(i)) * pitch;
+                if constexpr (kF32) {
+                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, c0), r,
+                                                          static_cast<int>(v), static_cast<int>(row), 0);
+                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, c1), r,
+                                                          static_cast<int>(v),
+                                                          static_cast<int>(row + pitch), 0);
+                } else {
+                    const uint32_t y = pack_bf16x2(c0, c1);
+                    store_b16(r, v, row, static_cast<uint16_t>(y));
+                    store_b16_hi(r, v, row + pitch, y);
+                }
+            }
+        }
+    };
+    template <bool kF32, bool kAdd>
+    __device__ __forceinline__ Mode<kF32, kAdd> mode() const {
+        Mode<kF32, kAdd> m;
+        m.C = C;
+        m.add = add;
+        m.M = M;
+        m.N = N;
+        return m;
+    }
+    template <class F>
+    __device__ __forceinline__ void by_mode(const F &f) const {
+        if (f32) {
+            if (add) f(mode<true, true>());
+            else f(mode<true, false>());
+        } else {
+            if (add) f(mode<false, true>());
+            else f(mode<false, false>());
+        }
+    }
+
+    template <class S>
+    static constexpr bool paired() { return false; }
+    template <class S>
+    static constexpr int unit_blocks() { return 1; }
+    template <class S>
+    __device__ __forceinline__ static int unit_block(int u, int) { return u; }
+    template <class S, bool kFromAcc = true>
+    __device__ __forceinline__ void unit(const typename S::Acc &a0, const typename S::Acc &a1, int u,
+                                         int m0, int n0, int tid) const {
+        by_mode([&](const auto &m) { m.template unit<S, kFromAcc>(a0, a1, u, m0, n0, tid); });
+    }
+    template <class S>
+    __device__ __forceinline__ void apply(const typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0,
+                                          int tid) const {
+        by_mode([&](const auto &m) { m.template apply<S>(acc, m0, n0, tid); });
+    }
+};
+
 // An epilogue whose projection has low-rank adapters beside it: their terms are
 // expanded into the accumulators before Base's epilogue (lora.hpp).
 template <class Base>
@@ -367,7 +640,8 @@ template <class S>
 struct QuarterOf {
     static constexpr int kStage = (S::BM / 2 + S::BN / 2) * S::kRowBytes;
     static constexpr int kStages = S::kLdsBytes / kStage < 4 ? S::kLdsBytes / kStage : 4;
-    using type = TileShape<S::BM / 2, S::BN / 2, S::BK, 2, 2, kStages, S::EB, kStages, S::MI>;
+    using type = TileShape<S::BM / 2, S::BN / 2, S::BK, 2, 2, kStages, S::EB, kStages, S::MI, S::kATr,
+                           S::kBTr>;
 };
 
 enum TailMode { kTailNone = 0, kTailSplit = 1, kTailQuarter = 2, kTailReduceInKernel = 3 };
@@ -558,7 +832,9 @@ template <class S, class Epi, int TAIL>
 __global__ __launch_bounds__(S::kThreads, S::kOccupancy) void gemm_tiles_kernel(
     KMajor Ak, KMajor B, int M, int K, Epi epi, Schedule sch) {
     __shared__ __attribute__((aligned(128))) char smem[S::kLdsBytes];
-    if (K % S::BK == 0) gemm_tiles_run<S, Epi, TAIL, true>(smem, Ak, B, M, K, epi, sch);
+    // (strided operands' loads are the same whatever K is)
+    if constexpr (S::kATr && S::kBTr) gemm_tiles_run<S, Epi, TAIL, true>(smem, Ak, B, M, K, epi, sch);
+    else if (K % S::BK == 0) gemm_tiles_run<S, Epi, TAIL, true>(smem, Ak, B, M, K, epi, sch);
     else gemm_tiles_run<S, Epi, TAIL, false>(smem, Ak, B, M, K, epi, sch);
 }
 
@@ -974,6 +1250,14 @@ using ShapeSmallLora = TileShape<128, 64, 64, 4, 1, 4, 2, 4, 16>;
 // a tile the smaller one is faster (M=33 K=8960, 1536 columns: 27.4 against
 // 29.5 us).
 using ShapeThinLora = TileShape<64, 128, 64, 2, 2, 4, 2, 4, 16>;
+// The gradients' products.  By an activation (dH, dA): K-contiguous gradient rows
+// times a weight contracted by its rows, a strided B.  By a weight: both operands
+// strided.  The rings and tiles of the shapes above.
+using ShapeWideDx = TileShape<256, 256, 64, 2, 2, 2, 2, 3, 16, false, true>;
+using ShapeQuadDx = TileShape<128, 128, 64, 2, 2, 2, 2, 2, 16, false, true>;
+using ShapeSmallDx = TileShape<128, 64, 64, 4, 1, 4, 2, 4, 16, false, true>;
+using ShapeWideDw = TileShape<256, 256, 64, 2, 2, 2, 2, 3, 16, true, true>;
+using ShapeQuadDw = TileShape<128, 128, 64, 2, 2, 2, 2, 2, 16, true, true>;
 // Variant I on FP8 operands: the same three shapes with K steps of 128 FP8
 // values, so every tile row of a stage is 128 bytes and the LDS rings, load
 // counts and swizzles are those of the bf16 shapes (the 256x256 one with a

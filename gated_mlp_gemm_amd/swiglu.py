@@ -82,6 +82,13 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
     lib.swiglu_down_proj_lora.argtypes = lib.swiglu_fused_gemm_lora.argtypes
     lib.swiglu_gated_mlp_lora.argtypes = [P, P, P, P, P, P, I64, I64, P, P, P, I64, I64, P, P, P, P,
                                           I64, I64, I64, I64, P, U64, P]
+    lib.swiglu_fused_gemm_train.argtypes = [P, P, P, P, I64, I64, I64, P, U64, P]
+    lib.swiglu_gated_mlp_train.argtypes = [P, P, P, P, P, P, I64, I64, I64, P, U64, P]
+    lib.swiglu_down_proj_backward.argtypes = [P, P, P, P, P, P, I32, I64, I64, I64, P, U64, P]
+    lib.swiglu_fused_gemm_backward.argtypes = [P, P, P, P, P, P, P, P, I32, I64, I64, I64, P, U64,
+                                               P]
+    lib.swiglu_gated_mlp_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, I32, I64, I64,
+                                              I64, P, U64, P]
     lib.swiglu_select_variant.argtypes = [I64, I64, I64]
     lib.swiglu_m_switch.argtypes = []
     lib.swiglu_m_switch.restype = I64
@@ -96,7 +103,9 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
                  "swiglu_fused_gemm_fp8", "swiglu_fused_gemm_strided",
                  "swiglu_fused_gemm_noalloc", "swiglu_route_workspace_size", "swiglu_route",
                  "swiglu_route_backward", "swiglu_lora_workspace_size", "swiglu_fused_gemm_lora",
-                 "swiglu_down_proj_lora", "swiglu_gated_mlp_lora"):
+                 "swiglu_down_proj_lora", "swiglu_gated_mlp_lora", "swiglu_fused_gemm_train",
+                 "swiglu_gated_mlp_train", "swiglu_down_proj_backward",
+                 "swiglu_fused_gemm_backward", "swiglu_gated_mlp_backward"):
         getattr(lib, name).restype = I32
     _lib = lib
     return lib
@@ -402,6 +411,190 @@ def swiglu_gated_mlp(A: torch.Tensor, W_fused: torch.Tensor, W3t: torch.Tensor,
         _check(lib.swiglu_gated_mlp(_ptr(A), _ptr(W_fused), _ptr(W3t), _ptr(H), _ptr(Out),
                                     M, N, K, v, ws, wsb, _stream(A.device)), "swiglu_gated_mlp")
     return Out, H
+
+
+# ---------------------------------------------------------------------------
+# training
+# ---------------------------------------------------------------------------
+_GRAD_TYPES = {torch.float32: SWIGLU_F32, torch.bfloat16: SWIGLU_BF16}
+
+
+def _out(t: Optional[torch.Tensor], name: str, shape, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    return _dev_tensor(t, name, shape)
+
+
+def _weight_grad(dW: Optional[torch.Tensor], add: Optional[torch.Tensor], name: str, shape, dtype,
+                 need: bool, device) -> Optional[torch.Tensor]:
+    """The gradient's tensor (None if it is not needed), once it and `add` fit."""
+    if not need:
+        if dW is not None or add is not None:
+            raise ValueError(f"{name} is given but not needed")
+        return None
+    if add is not None:
+        _dev_typed(add, f"{name}_add", dtype, shape)
+    if dW is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _dev_typed(dW, name, dtype, shape)
+
+
+def _grad_dtype(grad_dtype, *tensors) -> torch.dtype:
+    """The weights' gradients' type: what is asked for, else that of the first
+    tensor given, else bfloat16."""
+    if grad_dtype is None:
+        grad_dtype = next((t.dtype for t in tensors if isinstance(t, torch.Tensor)), torch.bfloat16)
+    if grad_dtype not in _GRAD_TYPES:
+        raise TypeError(f"weights' gradients are float32 or bfloat16, not {grad_dtype}")
+    return grad_dtype
+
+
+def swiglu_fused_gemm_train(A: torch.Tensor, W_fused: torch.Tensor,
+                            H: Optional[torch.Tensor] = None, GU: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None
+                            ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """swiglu_fused_gemm keeping Gate and Up for the gradients: (H [M, N], GU [M, 2N],
+    Gate and Up of an output side by side)."""
+    lib = load_library()
+    M, K = A.shape
+    N = W_fused.shape[0] // 2
+    _dev_tensor(A, "A", (M, K))
+    _dev_tensor(W_fused, "W_fused", (2 * N, K))
+    H, GU = _out(H, "H", (M, N), A.device), _out(GU, "GU", (M, 2 * N), A.device)
+    with _on_device(A.device):
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_fused_gemm_train(_ptr(A), _ptr(W_fused), _ptr(H), _ptr(GU), M, N, K, ws,
+                                           wsb, _stream(A.device)), "swiglu_fused_gemm_train")
+    return H, GU
+
+
+def swiglu_gated_mlp_train(A: torch.Tensor, W_fused: torch.Tensor, W3t: torch.Tensor,
+                           H: Optional[torch.Tensor] = None, GU: Optional[torch.Tensor] = None,
+                           Out: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None
+                           ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """swiglu_gated_mlp keeping what its gradients need; returns (Out, H, GU)."""
+    lib = load_library()
+    M, K = A.shape
+    N = W_fused.shape[0] // 2
+    _dev_tensor(A, "A", (M, K))
+    _dev_tensor(W_fused, "W_fused", (2 * N, K))
+    _dev_tensor(W3t, "W3t", (K, N))
+    H, GU = _out(H, "H", (M, N), A.device), _out(GU, "GU", (M, 2 * N), A.device)
+    Out = _out(Out, "Out", (M, K), A.device)
+    with _on_device(A.device):
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_gated_mlp_train(_ptr(A), _ptr(W_fused), _ptr(W3t), _ptr(H), _ptr(GU),
+                                          _ptr(Out), M, N, K, ws, wsb, _stream(A.device)),
+               "swiglu_gated_mlp_train")
+    return Out, H, GU
+
+
+def swiglu_down_proj_backward(dOut: torch.Tensor, H: torch.Tensor, W3t: torch.Tensor,
+                              dH: Optional[torch.Tensor] = None,
+                              dW3t: Optional[torch.Tensor] = None,
+                              dW3t_add: Optional[torch.Tensor] = None, need_dH: bool = True,
+                              need_dW: bool = True, grad_dtype=None,
+                              workspace: Optional[torch.Tensor] = None
+                              ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradients of swiglu_down_proj: (dH [M, N], dW3t [D, N]), None for one that is
+    not needed.  dW3t is float32 or bfloat16 (grad_dtype, else the type of dW3t or
+    dW3t_add, else bfloat16), dW3t_add (it may be dW3t) is added to it."""
+    lib = load_library()
+    M, N = H.shape
+    D = W3t.shape[0]
+    _dev_tensor(dOut, "dOut", (M, D))
+    _dev_tensor(H, "H", (M, N))
+    _dev_tensor(W3t, "W3t", (D, N))
+    dtype = _grad_dtype(grad_dtype, dW3t, dW3t_add)
+    if not need_dH and dH is not None:
+        raise ValueError("dH is given but not needed")
+    dH = _out(dH, "dH", (M, N), H.device) if need_dH else None
+    dW3t = _weight_grad(dW3t, dW3t_add, "dW3t", (D, N), dtype, need_dW, H.device)
+    if dH is None and dW3t is None:
+        return None, None
+    with _on_device(H.device):
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_down_proj_backward(_ptr(dOut), _ptr(H), _ptr(W3t), _ptr(dH), _ptr(dW3t),
+                                             _ptr(dW3t_add), _GRAD_TYPES[dtype], M, N, D, ws, wsb,
+                                             _stream(H.device)), "swiglu_down_proj_backward")
+    return dH, dW3t
+
+
+def swiglu_fused_gemm_backward(dH: torch.Tensor, A: torch.Tensor, W_fused: torch.Tensor,
+                               GU: torch.Tensor, dGU: Optional[torch.Tensor] = None,
+                               dA: Optional[torch.Tensor] = None,
+                               dW_fused: Optional[torch.Tensor] = None,
+                               dW_fused_add: Optional[torch.Tensor] = None, need_dA: bool = True,
+                               need_dW: bool = True, grad_dtype=None,
+                               workspace: Optional[torch.Tensor] = None
+                               ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor],
+                                          torch.Tensor]:
+    """Gradients of swiglu_fused_gemm_train by its H: (dA [M, K], dW_fused [2N, K],
+    dGU [M, 2N]), None for one that is not needed.  dGU may be GU, which is then
+    overwritten; dW_fused as dW3t in swiglu_down_proj_backward."""
+    lib = load_library()
+    M, K = A.shape
+    N = W_fused.shape[0] // 2
+    _dev_tensor(dH, "dH", (M, N))
+    _dev_tensor(A, "A", (M, K))
+    _dev_tensor(W_fused, "W_fused", (2 * N, K))
+    _dev_tensor(GU, "GU", (M, 2 * N))
+    dtype = _grad_dtype(grad_dtype, dW_fused, dW_fused_add)
+    if not need_dA and dA is not None:
+        raise ValueError("dA is given but not needed")
+    dGU = _out(dGU, "dGU", (M, 2 * N), A.device)
+    dA = _out(dA, "dA", (M, K), A.device) if need_dA else None
+    dW_fused = _weight_grad(dW_fused, dW_fused_add, "dW_fused", (2 * N, K), dtype, need_dW, A.device)
+    with _on_device(A.device):
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_fused_gemm_backward(_ptr(dH), _ptr(A), _ptr(W_fused), _ptr(GU), _ptr(dGU),
+                                              _ptr(dA), _ptr(dW_fused), _ptr(dW_fused_add),
+                                              _GRAD_TYPES[dtype], M, N, K, ws, wsb,
+                                              _stream(A.device)), "swiglu_fused_gemm_backward")
+    return dA, dW_fused, dGU
+
+
+def swiglu_gated_mlp_backward(dOut: torch.Tensor, A: torch.Tensor, W_fused: torch.Tensor,
+                              W3t: torch.Tensor, H: torch.Tensor, GU: torch.Tensor,
+                              dGU: Optional[torch.Tensor] = None,
+                              dA: Optional[torch.Tensor] = None,
+                              dW_fused: Optional[torch.Tensor] = None,
+                              dW_fused_add: Optional[torch.Tensor] = None,
+                              dW3t: Optional[torch.Tensor] = None,
+                              dW3t_add: Optional[torch.Tensor] = None, need_dA: bool = True,
+                              need_dW: bool = True, grad_dtype=None,
+                              workspace: Optional[torch.Tensor] = None
+                              ) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor],
+                                         Optional[torch.Tensor], torch.Tensor]:
+    """Gradients of swiglu_gated_mlp_train by its Out: (dA, dW_fused, dW3t, dGU), None
+    for one that is not needed (need_dW: both weights').  H and GU: what the forward
+    pass returned; dGU may be GU, which is then overwritten; the weights' gradients as
+    in swiglu_down_proj_backward, both of one type."""
+    lib = load_library()
+    M, K = A.shape
+    N = W_fused.shape[0] // 2
+    _dev_tensor(dOut, "dOut", (M, K))
+    _dev_tensor(A, "A", (M, K))
+    _dev_tensor(W_fused, "W_fused", (2 * N, K))
+    _dev_tensor(W3t, "W3t", (K, N))
+    _dev_tensor(H, "H", (M, N))
+    _dev_tensor(GU, "GU", (M, 2 * N))
+    dtype = _grad_dtype(grad_dtype, dW_fused, dW_fused_add, dW3t, dW3t_add)
+    if not need_dA and dA is not None:
+        raise ValueError("dA is given but not needed")
+    dGU = _out(dGU, "dGU", (M, 2 * N), A.device)
+    dA = _out(dA, "dA", (M, K), A.device) if need_dA else None
+    dW_fused = _weight_grad(dW_fused, dW_fused_add, "dW_fused", (2 * N, K), dtype, need_dW, A.device)
+    dW3t = _weight_grad(dW3t, dW3t_add, "dW3t", (K, N), dtype, need_dW, A.device)
+    with _on_device(A.device):
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_gated_mlp_backward(_ptr(dOut), _ptr(A), _ptr(W_fused), _ptr(W3t), _ptr(H),
+                                             _ptr(GU), _ptr(dGU), _ptr(dA), _ptr(dW_fused),
+                                             _ptr(dW_fused_add), _ptr(dW3t), _ptr(dW3t_add),
+                                             _GRAD_TYPES[dtype], M, N, K, ws, wsb,
+                                             _stream(A.device)), "swiglu_gated_mlp_backward")
+    return dA, dW_fused, dW3t, dGU
 
 
 def swiglu_silu_mul(gate: torch.Tensor, up: torch.Tensor,

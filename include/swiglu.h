@@ -84,7 +84,7 @@ typedef enum swiglu_variant {
     SWIGLU_VARIANT_I = 2  /* interleaved: one GEMM over W_fused, paired epilogue */
 } swiglu_variant;
 
-/* Element types of the router's logits (swiglu_route). */
+/* Element types of the router's logits (swiglu_route) and of weights' gradients. */
 typedef enum swiglu_type { SWIGLU_F32 = 0, SWIGLU_BF16 = 1 } swiglu_type;
 
 /*
@@ -272,6 +272,64 @@ int swiglu_gated_mlp(const uint16_t *A, const uint16_t *W_fused,
                      const uint16_t *W3t, uint16_t *H, uint16_t *Out,
                      int64_t M, int64_t N, int64_t K, int variant,
                      void *workspace, uint64_t workspace_bytes, void *stream);
+
+/*
+ * Training: the block's forward pass keeping what its gradients need, and the
+ * gradients.  With G = A . W1, U = A . W2, s(x) = 1 / (1 + exp(-x)):
+ *
+ *     H = bf16(G s(G) U),  GU = bf16(G, U),  Out = bf16(H . W3)
+ *     dH = dOut . W3^T                                (not stored by the block)
+ *     dU = dH G s(G),  dG = dH U s(G) (1 + G (1 - s(G))),  dGU = bf16(dG, dU)
+ *     dA = bf16(dGU . W_fused^T)                      [M][K]
+ *     dW_fused = dGU^T . A,  dW3t = dOut^T . H        as W_fused and W3t lie
+ *
+ * GU and dGU are [M][2N], Gate and Up of one output side by side, as W_fused's
+ * rows.  G and U of the gradients are those that GU holds.  dGU is rounded to bf16
+ * because it is an operand of the next two products' MFMAs; all sums are fp32, and
+ * every other output is rounded once.  Results are bitwise reproducible for the
+ * same arguments and workspace size.
+ *
+ * swiglu_fused_gemm_train      H, GU (variant I's kernel; nothing else is stored)
+ * swiglu_gated_mlp_train       H, GU, Out
+ * swiglu_down_proj_backward    dH (rounded to bf16), dW3t, of a given dOut; D is
+ *                              the model width, as in swiglu_down_proj
+ * swiglu_fused_gemm_backward   dGU, dA, dW_fused, of a given dH
+ * swiglu_gated_mlp_backward    dGU, dA, dW_fused, dW3t, of a given dOut
+ *
+ * A gradient that is NULL is not computed, and what only it reads may be NULL
+ * (frozen weights; the first layer).  dGU may be GU itself, which is then
+ * overwritten; it is always stored.  The weights' gradients are fp32 or bf16
+ * (grad_type: SWIGLU_F32, SWIGLU_BF16); with an `_add` matrix, of the same type and
+ * shape, they are the sum of it and the gradient, rounded once, and `_add` may be
+ * the gradient's own memory (sums over micro-batches).
+ * Preconditions: those of swiglu_fused_gemm and swiglu_down_proj, with
+ * M <= 2^30, N <= 2^20 (2^21 and D <= 2^21 in swiglu_down_proj_backward), N, D >= 8
+ * in the backward calls; matrices 16-byte aligned; nothing else overlaps an output.
+ * M == 0 is no rows: the weights' gradients are zeros (or `_add`), nothing else is
+ * written.  workspace: optional, as for swiglu_fused_gemm (size from
+ * swiglu_workspace_size(M, N, K, -1, ...)); the launches of a call share it.
+ */
+int swiglu_fused_gemm_train(const uint16_t *A, const uint16_t *W_fused, uint16_t *H,
+                            uint16_t *GU, int64_t M, int64_t N, int64_t K, void *workspace,
+                            uint64_t workspace_bytes, void *stream);
+int swiglu_gated_mlp_train(const uint16_t *A, const uint16_t *W_fused, const uint16_t *W3t,
+                           uint16_t *H, uint16_t *GU, uint16_t *Out, int64_t M, int64_t N,
+                           int64_t K, void *workspace, uint64_t workspace_bytes, void *stream);
+int swiglu_down_proj_backward(const uint16_t *dOut, const uint16_t *H, const uint16_t *W3t,
+                              uint16_t *dH, void *dW3t, const void *dW3t_add, int grad_type,
+                              int64_t M, int64_t N, int64_t D, void *workspace,
+                              uint64_t workspace_bytes, void *stream);
+int swiglu_fused_gemm_backward(const uint16_t *dH, const uint16_t *A, const uint16_t *W_fused,
+                               const uint16_t *GU, uint16_t *dGU, uint16_t *dA, void *dW_fused,
+                               const void *dW_fused_add, int grad_type, int64_t M, int64_t N,
+                               int64_t K, void *workspace, uint64_t workspace_bytes,
+                               void *stream);
+int swiglu_gated_mlp_backward(const uint16_t *dOut, const uint16_t *A, const uint16_t *W_fused,
+                              const uint16_t *W3t, const uint16_t *H, const uint16_t *GU,
+                              uint16_t *dGU, uint16_t *dA, void *dW_fused,
+                              const void *dW_fused_add, void *dW3t, const void *dW3t_add,
+                              int grad_type, int64_t M, int64_t N, int64_t K, void *workspace,
+                              uint64_t workspace_bytes, void *stream);
 
 /*
  * FP8 inputs.  The pages' motivation is that quantisation (FP8, INT4) makes
