@@ -4,6 +4,7 @@
 
 Compiles ``csrc/kernels.hip`` (elementwise kernels and the launch dispatch),
 ``csrc/lora_kernels.hip`` (low-rank adapters), ``csrc/route_kernels.hip`` (the router),
+``csrc/mx4_kernels.hip`` (4-bit weights),
 ``csrc/kernel_instances.hip`` once per group of its instance list (the tile
 kernels, one object per group) and ``csrc/api.cpp`` (the C ABI) with hipcc,
 in parallel (``--jobs``, else ``MAX_JOBS``, else the CPU count), and links
@@ -76,6 +77,7 @@ def _objects():
     objs = [(f"inst{g:02d}", INSTANCES, [f"-DSWIGLU_INSTANCE={g}"])
             for g in range(instance_groups())]
     objs.append(("lora", os.path.join(CSRC, "lora_kernels.hip"), []))
+    objs.append(("mx4", os.path.join(CSRC, "mx4_kernels.hip"), []))
     objs.append(("route", os.path.join(CSRC, "route_kernels.hip"), []))
     objs.append(("kernels", os.path.join(CSRC, "kernels.hip"), []))
     objs.append(("api", os.path.join(CSRC, "api.cpp"), ["-x", "hip"]))

@@ -299,6 +299,19 @@ int check_grad_type(int grad_type) {
         return fail(SWIGLU_ERR_UNSUPPORTED, "unknown gradient type %d", grad_type);
     return SWIGLU_OK;
 }
+// A contraction over 4-bit weights: whole groups.
+int check_mx4_groups(const char *name, int64_t n) {
+    if (n < 32 || n % 32 != 0)
+        return fail(SWIGLU_ERR_SHAPE, "%s=%lld must be a positive multiple of 32", name, (long long)n);
+    return SWIGLU_OK;
+}
+int check_mx4_matrix(int64_t rows, int64_t K) {
+    int st = check_mx4_groups("K", K);
+    if (st != SWIGLU_OK) return st;
+    if (rows < 0 || rows > 2 * kMaxN || K > kMaxK)
+        return fail(SWIGLU_ERR_SHAPE, "size beyond limits (0<=rows<=2^23, K<=2^21)");
+    return SWIGLU_OK;
+}
 int grad_size(int grad_type) { return grad_type == SWIGLU_F32 ? 4 : 2; }
 // A sum that a weight's gradient is added to may be the gradient itself.
 const void *add_operand(const void *add, const void *dW) { return add == dW ? nullptr : add; }
@@ -1122,6 +1135,123 @@ int swiglu_gated_mlp_backward(const uint16_t *dOut, const uint16_t *A, const uin
         e = swiglu::launch_weight_grad(dGU, A, dW_fused, dW_fused_add, f32, (int)M, (int)(2 * N),
                                        (int)K, ws, s);
     return launched(e, "gated MLP backward");
+}
+
+int swiglu_quantize_mx4(const uint16_t *X, uint8_t *Q, uint8_t *S, int64_t rows, int64_t K,
+                        void *stream) {
+    int st = check_mx4_matrix(rows, K);
+    if (st != SWIGLU_OK) return st;
+    if (rows == 0) return ok();
+    const Operand ops[] = {
+        {"X", X, rows * K * 2, 16, false, false},
+        {"Q", Q, rows * K / 2, 16, true, false},
+        {"S", S, rows * K / 32, 1, true, false},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st == SWIGLU_OK) st = check_device();
+    if (st != SWIGLU_OK) return st;
+    return launched(swiglu::launch_quantize_mx4(X, Q, S, rows * K, (hipStream_t)stream),
+                    "4-bit quantizer");
+}
+
+int swiglu_dequantize_mx4(const uint8_t *Q, const uint8_t *S, uint16_t *X, int64_t rows, int64_t K,
+                          void *stream) {
+    int st = check_mx4_matrix(rows, K);
+    if (st != SWIGLU_OK) return st;
+    if (rows == 0) return ok();
+    const Operand ops[] = {
+        {"Q", Q, rows * K / 2, 16, false, false},
+        {"S", S, rows * K / 32, 1, false, false},
+        {"X", X, rows * K * 2, 16, true, false},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st == SWIGLU_OK) st = check_device();
+    if (st != SWIGLU_OK) return st;
+    return launched(swiglu::launch_dequantize_mx4(Q, S, X, rows * K, (hipStream_t)stream),
+                    "4-bit dequantizer");
+}
+
+int swiglu_fused_gemm_mx4(const uint16_t *A, const uint8_t *Wq, const uint8_t *Ws, uint16_t *Y,
+                          int64_t M, int64_t N, int64_t K, void *workspace,
+                          uint64_t workspace_bytes, void *stream) {
+    int st = check_gemm_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_mx4_groups("K", K);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0 || N == 0) return ok();
+    const Operand ops[] = {
+        {"A", A, M * K * 2, 16, false, false},
+        {"Wq", Wq, N * K, 16, false, false},
+        {"Ws", Ws, N * K / 16, 1, false, false},
+        {"Y", Y, M * N * 2, 16, true, false},
+        {"workspace", workspace, (int64_t)workspace_bytes, 256, true, true},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    return launched(swiglu::launch_fused_mx4(A, Wq, Ws, Y, (int)M, (int)N, (int)K,
+                                             make_ws(workspace, workspace_bytes, cus),
+                                             (hipStream_t)stream),
+                    "fused 4-bit");
+}
+
+int swiglu_down_proj_mx4(const uint16_t *H, const uint8_t *W3q, const uint8_t *W3s, uint16_t *Out,
+                         int64_t M, int64_t N, int64_t D, void *workspace,
+                         uint64_t workspace_bytes, void *stream) {
+    int st = check_down_shape(M, N, D);
+    if (st == SWIGLU_OK) st = check_mx4_groups("N", N);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0 || D == 0) return ok();
+    const Operand ops[] = {
+        {"H", H, M * N * 2, 16, false, false},
+        {"W3q", W3q, D * N / 2, 16, false, false},
+        {"W3s", W3s, D * N / 32, 1, false, false},
+        {"Out", Out, M * D * 2, 16, true, false},
+        {"workspace", workspace, (int64_t)workspace_bytes, 256, true, true},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    return launched(swiglu::launch_down_proj_mx4(H, W3q, W3s, Out, (int)M, (int)N, (int)D,
+                                                 make_ws(workspace, workspace_bytes, cus),
+                                                 (hipStream_t)stream),
+                    "down projection 4-bit");
+}
+
+int swiglu_gated_mlp_mx4(const uint16_t *A, const uint8_t *Wq, const uint8_t *Ws,
+                         const uint8_t *W3q, const uint8_t *W3s, uint16_t *H, uint16_t *Out,
+                         int64_t M, int64_t N, int64_t K, void *workspace,
+                         uint64_t workspace_bytes, void *stream) {
+    int st = check_gemm_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_down_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_mx4_groups("K", K);
+    if (st == SWIGLU_OK) st = check_mx4_groups("N", N);
+    if (st != SWIGLU_OK) return st;
+    if (M == 0) return ok();
+    const Operand ops[] = {
+        {"A", A, M * K * 2, 16, false, false},
+        {"Wq", Wq, N * K, 16, false, false},
+        {"Ws", Ws, N * K / 16, 1, false, false},
+        {"W3q", W3q, K * N / 2, 16, false, false},
+        {"W3s", W3s, K * N / 32, 1, false, false},
+        {"H", H, M * N * 2, 16, true, false},
+        {"Out", Out, M * K * 2, 16, true, false},
+        {"workspace", workspace, (int64_t)workspace_bytes, 256, true, true},
+    };
+    st = check_operands(ops, sizeof ops / sizeof ops[0]);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    const hipStream_t s = (hipStream_t)stream;
+    const swiglu::GemmWorkspace ws = make_ws(workspace, workspace_bytes, cus);
+    const hipError_t e = swiglu::launch_fused_mx4(A, Wq, Ws, H, (int)M, (int)N, (int)K, ws, s);
+    if (e != hipSuccess) return launched(e, "gated MLP 4-bit: fused SwiGLU");
+    return launched(swiglu::launch_down_proj_mx4(H, W3q, W3s, Out, (int)M, (int)N, (int)K, ws, s),
+                    "gated MLP 4-bit: down projection");
 }
 
 }  // extern "C"

@@ -44,6 +44,10 @@
 // same rings, loads and MFMAs: its panel lies in LDS in pieces of 4 k x 32
 // columns (256 bytes), and a fragment is two transposing 64-bit reads, each
 // 4 k x 16 columns of one piece (StridedLoader, TrFrag).
+//
+// 4-bit weights.  A shape may take B as 4-bit codes with a power of two for each
+// 32 k (kBMx4): its panel goes through registers, where the codes become bf16
+// exactly, into the same LDS layout (Mx4Loader).
 #pragma once
 
 #include <type_traits>
@@ -63,7 +67,8 @@ namespace swiglu {
 // registers of the 32x32 one.  A K step of BK elements moves BK * EB bytes
 // per tile row either way.
 template <int BM_, int BN_, int BK_, int WM_, int WN_, int STAGES_, int EB_ = 2,
-          int BSTAGES_ = STAGES_, int MI_ = 32, bool ATR_ = false, bool BTR_ = false>
+          int BSTAGES_ = STAGES_, int MI_ = 32, bool ATR_ = false, bool BTR_ = false,
+          bool BMX4_ = false>
 struct TileShape {
     static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_;
     static constexpr int STAGES = STAGES_;     // A ring
@@ -71,6 +76,7 @@ struct TileShape {
     static constexpr int MI = MI_;
     static constexpr int EB = EB_;
     static constexpr bool kATr = ATR_, kBTr = BTR_;   // strided operands
+    static constexpr bool kBMx4 = BMX4_;              // 4-bit weights
     static constexpr int kWaves = WM * WN;
     static constexpr int kThreads = 64 * kWaves;
     static constexpr int kWaveM = BM / WM;
@@ -95,6 +101,12 @@ struct TileShape {
     static constexpr int kDmaA = kABytes / (kThreads * 16);
     static constexpr int kDmaB = kBBytes / (kThreads * 16);
     static constexpr int kDmaPerStep = kDmaA + kDmaB;
+    // 4-bit weights: bytes of codes a lane takes from one row at once, how often a
+    // K step, and its loads into registers (codes and a scale each)
+    static constexpr int kMx4Bytes = BN * BK / 2 / kThreads < 16 ? BN * BK / 2 / kThreads : 16;
+    static constexpr int kMx4Units = BN * BK / 2 / (kThreads * kMx4Bytes);
+    // vector memory loads that count in vmcnt for B, a K step
+    static constexpr int kVmB = BMX4_ ? 2 * kMx4Units : kDmaB;
     // workgroups resident per CU that the kernel is built for: two when two
     // fit the 160 KiB of LDS (the kernel then keeps to 256 registers a lane)
     static constexpr int kOccupancy = (2 * kLdsBytes <= 160 * 1024) ? 2 : 1;
@@ -111,6 +123,8 @@ struct TileShape {
     static_assert(kDmaA * STAGES + kDmaB * BSTAGES < 64, "vmcnt is a 6-bit counter");
     static_assert(kWaves == 4, "4 waves, one per SIMD (the pipeline below)");
     static_assert((!kATr && !kBTr) || (MI == 16 && BK == 64), "strided operands: bf16, 16x16 MFMAs");
+    static_assert(!kBMx4 || (MI == 16 && BK == 64 && !kATr && !kBTr && BSTAGES == 2),
+                  "4-bit weights: K-contiguous, 16x16 MFMAs, two stages");
 
     // Row and column, within its 32x32 block, of accumulator register r of
     // lane l: row_l(l) + row_r(r) and col_l(l) + col_r(r) (device.hpp gives
@@ -191,6 +205,9 @@ struct KMajor {
     // Elements from one physical row to the next (a row-strided view); 0: K
     // (contiguous rows).
     int ld;
+    // 4-bit weights: base holds codes [rows][K / 2], and these are the exponents
+    // (plus 127) of the powers of two [rows][K / 32].
+    const uint8_t *scales;
 };
 
 // Panel row whose data lands in LDS row `r` of a de-interleaved panel: within
@@ -372,21 +389,137 @@ struct StridedLoader {
     }
 };
 
+template <int OFF>
+__device__ __forceinline__ void asm_write_b128(uint32_t addr, const u32x4 &v) {
+    asm volatile("ds_write_b128 %0, %1 offset:%2" ::"v"(addr), "v"(v), "i"(OFF));
+}
+
+// A panel of 4-bit weights (E2M1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives;
+// the even k in a byte's low half).  A lane takes kMx4Bytes of codes of one row
+// and their scale into registers two K steps before it converts them
+// (v_cvt_scalef32_pk_bf16_fp4: exact, a number of 2 bits times a power of two) and
+// writes them to where the direct-to-LDS loads of a bf16 panel would have put
+// them.  issue() keeps the panel loaders' interface: its load j converts and
+// writes one 16-byte chunk, the last one also fetches the codes of two steps on
+// into the registers just emptied.  The ring has two stages, and a step's stage is
+// its registers' too.
+//
+// Converting here and not where the fragments are read halves the conversions (two
+// waves read each fragment) and leaves the MFMAs' operands to LDS reads alone.
+template <class S, int NROWS, int NDMA>
+struct Mx4Loader {
+    static constexpr int kBytes = S::kMx4Bytes, kUnits = S::kMx4Units;
+    static constexpr int kWords = kBytes / 4;                  // chunks of 8 k
+    static constexpr int kPerRow = S::BK / 2 / kBytes;         // lanes of a row
+    static constexpr int kRows = S::kThreads / kPerRow;        // rows of a unit
+    static_assert(kUnits * kWords == NDMA && kUnits * kRows == NROWS && kRows % 32 == 0,
+                  "the chunks of a panel, whole periods of the swizzle a unit");
+    struct Raw {
+        uint32_t w[kUnits][kWords];
+        uint32_t scale[kUnits];
+    };
+    __amdgpu_buffer_rsrc_t codes, scales;
+    uint32_t voff[kUnits], soff[kUnits];   // byte offsets of the lane's codes and scale at k0 = 0
+    uint32_t out[kWords];                  // LDS addresses of the lane's chunks, stage 0, unit 0
+    SWIGLU_LDS char *ring;                 // the B ring
+    int klim;                              // K minus the first k of the lane's codes
+    int klen;
+    mutable Raw raw[2];
+
+    __device__ __forceinline__ void init(const KMajor &op, int r0, int K, SWIGLU_LDS char *ring_,
+                                         int k_first) {
+        const int row_bytes = K / 2, row_scales = K / 32;
+        const int64_t left = op.rows > r0 ? op.rows - r0 : 0;
+        codes = make_rsrc(static_cast<const char *>(op.base) + static_cast<int64_t>(r0) * row_bytes,
+                          static_cast<uint32_t>(min(left, static_cast<int64_t>(NROWS)) * row_bytes));
+        scales = make_rsrc(op.scales + static_cast<int64_t>(r0) * row_scales,
+                           static_cast<uint32_t>(min(left, static_cast<int64_t>(NROWS)) * row_scales));
+        ring = ring_;
+        klen = K;
+        const int tid = threadIdx.x;
+        const int part = tid % kPerRow;
+        klim = K - part * kBytes * 2;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int r = u * kRows + tid / kPerRow;
+            const int g = op.pairs ? pair_row(r) : r;
+            voff[u] = static_cast<uint32_t>(g) * row_bytes + part * kBytes;
+            soff[u] = static_cast<uint32_t>(g) * row_scales + part * kBytes / 16;
+        }
+        const int r = tid / kPerRow;
+        const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(ring_));
+#pragma unroll
+        for (int c = 0; c < kWords; ++c)
+            out[c] = base + r * S::kRowBytes + (((part * kWords + c) ^ swz<S>(r)) * 16);
+        fetch(raw[0], k_first);
+        fetch(raw[1], k_first + S::BK);
+    }
+    // (codes past K read zeros, and so do their scales: nothing of the next row)
+    __device__ __forceinline__ void fetch(Raw &x, int k0) const {
+        const bool in = k0 < klim;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int v = static_cast<int>(in ? voff[u] : kOutOfRange);
+            if constexpr (kBytes == 16) {
+                const u32x4 y = __builtin_amdgcn_raw_buffer_load_b128(codes, v, k0 / 2, 0);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) x.w[u][c] = y[c];
+            } else {
+                const u32x2 y = __builtin_amdgcn_raw_buffer_load_b64(codes, v, k0 / 2, 0);
+                x.w[u][0] = y[0];
+                x.w[u][1] = y[1];
+            }
+            x.scale[u] = __builtin_amdgcn_raw_buffer_load_b8(
+                scales, static_cast<int>(in ? soff[u] : kOutOfRange), k0 / 32, 0);
+        }
+    }
+    template <int STAGE, int U, int C>
+    __device__ __forceinline__ void write(const Raw &x) const {
+        const uint32_t w = x.w[U][C];
+        const float s = __builtin_bit_cast(float, x.scale[U] << 23);
+        u32x4 v;
+        v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+        v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+        v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+        v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+        asm_write_b128<STAGE * S::kBBytes + U * kRows * S::kRowBytes>(out[C], v);
+    }
+    template <int STAGE, int... J>
+    __device__ __forceinline__ void issue_stage(int k0, int only,
+                                                std::integer_sequence<int, J...>) const {
+        (
+            [&] {
+                if (only < 0 || only == J) write<STAGE, J / kWords, J % kWords>(raw[STAGE]);
+            }(),
+            ...);
+        if (only < 0 || only == NDMA - 1) fetch(raw[STAGE], k0 + 2 * S::BK);
+    }
+    template <bool kEven = false>
+    __device__ __forceinline__ void issue(int k0, SWIGLU_LDS char *panel_lds, int only = -1) const {
+        if (panel_lds == ring) issue_stage<0>(k0, only, std::make_integer_sequence<int, NDMA>{});
+        else issue_stage<1>(k0, only, std::make_integer_sequence<int, NDMA>{});
+    }
+};
+
 // Loader of one output tile: the A panel and the B panel of each K step.
 template <class S>
 struct TileLoader {
     typename std::conditional<S::kATr, StridedLoader<S, S::BM, S::kDmaA>,
                               PanelLoader<S, S::BM, S::kDmaA>>::type a;
-    using PanelB = typename std::conditional<S::kBTr, StridedLoader<S, S::BN, S::kDmaB>,
-                                             PanelLoader<S, S::BN, S::kDmaB>>::type;
+    using PanelB = typename std::conditional<
+        S::kBMx4, Mx4Loader<S, S::BN, S::kDmaB>,
+        typename std::conditional<S::kBTr, StridedLoader<S, S::BN, S::kDmaB>,
+                                  PanelLoader<S, S::BN, S::kDmaB>>::type>::type;
     PanelB b;
     int K;
 
-    __device__ __forceinline__ void init(const KMajor &A, int m0, const KMajor &B, int n0,
-                                         int K_) {
+    // lds: the rings; kb: the first K step that is loaded
+    __device__ __forceinline__ void init(const KMajor &A, int m0, const KMajor &B, int n0, int K_,
+                                         SWIGLU_LDS char *lds = nullptr, int kb = 0) {
         K = K_;
         a.init(A, m0, K_);
-        b.init(B, n0, K_);
+        if constexpr (S::kBMx4) b.init(B, n0, K_, lds + S::kBRing, kb * S::BK);
+        else b.init(B, n0, K_);
     }
 
     // Load the A (part 0) or B (part 1, from panel `bp`) panel of K step
@@ -520,8 +653,9 @@ struct IssueOrder {
                 const bool a_part = (k == 0) == kAFirst;
                 const int step = g + (a_part ? S::STAGES : S::BSTAGES);
                 if (step < 0) continue;
-                total += a_part ? S::kDmaA : S::kDmaB;
-                if (step == s) (a_part ? end_a : end_b) = total;
+                total += a_part ? S::kDmaA : S::kVmB;
+                // (4-bit weights are awaited where they are converted)
+                if (step == s && (a_part || !S::kBMx4)) (a_part ? end_a : end_b) = total;
             }
         }
         return total - (end_a > end_b ? end_a : end_b);
@@ -841,6 +975,7 @@ struct Pipeline {
     }
     __device__ __forceinline__ void prologue_wait() {
         wait_vmcnt<Order::kWaitPrologue>();
+        if constexpr (S::kBMx4) asm volatile("s_waitcnt lgkmcnt(0)");   // the panels written here
         block_barrier();
         read_frags<S, 0>(addr_a(0), addr_b(0), off, f[0]);
     }

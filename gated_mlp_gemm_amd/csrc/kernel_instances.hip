@@ -156,6 +156,26 @@ template struct ReduceLaunch<ShapeQuad, PairMulKeep>;
 template struct ReduceLaunch<ShapeSmallDx, GateGradEpilogue>;
 template struct ReduceLaunch<ShapeSmallDx, StoreEpilogue>;
 template struct ReduceLaunch<ShapeSmallLora, PairMulKeep>;
+#elif SWIGLU_INSTANCE == 30
+template struct TilesLaunch<ShapeWideMx4, PairMulEpilogue, kTailSplit>;
+#elif SWIGLU_INSTANCE == 31
+template struct TilesLaunch<ShapeWideMx4, StoreEpilogue, kTailSplit>;
+#elif SWIGLU_INSTANCE == 32
+template struct TilesLaunch<ShapeQuadMx4, PairMulEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeQuadMx4, StoreEpilogue, kTailSplit>;
+#elif SWIGLU_INSTANCE == 33
+template struct TilesLaunch<ShapeSmallMx4, PairMulEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeSmallMx4, StoreEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeThinMx4, PairMulEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeThinMx4, StoreEpilogue, kTailSplit>;
+template struct ReduceLaunch<ShapeWideMx4, PairMulEpilogue>;
+template struct ReduceLaunch<ShapeWideMx4, StoreEpilogue>;
+template struct ReduceLaunch<ShapeQuadMx4, PairMulEpilogue>;
+template struct ReduceLaunch<ShapeQuadMx4, StoreEpilogue>;
+template struct ReduceLaunch<ShapeSmallMx4, PairMulEpilogue>;
+template struct ReduceLaunch<ShapeSmallMx4, StoreEpilogue>;
+template struct ReduceLaunch<ShapeThinMx4, PairMulEpilogue>;
+template struct ReduceLaunch<ShapeThinMx4, StoreEpilogue>;
 #else
 #error "SWIGLU_INSTANCE is past the end of the instance list"
 #endif

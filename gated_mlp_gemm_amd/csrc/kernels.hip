@@ -750,6 +750,32 @@ hipError_t launch_weight_grad(const uint16_t *dY, const uint16_t *X, void *dW, c
     return launch_split_gemm<ShapeWideDw>(A, B, rows, cols, M, epi, ws, stream);
 }
 
+// ---------------------------------------------------------------------------
+// 4-bit weights
+// ---------------------------------------------------------------------------
+template <class Epi>
+static hipError_t launch_mx4(const uint16_t *X, const KMajor &B, int M, int cols, int K,
+                             const Epi &epi, const GemmWorkspace &ws, hipStream_t stream) {
+    const KMajor A{X, M, 1, 0, 0, 0, nullptr};
+    if (M <= ShapeThinMx4::BM && cdiv(cols, ShapeThinMx4::BN) >= ws.cus)
+        return launch_split_gemm<ShapeThinMx4>(A, B, M, cols, K, epi, ws, stream);
+    if (M <= 128) return launch_split_gemm<ShapeSmallMx4>(A, B, M, cols, K, epi, ws, stream);
+    if (quad_split_faster<ShapeWideMx4, ShapeQuadMx4>(M, cols, K, ws))
+        return launch_split_gemm<ShapeQuadMx4>(A, B, M, cols, K, epi, ws, stream);
+    return launch_split_gemm<ShapeWideMx4>(A, B, M, cols, K, epi, ws, stream);
+}
+hipError_t launch_fused_mx4(const uint16_t *A, const uint8_t *Wq, const uint8_t *Ws, uint16_t *Y,
+                            int M, int N, int K, const GemmWorkspace &ws, hipStream_t stream) {
+    return launch_mx4(A, KMajor{Wq, 2 * N, 1, 0, 0, 0, Ws}, M, 2 * N, K,
+                      PairMulEpilogue{Y, M, N, N, 1.0f}, ws, stream);
+}
+hipError_t launch_down_proj_mx4(const uint16_t *H, const uint8_t *W3q, const uint8_t *W3s,
+                                uint16_t *Out, int M, int N, int D, const GemmWorkspace &ws,
+                                hipStream_t stream) {
+    return launch_mx4(H, KMajor{W3q, D, 1, 0, 0, 0, W3s}, M, D, N, StoreEpilogue{Out, M, D}, ws,
+                      stream);
+}
+
 // dGU of a given dH: the epilogue's arithmetic, 8 outputs of H a lane.
 __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t *__restrict__ dH,
                                                         const uint16_t *GU, uint16_t *dGU,

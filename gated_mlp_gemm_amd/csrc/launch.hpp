@@ -72,6 +72,16 @@ hipError_t launch_gate_grad(const uint16_t *dH, const uint16_t *GU, uint16_t *dG
 hipError_t launch_weight_grad(const uint16_t *dY, const uint16_t *X, void *dW, const void *add,
                               bool f32, int M, int rows, int cols, const GemmWorkspace &ws,
                               hipStream_t stream);
+// 4-bit weights: codes [rows][K / 2] and scales [rows][K / 32] of `count` numbers.
+hipError_t launch_quantize_mx4(const uint16_t *x, uint8_t *q, uint8_t *s, int64_t count,
+                               hipStream_t stream);
+hipError_t launch_dequantize_mx4(const uint8_t *q, const uint8_t *s, uint16_t *x, int64_t count,
+                                 hipStream_t stream);
+hipError_t launch_fused_mx4(const uint16_t *A, const uint8_t *Wq, const uint8_t *Ws, uint16_t *Y,
+                            int M, int N, int K, const GemmWorkspace &ws, hipStream_t stream);
+hipError_t launch_down_proj_mx4(const uint16_t *H, const uint8_t *W3q, const uint8_t *W3s,
+                                uint16_t *Out, int M, int N, int D, const GemmWorkspace &ws,
+                                hipStream_t stream);
 // FP8 (E4M3) path: q = fp8(x * 2^-scale_exp); variant I on FP8 operands with
 // the epilogue scaling Gate and Up by `scale` (= 2^(a_exp + w_exp)).
 hipError_t launch_quantize_fp8(const uint16_t *x, uint8_t *q, int64_t count, int scale_exp,

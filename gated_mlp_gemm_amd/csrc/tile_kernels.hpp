@@ -617,7 +617,7 @@ __device__ __forceinline__ void tile_mainloop(SWIGLU_LDS char *lds, const KMajor
     Pipeline<S> pl;
     pl.init(lds);
     TileLoader<S> ld;
-    ld.init(A, m0, B, n0, K);
+    ld.init(A, m0, B, n0, K, lds, kb);
     const int len = ke - kb;
     // steps past the range load nothing (K step nk is past the end of K)
     auto issue = [&](int s, int part, SWIGLU_LDS char *dst, int j) {
@@ -686,7 +686,7 @@ __device__ __forceinline__ bool gemm_tiles_body(char *smem, const KMajor &Ak, co
             TileLoader<S> ld;
             int j = b, tm, tn;
             tile_coords(xcd_order(j, sch.dp), sch.tiles_m, sch.tiles_n, sch.group_m, tm, tn);
-            ld.init(Ak, tm * S::BM, B, tn * S::BN, K);
+            ld.init(Ak, tm * S::BM, B, tn * S::BN, K, lds);
             const int nk = sch.nk;
             // steps past the end load nothing (K step nk is past the end of K)
             auto issue = [&](int s, int part, SWIGLU_LDS char *dst, int j) {
@@ -706,7 +706,7 @@ __device__ __forceinline__ bool gemm_tiles_body(char *smem, const KMajor &Ak, co
                 if (j + grid < sch.dp) {
                     tile_coords(xcd_order(j + grid, sch.dp), sch.tiles_m, sch.tiles_n, sch.group_m, tm,
                                 tn);
-                    ld.init(Ak, tm * S::BM, B, tn * S::BN, K);
+                    ld.init(Ak, tm * S::BM, B, tn * S::BN, K, lds);
                     pl.prologue_issue(issue);
                 }
                 epi.template apply<S>(acc, m0, n0, adapters.thread());
@@ -1258,6 +1258,12 @@ using ShapeQuadDx = TileShape<128, 128, 64, 2, 2, 2, 2, 2, 16, false, true>;
 using ShapeSmallDx = TileShape<128, 64, 64, 4, 1, 4, 2, 4, 16, false, true>;
 using ShapeWideDw = TileShape<256, 256, 64, 2, 2, 2, 2, 3, 16, true, true>;
 using ShapeQuadDw = TileShape<128, 128, 64, 2, 2, 2, 2, 2, 16, true, true>;
+// 4-bit weights (codes through registers into a two-stage ring).  The 256x256 and
+// 128x128 tiles of the shapes above, and tiles of few rows with 16x16 MFMAs.
+using ShapeWideMx4 = TileShape<256, 256, 64, 2, 2, 2, 2, 2, 16, false, false, true>;
+using ShapeQuadMx4 = TileShape<128, 128, 64, 2, 2, 2, 2, 2, 16, false, false, true>;
+using ShapeSmallMx4 = TileShape<128, 64, 64, 4, 1, 4, 2, 2, 16, false, false, true>;
+using ShapeThinMx4 = TileShape<64, 128, 64, 2, 2, 4, 2, 2, 16, false, false, true>;
 // Variant I on FP8 operands: the same three shapes with K steps of 128 FP8
 // values, so every tile row of a stage is 128 bytes and the LDS rings, load
 // counts and swizzles are those of the bf16 shapes (the 256x256 one with a

@@ -89,6 +89,11 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
                                                P]
     lib.swiglu_gated_mlp_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, I32, I64, I64,
                                               I64, P, U64, P]
+    lib.swiglu_quantize_mx4.argtypes = [P, P, P, I64, I64, P]
+    lib.swiglu_dequantize_mx4.argtypes = [P, P, P, I64, I64, P]
+    lib.swiglu_fused_gemm_mx4.argtypes = [P, P, P, P, I64, I64, I64, P, U64, P]
+    lib.swiglu_down_proj_mx4.argtypes = [P, P, P, P, I64, I64, I64, P, U64, P]
+    lib.swiglu_gated_mlp_mx4.argtypes = [P, P, P, P, P, P, P, I64, I64, I64, P, U64, P]
     lib.swiglu_select_variant.argtypes = [I64, I64, I64]
     lib.swiglu_m_switch.argtypes = []
     lib.swiglu_m_switch.restype = I64
@@ -105,7 +110,9 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
                  "swiglu_route_backward", "swiglu_lora_workspace_size", "swiglu_fused_gemm_lora",
                  "swiglu_down_proj_lora", "swiglu_gated_mlp_lora", "swiglu_fused_gemm_train",
                  "swiglu_gated_mlp_train", "swiglu_down_proj_backward",
-                 "swiglu_fused_gemm_backward", "swiglu_gated_mlp_backward"):
+                 "swiglu_fused_gemm_backward", "swiglu_gated_mlp_backward", "swiglu_quantize_mx4",
+                 "swiglu_dequantize_mx4", "swiglu_fused_gemm_mx4", "swiglu_down_proj_mx4",
+                 "swiglu_gated_mlp_mx4"):
         getattr(lib, name).restype = I32
     _lib = lib
     return lib
@@ -950,6 +957,102 @@ def swiglu_gated_mlp_lora(A: torch.Tensor, W_fused: torch.Tensor, W3t: torch.Ten
         _check(lib.swiglu_gated_mlp_lora(_ptr(A), _ptr(W_fused), _ptr(W3t), *up, *dn, _ptr(ids),
                                          _ptr(weights), _ptr(H), _ptr(Out), M, N, K, J, ws, wsb,
                                          _stream(A.device)), "swiglu_gated_mlp_lora")
+    return Out, H
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights
+# ---------------------------------------------------------------------------
+def _mx4(Q: torch.Tensor, S: torch.Tensor, names, rows: int, K: int):
+    """The codes [rows, K / 2] and scales [rows, K / 32] of a matrix."""
+    _dev_typed(Q, names[0], torch.uint8, (rows, K // 2))
+    _dev_typed(S, names[1], torch.uint8, (rows, K // 32))
+
+
+def swiglu_quantize_mx4(X: torch.Tensor, Q: Optional[torch.Tensor] = None,
+                        S: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """4-bit codes and scales of X [rows, K] (K a multiple of 32), e.g. of W_fused or
+    W3t: (Q [rows, K / 2], S [rows, K / 32]), both uint8."""
+    lib = load_library()
+    rows, K = X.shape
+    _dev_tensor(X, "X", (rows, K))
+    if Q is None:
+        Q = torch.empty((rows, K // 2), dtype=torch.uint8, device=X.device)
+    if S is None:
+        S = torch.empty((rows, K // 32), dtype=torch.uint8, device=X.device)
+    _mx4(Q, S, ("Q", "S"), rows, K)
+    with _on_device(X.device):
+        _check(lib.swiglu_quantize_mx4(_ptr(X), _ptr(Q), _ptr(S), rows, K, _stream(X.device)),
+               "swiglu_quantize_mx4")
+    return Q, S
+
+
+def swiglu_dequantize_mx4(Q: torch.Tensor, S: torch.Tensor,
+                          X: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The numbers [rows, K] (bfloat16, exact) that codes and scales stand for."""
+    lib = load_library()
+    rows, K = Q.shape[0], 2 * Q.shape[1]
+    _mx4(Q, S, ("Q", "S"), rows, K)
+    X = _out(X, "X", (rows, K), Q.device)
+    with _on_device(Q.device):
+        _check(lib.swiglu_dequantize_mx4(_ptr(Q), _ptr(S), _ptr(X), rows, K, _stream(Q.device)),
+               "swiglu_dequantize_mx4")
+    return X
+
+
+def swiglu_fused_gemm_mx4(A: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor,
+                          Y: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """swiglu_fused_gemm with the packed weight as 4-bit codes Wq [2N, K / 2] and
+    scales Ws [2N, K / 32]."""
+    lib = load_library()
+    M, K = A.shape
+    _dev_tensor(A, "A", (M, K))
+    N = Wq.shape[0] // 2
+    _mx4(Wq, Ws, ("Wq", "Ws"), 2 * N, K)
+    Y = _out(Y, "Y", (M, N), A.device)
+    with _on_device(A.device):
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_fused_gemm_mx4(_ptr(A), _ptr(Wq), _ptr(Ws), _ptr(Y), M, N, K, ws, wsb,
+                                         _stream(A.device)), "swiglu_fused_gemm_mx4")
+    return Y
+
+
+def swiglu_down_proj_mx4(H: torch.Tensor, W3q: torch.Tensor, W3s: torch.Tensor,
+                         Out: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """swiglu_down_proj with W3t as 4-bit codes W3q [D, N / 2] and scales W3s [D, N / 32]."""
+    lib = load_library()
+    M, N = H.shape
+    _dev_tensor(H, "H", (M, N))
+    D = W3q.shape[0]
+    _mx4(W3q, W3s, ("W3q", "W3s"), D, N)
+    Out = _out(Out, "Out", (M, D), H.device)
+    with _on_device(H.device):
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_down_proj_mx4(_ptr(H), _ptr(W3q), _ptr(W3s), _ptr(Out), M, N, D, ws, wsb,
+                                        _stream(H.device)), "swiglu_down_proj_mx4")
+    return Out
+
+
+def swiglu_gated_mlp_mx4(A: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, W3q: torch.Tensor,
+                         W3s: torch.Tensor, H: Optional[torch.Tensor] = None,
+                         Out: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None
+                         ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """swiglu_gated_mlp with both weights as 4-bit codes and scales; returns (Out, H)."""
+    lib = load_library()
+    M, K = A.shape
+    _dev_tensor(A, "A", (M, K))
+    N = Wq.shape[0] // 2
+    _mx4(Wq, Ws, ("Wq", "Ws"), 2 * N, K)
+    _mx4(W3q, W3s, ("W3q", "W3s"), K, N)
+    H, Out = _out(H, "H", (M, N), A.device), _out(Out, "Out", (M, K), A.device)
+    with _on_device(A.device):
+        ws, wsb = _ws(workspace)
+        _check(lib.swiglu_gated_mlp_mx4(_ptr(A), _ptr(Wq), _ptr(Ws), _ptr(W3q), _ptr(W3s), _ptr(H),
+                                        _ptr(Out), M, N, K, ws, wsb, _stream(A.device)),
+               "swiglu_gated_mlp_mx4")
     return Out, H
 
 

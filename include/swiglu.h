@@ -469,6 +469,49 @@ int swiglu_gated_mlp_lora(const uint16_t *X, const uint16_t *W_fused, const uint
                           void *stream);
 
 /*
+ * 4-bit weights with a scale for each group (serving: a few rows are bound by the
+ * bytes of the weights).  Row r of a matrix [rows][K] holds, for K a multiple of 32,
+ *     Q [rows][K / 2]    codes of E2M1 (1 sign, 2 exponent, 1 mantissa bit: 0, 0.5,
+ *                        1, 1.5, 2, 3, 4, 6), even k in a byte's low half
+ *     S [rows][K / 32]   the exponent, plus 127, of the power of two that 32
+ *                        consecutive k share; 255: the group is NaN
+ * and stands for code * 2^(S - 127) (the OCP MXFP4 format).  Those numbers are
+ * exact in bf16 (2^128 and above: infinity), so the calls below compute what the
+ * calls without "mx4" compute of them: exact products with the bf16 activations,
+ * fp32 sums, one rounding of each output.
+ *
+ * swiglu_quantize_mx4: codes nearest to X (ties to even) with S = max(0, e - 2) for
+ *     the biased exponent e of the group's largest magnitude, which then lies in
+ *     [4, 8) of the scale (above 6 it becomes 6); a group with an infinity or NaN
+ *     has S = 255 and codes 0.
+ * swiglu_dequantize_mx4: the numbers, as bf16.
+ * Both: 0 <= rows <= 2^23, 32 <= K <= 2^21, K % 32 == 0.  The packed W_fused or W3t
+ * (rows 2N or D) is quantized as it lies.
+ *
+ * swiglu_fused_gemm_mx4   Y = bf16(SiLU(A . W1) * (A . W2)), Wq, Ws of W_fused [2N][K]
+ * swiglu_down_proj_mx4    Out = bf16(H . W3), W3q, W3s of W3t [D][N]
+ * swiglu_gated_mlp_mx4    the two in turn, H between them as in swiglu_gated_mlp
+ * Preconditions: those of the calls without "mx4", and the contraction (K; N of the
+ * down projection) a multiple of 32; matrices and codes 16-byte aligned, scales at
+ * any address.  workspace: optional, as for swiglu_fused_gemm (size from
+ * swiglu_workspace_size(M, N, K, -1, ...)).
+ */
+int swiglu_quantize_mx4(const uint16_t *X, uint8_t *Q, uint8_t *S, int64_t rows, int64_t K,
+                        void *stream);
+int swiglu_dequantize_mx4(const uint8_t *Q, const uint8_t *S, uint16_t *X, int64_t rows,
+                          int64_t K, void *stream);
+int swiglu_fused_gemm_mx4(const uint16_t *A, const uint8_t *Wq, const uint8_t *Ws, uint16_t *Y,
+                          int64_t M, int64_t N, int64_t K, void *workspace,
+                          uint64_t workspace_bytes, void *stream);
+int swiglu_down_proj_mx4(const uint16_t *H, const uint8_t *W3q, const uint8_t *W3s,
+                         uint16_t *Out, int64_t M, int64_t N, int64_t D, void *workspace,
+                         uint64_t workspace_bytes, void *stream);
+int swiglu_gated_mlp_mx4(const uint16_t *A, const uint8_t *Wq, const uint8_t *Ws,
+                         const uint8_t *W3q, const uint8_t *W3s, uint16_t *H, uint16_t *Out,
+                         int64_t M, int64_t N, int64_t K, void *workspace,
+                         uint64_t workspace_bytes, void *stream);
+
+/*
  * What a call would launch, as text (host only; queries the current device's
  * compute-unit count): for swiglu_fused_gemm with `variant` (AUTO, S, I) or
  * for swiglu_unfused_ablation (-1), for the down projection of
