@@ -1181,7 +1181,7 @@ int swiglu_fused_gemm_mx4(const uint16_t *A, const uint8_t *Wq, const uint8_t *W
     const Operand ops[] = {
         {"A", A, M * K * 2, 16, false, false},
         {"Wq", Wq, N * K, 16, false, false},
-        {"Ws", Ws, N * K / 16, 1, false, false},
+        {"Ws", Ws, N * K / 16, 4, false, false},
         {"Y", Y, M * N * 2, 16, true, false},
         {"workspace", workspace, (int64_t)workspace_bytes, 256, true, true},
     };
@@ -1206,7 +1206,7 @@ int swiglu_down_proj_mx4(const uint16_t *H, const uint8_t *W3q, const uint8_t *W
     const Operand ops[] = {
         {"H", H, M * N * 2, 16, false, false},
         {"W3q", W3q, D * N / 2, 16, false, false},
-        {"W3s", W3s, D * N / 32, 1, false, false},
+        {"W3s", W3s, D * N / 32, 4, false, false},
         {"Out", Out, M * D * 2, 16, true, false},
         {"workspace", workspace, (int64_t)workspace_bytes, 256, true, true},
     };
@@ -1234,9 +1234,9 @@ int swiglu_gated_mlp_mx4(const uint16_t *A, const uint8_t *Wq, const uint8_t *Ws
     const Operand ops[] = {
         {"A", A, M * K * 2, 16, false, false},
         {"Wq", Wq, N * K, 16, false, false},
-        {"Ws", Ws, N * K / 16, 1, false, false},
+        {"Ws", Ws, N * K / 16, 4, false, false},
         {"W3q", W3q, K * N / 2, 16, false, false},
-        {"W3s", W3s, K * N / 32, 1, false, false},
+        {"W3s", W3s, K * N / 32, 4, false, false},
         {"H", H, M * N * 2, 16, true, false},
         {"Out", Out, M * K * 2, 16, true, false},
         {"workspace", workspace, (int64_t)workspace_bytes, 256, true, true},

@@ -573,6 +573,11 @@ __device__ __forceinline__ u32x4 asm_read_b128(uint32_t addr) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t asm_read_u8(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ds_read_u8 %0, %1" : "=v"(r) : "v"(addr));
+    return r;
+}
 template <int OFF>
 __device__ __forceinline__ u32x2 asm_read_tr(uint32_t addr) {
     u32x2 r;

@@ -166,16 +166,12 @@ template struct TilesLaunch<ShapeQuadMx4, StoreEpilogue, kTailSplit>;
 #elif SWIGLU_INSTANCE == 33
 template struct TilesLaunch<ShapeSmallMx4, PairMulEpilogue, kTailSplit>;
 template struct TilesLaunch<ShapeSmallMx4, StoreEpilogue, kTailSplit>;
-template struct TilesLaunch<ShapeThinMx4, PairMulEpilogue, kTailSplit>;
-template struct TilesLaunch<ShapeThinMx4, StoreEpilogue, kTailSplit>;
 template struct ReduceLaunch<ShapeWideMx4, PairMulEpilogue>;
 template struct ReduceLaunch<ShapeWideMx4, StoreEpilogue>;
 template struct ReduceLaunch<ShapeQuadMx4, PairMulEpilogue>;
 template struct ReduceLaunch<ShapeQuadMx4, StoreEpilogue>;
 template struct ReduceLaunch<ShapeSmallMx4, PairMulEpilogue>;
 template struct ReduceLaunch<ShapeSmallMx4, StoreEpilogue>;
-template struct ReduceLaunch<ShapeThinMx4, PairMulEpilogue>;
-template struct ReduceLaunch<ShapeThinMx4, StoreEpilogue>;
 #else
 #error "SWIGLU_INSTANCE is past the end of the instance list"
 #endif

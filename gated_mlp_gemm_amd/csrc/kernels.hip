@@ -757,8 +757,16 @@ template <class Epi>
 static hipError_t launch_mx4(const uint16_t *X, const KMajor &B, int M, int cols, int K,
                              const Epi &epi, const GemmWorkspace &ws, hipStream_t stream) {
     const KMajor A{X, M, 1, 0, 0, 0, nullptr};
-    if (M <= ShapeThinMx4::BM && cdiv(cols, ShapeThinMx4::BN) >= ws.cus)
-        return launch_split_gemm<ShapeThinMx4>(A, B, M, cols, K, epi, ws, stream);
+    if (M <= kMx4FewRows) {
+        constexpr bool kGated = std::is_same<Epi, PairMulEpilogue>::value;
+        uint16_t *y;
+        if constexpr (kGated) y = epi.Y;
+        else y = epi.C;
+        const hipError_t e =
+            launch_mx4_few(X, static_cast<const uint8_t *>(B.base), B.scales, y, M, cols, K, kGated,
+                           ws.cus, stream);
+        if (e != hipErrorNotSupported) return e;
+    }
     if (M <= 128) return launch_split_gemm<ShapeSmallMx4>(A, B, M, cols, K, epi, ws, stream);
     if (quad_split_faster<ShapeWideMx4, ShapeQuadMx4>(M, cols, K, ws))
         return launch_split_gemm<ShapeQuadMx4>(A, B, M, cols, K, epi, ws, stream);

@@ -77,6 +77,12 @@ hipError_t launch_quantize_mx4(const uint16_t *x, uint8_t *q, uint8_t *s, int64_
                                hipStream_t stream);
 hipError_t launch_dequantize_mx4(const uint8_t *q, const uint8_t *s, uint16_t *x, int64_t count,
                                  hipStream_t stream);
+// The product of at most kMx4FewRows rows with a weight [rows][K] (gated: the packed
+// one, Y [M][rows / 2]); hipErrorNotSupported where K is too long for it, nothing
+// launched.
+constexpr int kMx4FewRows = 64;
+hipError_t launch_mx4_few(const uint16_t *X, const uint8_t *Q, const uint8_t *S, uint16_t *Y, int M,
+                          int rows, int K, bool gated, int cus, hipStream_t stream);
 hipError_t launch_fused_mx4(const uint16_t *A, const uint8_t *Wq, const uint8_t *Ws, uint16_t *Y,
                             int M, int N, int K, const GemmWorkspace &ws, hipStream_t stream);
 hipError_t launch_down_proj_mx4(const uint16_t *H, const uint8_t *W3q, const uint8_t *W3s,

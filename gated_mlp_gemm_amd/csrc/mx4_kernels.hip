@@ -1,4 +1,5 @@
-// 4-bit weights: laying them out (quantize) and reading them back (dequantize).
+// 4-bit weights: laying them out (quantize), reading them back (dequantize), and the
+// products of few rows with them (mx4_few.hpp).
 //
 // A number is a code of E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) times
 // a power of two that 32 consecutive numbers of a row share, 2^(S - 127); S = 255
@@ -6,6 +7,9 @@
 #include "launch.hpp"
 
 #include "device.hpp"
+#include "mx4_few.hpp"
+
+#include <atomic>
 
 namespace swiglu {
 
@@ -92,6 +96,73 @@ hipError_t launch_dequantize_mx4(const uint8_t *q, const uint8_t *s, uint16_t *x
     hipLaunchKernelGGL(dequantize_mx4_kernel, dim3(chunk_grid(chunks)), dim3(256), 0, stream,
                        reinterpret_cast<const uint32_t *>(q), s, x, chunks);
     return hipGetLastError();
+}
+
+// One launch; hipErrorNotSupported where a compute unit's LDS does not hold the scales.
+template <bool GATED, int R, int NX, int D, int W>
+static hipError_t run_few(const uint16_t *X, const uint8_t *Q, const uint8_t *S, uint16_t *Y, int M,
+                          int rows, int K, hipStream_t stream) {
+    using P = Mx4Few<GATED, R, NX, D, W>;
+    constexpr int kLds = 160 * 1024;
+    if (P::lds_bytes(K) > kLds) return hipErrorNotSupported;
+    const auto kernel = mx4_few_kernel<GATED, R, NX, D, W>;
+    // a device takes more than 64 KiB of LDS a launch once it has been told so
+    static std::atomic<uint64_t> told[4];
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    std::atomic<uint64_t> &mine = told[(dev >> 6) & 3];
+    if (!(mine.load(std::memory_order_acquire) >> (dev & 63) & 1)) {
+        e = hipFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+        if (e != hipSuccess) return e;
+        mine.fetch_or(uint64_t{1} << (dev & 63), std::memory_order_release);
+    }
+    hipLaunchKernelGGL(kernel, dim3((rows + P::kRows - 1) / P::kRows), dim3(P::kThreads),
+                       P::lds_bytes(K), stream, X, Q, S, Y, M, rows, K);
+    return hipGetLastError();
+}
+
+// Rows of the weight a workgroup takes, by the 16-row tiles there are for a compute
+// unit: every workgroup reads all the activations, so more where that leaves the
+// device enough of them.  Measured, us, activations x weight (R = 1 / 2 / 4):
+//   M=16  896 x 4864 4.2 / 5.0 / 6.7, 8192 x 29568 47.1 / 36.5 / 49.6,
+//         27648 x 5120 29.0 / 24.7 / 20.9
+//   M=64  896 x 4864 8.8 / 9.8 / 14.8, 8192 x 29568 113 / 71 / 94,
+//         27648 x 5120 68 / 50 / 41
+// With at most 4 rows of activations there is little to share: R = 1 (37888 x 3584 14.0
+// against 14.5 us), with 8 waves for 4 where a compute unit has one workgroup (3584 x
+// 18944 8.3 against 9.5), R = 2 for long rows of many (59136 x 8192 47.5 against 51.3).
+template <bool GATED>
+static hipError_t launch_few(const uint16_t *X, const uint8_t *Q, const uint8_t *S, uint16_t *Y,
+                             int M, int rows, int K, int cus, hipStream_t stream) {
+    const int64_t tiles = (static_cast<int64_t>(rows) + 15) / 16;
+    const int r = tiles <= cus ? 1 : tiles < 4 * static_cast<int64_t>(cus) ? 2 : 4;
+#define SWIGLU_FEW(R, NX, D, W) run_few<GATED, R, NX, D, W>(X, Q, S, Y, M, rows, K, stream)
+    if (M <= 4) {
+        if (r == 1) return SWIGLU_FEW(1, 1, 4, 8);
+        if (r == 4 && K >= 8192) return SWIGLU_FEW(2, 1, 4, 4);
+        return SWIGLU_FEW(1, 1, 4, 4);
+    }
+    if (M <= 8) return r == 1 ? SWIGLU_FEW(1, 2, 2, 8) : SWIGLU_FEW(2, 2, 2, 4);
+    if (M <= 16)
+        return r == 1 ? SWIGLU_FEW(1, 4, 2, 4)
+                      : r == 2 ? SWIGLU_FEW(2, 4, 2, 4) : SWIGLU_FEW(4, 4, 2, 4);
+    if (M <= 32)
+        return r == 1 ? SWIGLU_FEW(1, 8, 2, 4)
+                      : r == 2 ? SWIGLU_FEW(2, 8, 2, 4) : SWIGLU_FEW(4, 8, 1, 4);
+    if (M <= 48)
+        return r == 1 ? SWIGLU_FEW(1, 12, 1, 8)
+                      : r == 2 ? SWIGLU_FEW(2, 12, 1, 8) : SWIGLU_FEW(4, 12, 1, 4);
+    return r == 1 ? SWIGLU_FEW(1, 16, 1, 8)
+                  : r == 2 ? SWIGLU_FEW(2, 16, 1, 4) : SWIGLU_FEW(4, 16, 1, 4);
+#undef SWIGLU_FEW
+}
+
+hipError_t launch_mx4_few(const uint16_t *X, const uint8_t *Q, const uint8_t *S, uint16_t *Y, int M,
+                          int rows, int K, bool gated, int cus, hipStream_t stream) {
+    return gated ? launch_few<true>(X, Q, S, Y, M, rows, K, cus, stream)
+                 : launch_few<false>(X, Q, S, Y, M, rows, K, cus, stream);
 }
 
 }  // namespace swiglu

@@ -1263,7 +1263,6 @@ using ShapeQuadDw = TileShape<128, 128, 64, 2, 2, 2, 2, 2, 16, true, true>;
 using ShapeWideMx4 = TileShape<256, 256, 64, 2, 2, 2, 2, 2, 16, false, false, true>;
 using ShapeQuadMx4 = TileShape<128, 128, 64, 2, 2, 2, 2, 2, 16, false, false, true>;
 using ShapeSmallMx4 = TileShape<128, 64, 64, 4, 1, 4, 2, 2, 16, false, false, true>;
-using ShapeThinMx4 = TileShape<64, 128, 64, 2, 2, 4, 2, 2, 16, false, false, true>;
 // Variant I on FP8 operands: the same three shapes with K steps of 128 FP8
 // values, so every tile row of a stage is 128 bytes and the LDS rings, load
 // counts and swizzles are those of the bf16 shapes (the 256x256 one with a
