@@ -1003,7 +1003,7 @@ int swiglu_gated_mlp_train(const uint16_t *A, const uint16_t *W_fused, const uin
     const hipError_t e =
         swiglu::launch_fused_train(A, W_fused, H, GU, (int)M, (int)N, (int)K, ws, s);
     if (e != hipSuccess) return launched(e, "gated MLP training forward: fused SwiGLU");
-    return launched(swiglu::launch_down_proj(H, W3t, Out, (int)M, (int)N, (int)K, ws, s),
+    return launched(swiglu::launch_down_train(H, W3t, Out, (int)M, (int)N, (int)K, ws, s),
                     "gated MLP training forward: down projection");
 }
 

@@ -130,31 +130,31 @@ template struct ReduceLaunch<ShapeSmallLora, StoreEpilogue>;
 #elif SWIGLU_INSTANCE == 23
 template struct TilesLaunch<ShapeWideDx, GateGradEpilogue, kTailSplit>;
 #elif SWIGLU_INSTANCE == 24
-template struct TilesLaunch<ShapeWideDx, StoreEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeWideDx, ActivationGradEpilogue, kTailSplit>;
 #elif SWIGLU_INSTANCE == 25
 template struct TilesLaunch<ShapeWideDw, WeightGradEpilogue, kTailSplit>;
 #elif SWIGLU_INSTANCE == 26
 template struct TilesLaunch<ShapeWide, PairMulKeep, kTailSplit>;
 #elif SWIGLU_INSTANCE == 27
 template struct TilesLaunch<ShapeQuadDx, GateGradEpilogue, kTailSplit>;
-template struct TilesLaunch<ShapeQuadDx, StoreEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeQuadDx, ActivationGradEpilogue, kTailSplit>;
 #elif SWIGLU_INSTANCE == 28
 template struct TilesLaunch<ShapeQuadDw, WeightGradEpilogue, kTailSplit>;
 template struct TilesLaunch<ShapeQuad, PairMulKeep, kTailSplit>;
 #elif SWIGLU_INSTANCE == 29
 template struct TilesLaunch<ShapeSmallDx, GateGradEpilogue, kTailSplit>;
-template struct TilesLaunch<ShapeSmallDx, StoreEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeSmallDx, ActivationGradEpilogue, kTailSplit>;
 template struct TilesLaunch<ShapeSmallLora, PairMulKeep, kTailSplit>;
 template struct ReduceLaunch<ShapeWideDx, GateGradEpilogue>;
-template struct ReduceLaunch<ShapeWideDx, StoreEpilogue>;
+template struct ReduceLaunch<ShapeWideDx, ActivationGradEpilogue>;
 template struct ReduceLaunch<ShapeWideDw, WeightGradEpilogue>;
 template struct ReduceLaunch<ShapeWide, PairMulKeep>;
 template struct ReduceLaunch<ShapeQuadDx, GateGradEpilogue>;
-template struct ReduceLaunch<ShapeQuadDx, StoreEpilogue>;
+template struct ReduceLaunch<ShapeQuadDx, ActivationGradEpilogue>;
 template struct ReduceLaunch<ShapeQuadDw, WeightGradEpilogue>;
 template struct ReduceLaunch<ShapeQuad, PairMulKeep>;
 template struct ReduceLaunch<ShapeSmallDx, GateGradEpilogue>;
-template struct ReduceLaunch<ShapeSmallDx, StoreEpilogue>;
+template struct ReduceLaunch<ShapeSmallDx, ActivationGradEpilogue>;
 template struct ReduceLaunch<ShapeSmallLora, PairMulKeep>;
 #elif SWIGLU_INSTANCE == 30
 template struct TilesLaunch<ShapeWideMx4, PairMulEpilogue, kTailSplit>;
@@ -172,6 +172,10 @@ template struct ReduceLaunch<ShapeQuadMx4, PairMulEpilogue>;
 template struct ReduceLaunch<ShapeQuadMx4, StoreEpilogue>;
 template struct ReduceLaunch<ShapeSmallMx4, PairMulEpilogue>;
 template struct ReduceLaunch<ShapeSmallMx4, StoreEpilogue>;
+#elif SWIGLU_INSTANCE == 34
+template struct TilesLaunch<ShapeWideDx, GateGradEpilogue, kTailQuarter>;
+#elif SWIGLU_INSTANCE == 35
+template struct TilesLaunch<ShapeWide, PairMulKeep, kTailQuarter>;
 #else
 #error "SWIGLU_INSTANCE is past the end of the instance list"
 #endif

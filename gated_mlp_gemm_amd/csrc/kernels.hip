@@ -235,7 +235,7 @@ constexpr double quarter_step_us() {
 //    ceil(nk / s) steps plus the reduction.
 // ws.tail forces one of them where it applies.  `us`, if given, receives the
 // predicted time of the whole schedule.
-template <class S, bool kQuarters = kQuarterable<S>>
+template <class S>
 static Schedule make_schedule(int M, int cols, int K, const GemmWorkspace &ws,
                               double *us = nullptr) {
     Schedule sch{};
@@ -258,7 +258,7 @@ static Schedule make_schedule(int M, int cols, int K, const GemmWorkspace &ws,
     if (L == 0) return sch;
     const bool forced = ws.tail != kTailAuto;
     double best = round;                            // tail tiles whole
-    if (kQuarters && (!forced || ws.tail == kTailQuarters)) {
+    if (kQuarterable<S> && (!forced || ws.tail == kTailQuarters)) {
         const double t = cdiv(4 * L, G) * (kRoundUs + sch.nk * quarter_step_us<S>());
         if (forced || t < best) {
             best = t;
@@ -668,30 +668,119 @@ hipError_t launch_lora_project(const uint16_t *X, const uint16_t *W, uint16_t *Y
 // ---------------------------------------------------------------------------
 // Training: the forward pass that keeps Gate and Up, and the gradients' products.
 // The kernels without tail work are those with a split tail, given none.
+//
+// Their schedules come from a cost model of their own (us; the products of seven
+// M x K x N from M=33 to 8192, each forced through every tile shape and tail): a
+// round of tiles costs kRound for its prologue and epilogue, what its epilogue moves
+// beyond bf16 results (`extra`, of a round of 256x256 tiles: every compute unit stores
+// at the same time), and a K step's time, which is shorter where half the device is
+// idle.  A split tail takes as many pieces as are worth their partials.  Against the
+// schedules of make_schedule(), whose steps of 256x256 tiles are dearer: M=8192 K=17920,
+// 1536 columns 414 -> 372 us, M=2048 K=1536, 8960 columns 67 -> 60.
 // ---------------------------------------------------------------------------
-template <class S, class Epi>
+template <class S>
+struct GradCost {
+    static constexpr bool kWide = S::BM == 256;
+    static constexpr bool kTwo = S::kOccupancy == 2;      // 128x128, two a compute unit
+    static constexpr double kRound = kWide ? 8.0 : 4.0;
+    static double step(int64_t tiles, int cus) {
+        if (kWide) return tiles > cus / 2 ? 1.2 : 1.05;
+        if (kTwo) return tiles > cus ? 0.85 : 0.6;
+        return 0.35;                                       // 128x64
+    }
+    // `tiles` at most one round of them, nk K steps each
+    static double round(int64_t tiles, int nk, double extra, int cus) {
+        const double share = static_cast<double>(tiles) * S::BM * S::BN / (256.0 * 256.0 * cus);
+        return kRound + extra * (share < 1.0 ? share : 1.0) + nk * step(tiles, cus);
+    }
+};
+template <class S, bool kQuarters>
+static Schedule make_grad_schedule(int M, int cols, int K, double extra, const GemmWorkspace &ws,
+                                   double *us = nullptr) {
+    using Cost = GradCost<S>;
+    Schedule sch{};
+    sch.tiles_m = cdiv(M, S::BM);
+    sch.tiles_n = cdiv(cols, S::BN);
+    sch.nk = cdiv(K, S::BK);
+    sch.group_m = sch.tiles_m <= 8 && sch.nk <= 32 ? 4 : 8;
+    const int64_t T = static_cast<int64_t>(sch.tiles_m) * sch.tiles_n;
+    sch.dp = static_cast<int>(T);
+    if (us) *us = 0.0;
+    const int G = ws.cus * S::kOccupancy;           // workgroup slots
+    if (G <= 0) return sch;
+    const int64_t L = T % G;
+    const double whole = static_cast<double>(T / G) * Cost::round(G, sch.nk, extra, ws.cus);
+    if (us) *us = whole + (L ? Cost::round(L, sch.nk, extra, ws.cus) : 0.0);
+    if (L == 0 || sch.nk == 0 || ws.tail == kTailWhole) return sch;
+    const bool forced = ws.tail != kTailAuto;
+    double best = Cost::round(L, sch.nk, extra, ws.cus);
+    if (kQuarters && (!forced || ws.tail == kTailQuarters)) {
+        // where not every workgroup has as many quarters, the whole rounds run out of
+        // step, and half of the extra costs nothing
+        const double drift = (4 * L) % G ? 0.5 * extra * static_cast<double>(T / G) : 0.0;
+        const double t = cdiv(4 * L, G) * (Cost::kRound + sch.nk * 0.6) - drift;
+        if (forced || t < best) {
+            best = t;
+            sch.dp = static_cast<int>(T - L);
+            sch.split_tiles = static_cast<int>(L);
+            sch.quartered = 1;
+        }
+    }
+    const bool has_ws = ws.base != nullptr && ws.bytes >= workspace_bytes_for(ws.cus);
+    if (has_ws && (!forced || ws.tail == kTailPieces)) {
+        const int most = static_cast<int>(min(G / L, static_cast<int64_t>(sch.nk)));
+        for (int s = 2; s <= most; ++s) {
+            const double partials = static_cast<double>(L) * s * S::BM * S::BN * 4.0 * 2.0;
+            const double t = Cost::round(L * s, cdiv(sch.nk, s), 0.0, ws.cus) + kReduceUs +
+                             partials / kPartialBytesPerUs;
+            if ((forced && s == most) || t < best) {
+                best = t;
+                sch.dp = static_cast<int>(T - L);
+                sch.split_tiles = static_cast<int>(L);
+                sch.quartered = 0;
+                sch.pieces = s;
+                sch.partials = reinterpret_cast<float *>(ws.base);
+            }
+        }
+    }
+    if (us) *us = whole + best;
+    return sch;
+}
+
+template <class S, class Epi, bool kQuarters = false>
 static hipError_t launch_split_gemm(const KMajor &A, KMajor B, int M, int cols, int K,
-                                    const Epi &epi, const GemmWorkspace &ws, hipStream_t stream) {
-    Schedule sch = make_schedule<S, false>(M, cols, K, ws);
+                                    const Epi &epi, const GemmWorkspace &ws, hipStream_t stream,
+                                    double extra = 0.0) {
+    Schedule sch = make_grad_schedule<S, kQuarters>(M, cols, K, extra, ws);
     sch.grid = launch_grid<S>(sch, ws.cus);
     B.pairs = Epi::template paired<S>() ? 1 : 0;   // de-interleaved weight panels
     if (sch.grid <= 0) return hipSuccess;
+    if constexpr (kQuarters)
+        if (sch.quartered)
+            return TilesLaunch<S, Epi, kTailQuarter>::run(sch.grid, A, B, M, K, epi, sch, stream);
     const hipError_t e =
         TilesLaunch<S, Epi, kTailSplit>::run(sch.grid, A, B, M, K, epi, sch, stream);
     if (e != hipSuccess || sch.pieces == 0) return e;
     constexpr int kWavesPerTile = S::kWaves * S::TM * S::TN / Epi::template unit_blocks<S>();
     return ReduceLaunch<S, Epi>::run(sch.split_tiles * kWavesPerTile, epi, sch, stream);
 }
-template <class Wide, class Quad>
-static bool quad_split_faster(int M, int cols, int K, const GemmWorkspace &ws) {
-    if (ws.tile == 256) return false;
-    if (ws.tile == 128) return true;
-    if (ws.cus <= 0) return false;
-    double wide = 0.0, quad = 0.0;
-    make_schedule<Wide, false>(M, cols, K, ws, &wide);
-    make_schedule<Quad, false>(M, cols, K, ws, &quad);
-    return quad < wide;
+// The 256x256 tiles or the 128x128 ones, whichever the model predicts faster.
+template <class Wide, class Quad, class Epi, bool kQuarters = false>
+static hipError_t launch_wide_or_quad(const KMajor &A, const KMajor &B, int M, int cols, int K,
+                                      const Epi &epi, double extra, const GemmWorkspace &ws,
+                                      hipStream_t stream) {
+    double wide = 0.0, quad = 1.0;
+    if (ws.tile == 0) {
+        make_grad_schedule<Wide, kQuarters>(M, cols, K, extra, ws, &wide);
+        make_grad_schedule<Quad, false>(M, cols, K, extra, ws, &quad);
+    }
+    if (ws.tile == 128 || (ws.tile == 0 && quad < wide))
+        return launch_split_gemm<Quad>(A, B, M, cols, K, epi, ws, stream, extra);
+    return launch_split_gemm<Wide, Epi, kQuarters>(A, B, M, cols, K, epi, ws, stream, extra);
 }
+// What a round's epilogues cost beyond bf16 results: 4 bytes more a pair of columns
+// (Gate and Up kept); 8 more an element (Gate and Up read, their gradients written).
+constexpr double kKeepUs = 6.0, kGateGradUs = 20.0;
 
 hipError_t launch_fused_train(const uint16_t *A, const uint16_t *Wf, uint16_t *H, uint16_t *GU,
                               int M, int N, int K, const GemmWorkspace &ws, hipStream_t stream) {
@@ -706,25 +795,38 @@ hipError_t launch_fused_train(const uint16_t *A, const uint16_t *Wf, uint16_t *H
     epi.GU = GU;
     if (M <= 128 && !small_m_quad_tiles(M, 2 * N, ws))
         return launch_split_gemm<ShapeSmallLora>(Ak, B, M, 2 * N, K, epi, ws, stream);
-    if (M <= 128 || quad_split_faster<ShapeWide, ShapeQuad>(M, 2 * N, K, ws))
-        return launch_split_gemm<ShapeQuad>(Ak, B, M, 2 * N, K, epi, ws, stream);
-    return launch_split_gemm<ShapeWide>(Ak, B, M, 2 * N, K, epi, ws, stream);
+    if (M <= 128) return launch_split_gemm<ShapeQuad>(Ak, B, M, 2 * N, K, epi, ws, stream);
+    return launch_wide_or_quad<ShapeWide, ShapeQuad, PairMulKeep, true>(Ak, B, M, 2 * N, K, epi,
+                                                                        kKeepUs, ws, stream);
+}
+hipError_t launch_down_train(const uint16_t *H, const uint16_t *W3t, uint16_t *Out, int M, int N,
+                             int D, const GemmWorkspace &ws, hipStream_t stream) {
+    const KMajor A{H, M, 1, 0, 0, 0, nullptr};
+    const KMajor B{W3t, D, 1, 0, 0, 0, nullptr};
+    const StoreEpilogue epi{Out, M, D};
+    if (M <= 128) return launch_split_gemm<ShapeSmall>(A, B, M, D, N, epi, ws, stream);
+    return launch_wide_or_quad<ShapeWide, ShapeQuad>(A, B, M, D, N, epi, 0.0, ws, stream);
 }
 
 // D [M][cols] = dY [M][C] . W [C][cols], with a weight contracted by its rows.
-template <class Epi>
+template <class Epi, bool kQuarters = false>
 static hipError_t launch_dx(const uint16_t *dY, const uint16_t *W, int M, int cols, int C,
-                            const Epi &epi, const GemmWorkspace &ws, hipStream_t stream) {
-    const KMajor A{dY, M, 1, 0, 0, 0};
-    const KMajor B{W, cols, 1, 0, 0, cols};
+                            const Epi &epi, double extra, const GemmWorkspace &ws,
+                            hipStream_t stream) {
+    const KMajor A{dY, M, 1, 0, 0, 0, nullptr};
+    const KMajor B{W, cols, 1, 0, 0, cols, nullptr};
     if (M <= 128) return launch_split_gemm<ShapeSmallDx>(A, B, M, cols, C, epi, ws, stream);
-    if (quad_split_faster<ShapeWideDx, ShapeQuadDx>(M, cols, C, ws))
-        return launch_split_gemm<ShapeQuadDx>(A, B, M, cols, C, epi, ws, stream);
-    return launch_split_gemm<ShapeWideDx>(A, B, M, cols, C, epi, ws, stream);
+    return launch_wide_or_quad<ShapeWideDx, ShapeQuadDx, Epi, kQuarters>(A, B, M, cols, C, epi,
+                                                                         extra, ws, stream);
 }
 hipError_t launch_grad_input(const uint16_t *dY, const uint16_t *W, uint16_t *dX, int M, int cols,
                              int C, const GemmWorkspace &ws, hipStream_t stream) {
-    return launch_dx(dY, W, M, cols, C, StoreEpilogue{dX, M, cols}, ws, stream);
+    ActivationGradEpilogue epi;
+    epi.C = dX;
+    epi.add = nullptr;
+    epi.M = M;
+    epi.N = cols;
+    return launch_dx(dY, W, M, cols, C, epi, 0.0, ws, stream);
 }
 hipError_t launch_grad_gate_up(const uint16_t *dOut, const uint16_t *W3t, const uint16_t *GU,
                                uint16_t *dGU, int M, int N, int D, const GemmWorkspace &ws,
@@ -734,20 +836,20 @@ hipError_t launch_grad_gate_up(const uint16_t *dOut, const uint16_t *W3t, const 
     epi.dGU = dGU;
     epi.M = M;
     epi.N = N;
-    return launch_dx(dOut, W3t, M, N, D, epi, ws, stream);
+    return launch_dx<GateGradEpilogue, true>(dOut, W3t, M, N, D, epi, kGateGradUs, ws, stream);
 }
 
 hipError_t launch_weight_grad(const uint16_t *dY, const uint16_t *X, void *dW, const void *add,
                               bool f32, int M, int rows, int cols, const GemmWorkspace &ws_,
                               hipStream_t stream) {
-    const KMajor A{dY, rows, 1, 0, 0, rows};
-    const KMajor B{X, cols, 1, 0, 0, cols};
+    const KMajor A{dY, rows, 1, 0, 0, rows, nullptr};
+    const KMajor B{X, cols, 1, 0, 0, cols, nullptr};
     const WeightGradEpilogue epi{dW, add, rows, cols, f32 ? 1 : 0};
     GemmWorkspace ws = ws_;
     if (M == 0) ws.tail = kTailWhole;   // no K step to split: the tiles store zeros (+ add)
-    if (quad_split_faster<ShapeWideDw, ShapeQuadDw>(rows, cols, M, ws))
-        return launch_split_gemm<ShapeQuadDw>(A, B, rows, cols, M, epi, ws, stream);
-    return launch_split_gemm<ShapeWideDw>(A, B, rows, cols, M, epi, ws, stream);
+    // 2 bytes more an element in fp32, and what is added is read
+    const double extra = ((f32 ? 2 : 0) + (add ? (f32 ? 4 : 2) : 0)) * (kGateGradUs / 8.0);
+    return launch_wide_or_quad<ShapeWideDw, ShapeQuadDw>(A, B, rows, cols, M, epi, extra, ws, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -768,9 +870,7 @@ static hipError_t launch_mx4(const uint16_t *X, const KMajor &B, int M, int cols
         if (e != hipErrorNotSupported) return e;
     }
     if (M <= 128) return launch_split_gemm<ShapeSmallMx4>(A, B, M, cols, K, epi, ws, stream);
-    if (quad_split_faster<ShapeWideMx4, ShapeQuadMx4>(M, cols, K, ws))
-        return launch_split_gemm<ShapeQuadMx4>(A, B, M, cols, K, epi, ws, stream);
-    return launch_split_gemm<ShapeWideMx4>(A, B, M, cols, K, epi, ws, stream);
+    return launch_wide_or_quad<ShapeWideMx4, ShapeQuadMx4>(A, B, M, cols, K, epi, 0.0, ws, stream);
 }
 hipError_t launch_fused_mx4(const uint16_t *A, const uint8_t *Wq, const uint8_t *Ws, uint16_t *Y,
                             int M, int N, int K, const GemmWorkspace &ws, hipStream_t stream) {

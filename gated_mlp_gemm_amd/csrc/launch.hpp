@@ -58,6 +58,9 @@ hipError_t launch_down_proj(const uint16_t *H, const uint16_t *W3t, uint16_t *Ou
 // Training.  H and GU [M][2N] (Gate and Up, bf16, interleaved) of one pass over A.
 hipError_t launch_fused_train(const uint16_t *A, const uint16_t *Wf, uint16_t *H, uint16_t *GU,
                               int M, int N, int K, const GemmWorkspace &ws, hipStream_t stream);
+// launch_down_proj with the training calls' schedules.
+hipError_t launch_down_train(const uint16_t *H, const uint16_t *W3t, uint16_t *Out, int M, int N,
+                             int D, const GemmWorkspace &ws, hipStream_t stream);
 // dX [M][cols] = bf16(dY [M][C] . W), W [C][cols] as the forward pass holds it.
 hipError_t launch_grad_input(const uint16_t *dY, const uint16_t *W, uint16_t *dX, int M, int cols,
                              int C, const GemmWorkspace &ws, hipStream_t stream);

@@ -276,59 +276,93 @@ struct StoreEpilogue {
     __device__ __forceinline__ static int unit_block(int u, int) { return u; }
 };
 
-// Byte offset of lane `lane`'s first element of block (tm, tn) of a wave in a
-// row-major matrix of 4-byte elements, ld a row, as lane_offsets' (the block's row
-// 32 tm aside, which is uniform).
-template <class S>
-__device__ __forceinline__ void lane_offsets4(uint32_t (&voff)[2], int tn, int cols_valid, int n0,
-                                              int ld, int tid) {
-    const int lane = tid & 63, wave = tid >> 6;
-    lane_offsets(voff, static_cast<uint32_t>((wave / S::WN) * S::kWaveM + S::row_l(lane)),
-                 (wave % S::WN) * S::kWaveN + tn * 32 + S::col_l(lane), cols_valid, n0, ld);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) voff[h] = voff[h] == kOutOfRange ? kOutOfRange : 2u * voff[h];
+// ---------------------------------------------------------------------------
+// Epilogues of the training calls.  In the 16x16 accumulator layout a lane's values
+// are 16 columns apart, so a store of each would move 2 or 4 bytes a lane and pieces
+// of 32 or 64 bytes of a row.  Lanes 2j and 2j+1 exchange one value of each two first
+// (Pairs): then a lane holds two adjacent columns, the even lane of the block's left
+// 16 columns, the odd lane of its right 16, and a wave's access covers 4 rows of 32
+// columns whole.
+// ---------------------------------------------------------------------------
+// (element p of a lane's 8 pairs: block row 16 (p / 4) + 4 (lane / 16) + p % 4)
+struct Pairs {
+    template <class S>
+    __device__ __forceinline__ static uint32_t column(int lane) {
+        static_assert(S::MI == 16, "16x16 MFMAs");
+        return static_cast<uint32_t>((lane & 14) + ((lane & 1) ? 16 : 0));
+    }
+    static constexpr int row(int p) { return 16 * (p >> 2) + (p & 3); }
+    // The lane's two adjacent values of left (its column of the left 16) and right.
+    __device__ __forceinline__ static void exchange(float left, float right, float &lo, float &hi) {
+        const float got = swap_adjacent_lanes(by_lane_parity(right, left));
+        lo = by_lane_parity(left, got);
+        hi = by_lane_parity(got, right);
+    }
+    // Accumulator registers of pair p: quads 2 (p / 4) (left) and the next (right).
+    static constexpr int left(int p) { return 8 * (p >> 2) + (p & 3); }
+    static constexpr int right(int p) { return 8 * (p >> 2) + 4 + (p & 3); }
+    template <bool kFromAcc, class Acc>
+    __device__ __forceinline__ static void of(const Acc &a, int p, float &lo, float &hi) {
+        exchange(acc_value<kFromAcc>(a.get(left(p))), acc_value<kFromAcc>(a.get(right(p))), lo, hi);
+    }
+    // Byte offset of the lane's first pair in a row-major matrix of `size`-byte elements,
+    // ld a row: wave tile rows from the matrix' row of `rsrc`, columns c0 (of the matrix)
+    // on, of which `valid` are in it.
+    template <class S>
+    __device__ __forceinline__ static uint32_t offset(int wave_row, int wave_col, int col_base,
+                                                      int valid, uint32_t ld, uint32_t size,
+                                                      int lane) {
+        const uint32_t c = static_cast<uint32_t>(wave_col) + column<S>(lane);
+        const uint32_t r = static_cast<uint32_t>(wave_row + 4 * (lane >> 4));
+        return static_cast<int>(c) < valid ? (r * ld + static_cast<uint32_t>(col_base) + c) * size
+                                           : kOutOfRange;
+    }
+};
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *base, int m0, int rows,
+                                                            uint32_t row_bytes) {
+    return make_rsrc(static_cast<const char *>(base) + static_cast<int64_t>(m0) * row_bytes,
+                     static_cast<uint32_t>(rows) * row_bytes);
 }
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc4(const void *base, int m0, int rows, int ld) {
-    return make_rsrc(static_cast<const char *>(base) + static_cast<int64_t>(m0) * ld * 4,
-                     static_cast<uint32_t>(rows) * static_cast<uint32_t>(ld) * 4u);
+__device__ __forceinline__ u32x2 load8(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff) {
+    return __builtin_amdgcn_raw_buffer_load_b64(r, static_cast<int>(off), static_cast<int>(soff), 0);
+}
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff,
+                                       uint32_t a, uint32_t b) {
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{a, b}, r, static_cast<int>(off),
+                                          static_cast<int>(soff), 0);
+}
+__device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff,
+                                       uint32_t a) {
+    __builtin_amdgcn_raw_buffer_store_b32(a, r, static_cast<int>(off), static_cast<int>(soff), 0);
 }
 
 // The training forward pass: variant I's epilogue, which also stores Gate and Up
-// as bf16, interleaved as W_fused's columns: GU [M][2N], one 4-byte store a pair
-// (Y is computed from the fp32 sums, bit for bit as without).  Paired layouts only.
+// as bf16, interleaved as W_fused's columns: GU [M][2N].  Paired layouts only.
 struct PairMulKeep : PairMulEpilogue {
     uint16_t *GU;
 
     template <class S, bool kFromAcc = true>
     __device__ __forceinline__ void unit(const typename S::Acc &g, const typename S::Acc &up, int u,
                                          int m0, int n0, int tid) const {
-        static_assert(S::TN % 2 == 0 && S::MI == 16, "paired layout");
+        static_assert(S::TN % 2 == 0, "paired layout");
         const int lane = tid & 63, wave = tid >> 6;
         const int tm = u / (S::TN / 2), tp = u % (S::TN / 2);
-        const int y0 = n0 / 2, ycols_valid = min(S::BN / 2, N - y0);
-        const int rows_valid = min(S::BM, M - m0);
-        const __amdgpu_buffer_rsrc_t ry = out_rsrc(Y, m0, rows_valid, ldy);
-        const __amdgpu_buffer_rsrc_t rg = rsrc4(GU, m0, rows_valid, N);
-        const uint32_t lrow = static_cast<uint32_t>((wave / S::WN) * S::kWaveM + S::row_l(lane));
-        uint32_t voff[2], goff[2];
-        lane_offsets(voff, lrow, (wave % S::WN) * (S::kWaveN / 2) + tp * 32 + S::col_l(lane),
-                     ycols_valid, y0, N);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) goff[h] = voff[h] == kOutOfRange ? kOutOfRange : 2u * voff[h];
+        const int y0 = n0 / 2, rows = min(S::BM, M - m0);
         const uint32_t pitch = static_cast<uint32_t>(N) * 2u;   // of Y (ldy = N here); GU: twice
+        const __amdgpu_buffer_rsrc_t ry = rows_rsrc(Y, m0, rows, pitch);
+        const __amdgpu_buffer_rsrc_t rg = rows_rsrc(GU, m0, rows, 2u * pitch);
+        const uint32_t off =
+            Pairs::offset<S>((wave / S::WN) * S::kWaveM, (wave % S::WN) * (S::kWaveN / 2) + tp * 32,
+                             y0, min(S::BN / 2, N - y0), static_cast<uint32_t>(N), 2u, lane);
+        const uint32_t goff = off == kOutOfRange ? kOutOfRange : 2u * off;
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            const float g0 = acc_value<kFromAcc>(g.get(i)), g1 = acc_value<kFromAcc>(g.get(i + 1));
-            const float u0 = acc_value<kFromAcc>(up.get(i)), u1 = acc_value<kFromAcc>(up.get(i + 1));
-            const uint32_t v = pack_bf16x2(silu(g0) * u0, silu(g1) * u1);
-            const uint32_t row = static_cast<uint32_t>(tm * 32 + S::row_r(i)) * pitch;
-            const int h = S::col_r(i) / 16;
-            store_b16(ry, voff[h], row, static_cast<uint16_t>(v));
-            store_b16_hi(ry, voff[h], row + pitch, v);
-            __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(g0, u0), rg, static_cast<int>(goff[h]),
-                                                  static_cast<int>(2u * row), 0);
-            __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(g1, u1), rg, static_cast<int>(goff[h]),
-                                                  static_cast<int>(2u * row + 2u * pitch), 0);
+        for (int p = 0; p < 8; ++p) {
+            float g0, g1, u0, u1;
+            Pairs::of<kFromAcc>(g, p, g0, g1);
+            Pairs::of<kFromAcc>(up, p, u0, u1);
+            const uint32_t row = static_cast<uint32_t>(tm * 32 + Pairs::row(p)) * pitch;
+            store4(ry, off, row, pack_bf16x2(silu(g0) * u0, silu(g1) * u1));
+            store8(rg, goff, 2u * row, pack_bf16x2(g0, u0), pack_bf16x2(g1, u1));
         }
     }
     template <class S>
@@ -344,13 +378,13 @@ struct PairMulKeep : PairMulEpilogue {
     }
 };
 
-// Epilogues that read a matrix of the output's shape beside the accumulators:
-// D::load fetches a block's 16 values a lane and D::finish uses them.  A block's
-// loads go out kAhead blocks before its use, so that a tile waits for memory about
-// once and not once a block.
+// Epilogues of one block at a time, which may read a matrix of the output's shape
+// beside the accumulators: D::load fetches a block's values and D::finish uses them.
+// A block's loads go out kAhead blocks before its use, so that a tile waits for
+// memory about once and not once a block.
 template <class D>
-struct ReadingEpilogue {
-    static constexpr int kAhead = 3;
+struct BlockEpilogue {
+    static constexpr int kAhead = 4;
     template <class S>
     static constexpr bool paired() { return false; }
     template <class S>
@@ -362,7 +396,7 @@ struct ReadingEpilogue {
     __device__ __forceinline__ void unit(const typename S::Acc &a0, const typename S::Acc &, int u,
                                          int m0, int n0, int tid) const {
         const D &d = static_cast<const D &>(*this);
-        uint32_t x[16];
+        u32x2 x[8];
         d.template load<S>(x, u, m0, n0, tid);
         d.template finish<S, kFromAcc>(a0, x, u, m0, n0, tid);
     }
@@ -371,7 +405,7 @@ struct ReadingEpilogue {
                                           int tid) const {
         const D &d = static_cast<const D &>(*this);
         constexpr int kUnits = S::TM * S::TN;
-        uint32_t x[kUnits][16];   // (kAhead + 1 of them live)
+        u32x2 x[kUnits][8];   // (kAhead + 1 of them live)
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < kUnits + kAhead; ++u) {
@@ -383,6 +417,19 @@ struct ReadingEpilogue {
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+    }
+    // The lane's offset of block u's first pair.
+    template <class S>
+    __device__ __forceinline__ static uint32_t block_offset(int u, int n0, int cols, uint32_t size,
+                                                            int tid) {
+        const int lane = tid & 63, wave = tid >> 6;
+        return Pairs::offset<S>((wave / S::WN) * S::kWaveM,
+                                (wave % S::WN) * S::kWaveN + (u % S::TN) * 32, n0,
+                                min(S::BN, cols - n0), static_cast<uint32_t>(cols), size, lane);
+    }
+    template <class S>
+    __device__ __forceinline__ static uint32_t block_row(int u, int p, uint32_t pitch) {
+        return static_cast<uint32_t>((u / S::TN) * 32 + Pairs::row(p)) * pitch;
     }
 };
 
@@ -397,44 +444,90 @@ __device__ __forceinline__ uint32_t gate_grad(float d, uint32_t gu) {
     const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f));
     return pack_bf16x2(d * u * (s * (1.0f + g * (1.0f - s))), d * (g * s));
 }
-struct GateGradEpilogue : ReadingEpilogue<GateGradEpilogue> {
+struct GateGradEpilogue : BlockEpilogue<GateGradEpilogue> {
     const uint16_t *GU;
     uint16_t *dGU;
     int M, N;
 
     template <class S>
-    __device__ __forceinline__ void load(uint32_t (&x)[16], int u, int m0, int n0, int tid) const {
-        const int tm = u / S::TN, tn = u % S::TN;
-        const __amdgpu_buffer_rsrc_t r = rsrc4(GU, m0, min(S::BM, M - m0), N);
-        uint32_t voff[2];
-        lane_offsets4<S>(voff, tn, min(S::BN, N - n0), n0, N, tid);
+    __device__ __forceinline__ void load(u32x2 (&x)[8], int u, int m0, int n0, int tid) const {
+        const uint32_t pitch = static_cast<uint32_t>(N) * 4u;
+        const __amdgpu_buffer_rsrc_t r = rows_rsrc(GU, m0, min(S::BM, M - m0), pitch);
+        const uint32_t off = block_offset<S>(u, n0, N, 4u, tid);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            x[i] = __builtin_amdgcn_raw_buffer_load_b32(
-                r, static_cast<int>(voff[S::col_r(i) / 16]),
-                static_cast<int>(static_cast<uint32_t>(tm * 32 + S::row_r(i)) *
-                                 static_cast<uint32_t>(N) * 4u), 0);
+        for (int p = 0; p < 8; ++p) x[p] = load8(r, off, block_row<S>(u, p, pitch));
     }
     template <class S, bool kFromAcc>
-    __device__ __forceinline__ void finish(const typename S::Acc &a, const uint32_t (&x)[16], int u,
+    __device__ __forceinline__ void finish(const typename S::Acc &a, const u32x2 (&x)[8], int u,
                                            int m0, int n0, int tid) const {
-        const int tm = u / S::TN, tn = u % S::TN;
-        const __amdgpu_buffer_rsrc_t r = rsrc4(dGU, m0, min(S::BM, M - m0), N);
-        uint32_t voff[2];
-        lane_offsets4<S>(voff, tn, min(S::BN, N - n0), n0, N, tid);
+        const uint32_t pitch = static_cast<uint32_t>(N) * 4u;
+        const __amdgpu_buffer_rsrc_t r = rows_rsrc(dGU, m0, min(S::BM, M - m0), pitch);
+        const uint32_t off = block_offset<S>(u, n0, N, 4u, tid);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            __builtin_amdgcn_raw_buffer_store_b32(
-                gate_grad(acc_value<kFromAcc>(a.get(i)), x[i]), r,
-                static_cast<int>(voff[S::col_r(i) / 16]),
-                static_cast<int>(static_cast<uint32_t>(tm * 32 + S::row_r(i)) *
-                                 static_cast<uint32_t>(N) * 4u), 0);
+        for (int p = 0; p < 8; ++p) {
+            float d0, d1;
+            Pairs::of<kFromAcc>(a, p, d0, d1);
+            const uint32_t gu0 = x[p][0], gu1 = x[p][1];
+            store8(r, off, block_row<S>(u, p, pitch), gate_grad(d0, gu0), gate_grad(d1, gu1));
+        }
     }
 };
 
-// A weight's gradient C [M][N] = D (+ add), rounded once, bf16 or fp32 (f32);
-// add: NULL, or a matrix of C's type and shape, C itself among them (each element
-// is read by the lane that stores it).
+// C [M][N] = D (+ add), rounded once, bf16 or fp32; add: a matrix of C's type and
+// shape, C itself among them (each element is read by the lane that stores it).
+template <bool kF32, bool kAdd>
+struct SumEpilogue : BlockEpilogue<SumEpilogue<kF32, kAdd>> {
+    using Base = BlockEpilogue<SumEpilogue<kF32, kAdd>>;
+    void *C;
+    const void *add;
+    int M, N;
+    static constexpr uint32_t kSize = kF32 ? 4 : 2;
+
+    template <class S>
+    __device__ __forceinline__ void load(u32x2 (&x)[8], int u, int m0, int n0, int tid) const {
+        if constexpr (kAdd) {
+            const uint32_t pitch = static_cast<uint32_t>(N) * kSize;
+            const __amdgpu_buffer_rsrc_t r = rows_rsrc(add, m0, min(S::BM, M - m0), pitch);
+            const uint32_t off = Base::template block_offset<S>(u, n0, N, kSize, tid);
+#pragma unroll
+            for (int p = 0; p < 8; ++p) {
+                const uint32_t row = Base::template block_row<S>(u, p, pitch);
+                if constexpr (kF32)
+                    x[p] = load8(r, off, row);
+                else
+                    x[p][0] = __builtin_amdgcn_raw_buffer_load_b32(r, static_cast<int>(off),
+                                                                   static_cast<int>(row), 0);
+            }
+        }
+    }
+    template <class S, bool kFromAcc>
+    __device__ __forceinline__ void finish(const typename S::Acc &a, const u32x2 (&x)[8], int u,
+                                           int m0, int n0, int tid) const {
+        const uint32_t pitch = static_cast<uint32_t>(N) * kSize;
+        const __amdgpu_buffer_rsrc_t r = rows_rsrc(C, m0, min(S::BM, M - m0), pitch);
+        const uint32_t off = Base::template block_offset<S>(u, n0, N, kSize, tid);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            float c0, c1;
+            Pairs::of<kFromAcc>(a, p, c0, c1);
+            if constexpr (kAdd) {
+                const uint32_t x0 = x[p][0], x1 = x[p][1];
+                c0 += __builtin_bit_cast(float, kF32 ? x0 : x0 << 16);
+                c1 += __builtin_bit_cast(float, kF32 ? x1 : x0 & 0xFFFF0000u);
+            }
+            const uint32_t row = Base::template block_row<S>(u, p, pitch);
+            if constexpr (kF32)
+                store8(r, off, row, __builtin_bit_cast(uint32_t, c0), __builtin_bit_cast(uint32_t, c1));
+            else
+                store4(r, off, row, pack_bf16x2(c0, c1));
+        }
+    }
+};
+
+// A gradient by an activation: bf16.
+struct ActivationGradEpilogue : SumEpilogue<false, false> {};
+
+// A weight's gradient: bf16 or fp32 (f32), with add or without (NULL).
 struct WeightGradEpilogue {
     void *C;
     const void *add;
@@ -442,78 +535,8 @@ struct WeightGradEpilogue {
     int f32;
 
     template <bool kF32, bool kAdd>
-    struct Mode : ReadingEpilogue<Mode<kF32, kAdd>> {
-        void *C;
-        const void *add;
-        int M, N;
-        static constexpr uint32_t kSize = kF32 ? 4 : 2;
-
-        template <class S>
-        __device__ __forceinline__ void offsets(uint32_t (&voff)[2], int tn, int n0, int tid) const {
-            if constexpr (kF32) {
-                lane_offsets4<S>(voff, tn, min(S::BN, N - n0), n0, N, tid);
-            } else {
-                const int lane = tid & 63, wave = tid >> 6;
-                lane_offsets(voff, static_cast<uint32_t>((wave / S::WN) * S::kWaveM + S::row_l(lane)),
-                             (wave % S::WN) * S::kWaveN + tn * 32 + S::col_l(lane),
-                             min(S::BN, N - n0), n0, N);
-            }
-        }
-        __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, int m0, int rows) const {
-            return make_rsrc(static_cast<const char *>(p) + static_cast<int64_t>(m0) * N * kSize,
-                             static_cast<uint32_t>(rows) * static_cast<uint32_t>(N) * kSize);
-        }
-        template <class S>
-        __device__ __forceinline__ void load(uint32_t (&x)[16], int u, int m0, int n0, int tid) const {
-            if constexpr (kAdd) {
-                const int tm = u / S::TN, tn = u % S::TN;
-                const __amdgpu_buffer_rsrc_t r = rsrc(add, m0, min(S::BM, M - m0));
-                uint32_t voff[2];
-                offsets<S>(voff, tn, n0, tid);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int v = static_cast<int>(voff[S::col_r(i) / 16]);
-                    const int s = static_cast<int>(static_cast<uint32_t>(tm * 32 + S::row_r(i)) *
-                                                   static_cast<uint32_t>(N) * kSize);
-                    if constexpr (kF32) x[i] = __builtin_amdgcn_raw_buffer_load_b32(r, v, s, 0);
-                    else x[i] = __builtin_amdgcn_raw_buffer_load_b16(r, v, s, 0);
-                }
-            }
-        }
-        template <class S, bool kFromAcc>
-        __device__ __forceinline__ void finish(const typename S::Acc &a, const uint32_t (&x)[16],
-                                               int u, int m0, int n0, int tid) const {
-            const int tm = u / S::TN, tn = u % S::TN;
-            const __amdgpu_buffer_rsrc_t r = rsrc(C, m0, min(S::BM, M - m0));
-            uint32_t voff[2];
-            offsets<S>(voff, tn, n0, tid);
-            const uint32_t pitch = static_cast<uint32_t>(N) * kSize;
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                float c0 = acc_value<kFromAcc>(a.get(i)), c1 = acc_value<kFromAcc>(a.get(i + 1));
-                if constexpr (kAdd) {
-                    c0 += __builtin_bit_cast(float, kF32 ? x[i] : x[i] << 16);
-                    c1 += __builtin_bit_cast(float, kF32 ? x[i + 1] : x[i + 1] << 16);
-                }
-                const uint32_t v = voff[S::col_r(i) / 16];
-                const uint32_t row = static_cast<uint32_t>(tm * 32 + S::row_r(i)) * pitch;
-                if constexpr (kF32) {
-                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, c0), r,
-                                                          static_cast<int>(v), static_cast<int>(row), 0);
-                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, c1), r,
-                                                          static_cast<int>(v),
-                                                          static_cast<int>(row + pitch), 0);
-                } else {
-                    const uint32_t y = pack_bf16x2(c0, c1);
-                    store_b16(r, v, row, static_cast<uint16_t>(y));
-                    store_b16_hi(r, v, row + pitch, y);
-                }
-            }
-        }
-    };
-    template <bool kF32, bool kAdd>
-    __device__ __forceinline__ Mode<kF32, kAdd> mode() const {
-        Mode<kF32, kAdd> m;
+    __device__ __forceinline__ SumEpilogue<kF32, kAdd> mode() const {
+        SumEpilogue<kF32, kAdd> m;
         m.C = C;
         m.add = add;
         m.M = M;
