@@ -401,7 +401,8 @@ __device__ __forceinline__ void asm_write_b128(uint32_t addr, const u32x4 &v) {
 // writes them to where the direct-to-LDS loads of a bf16 panel would have put
 // them.  issue() keeps the panel loaders' interface: its load j converts and
 // writes one 16-byte chunk, the last one also fetches the codes of two steps on
-// into the registers just emptied.  The ring has two stages, and a step's stage is
+// into the registers just emptied (the panel of step t+1 goes through step t's first
+// substep, whose MFMAs have the fewest other instructions beside them: see Pipeline).  The ring has two stages, and a step's stage is
 // its registers' too.
 //
 // Converting here and not where the fragments are read halves the conversions (two
@@ -658,22 +659,28 @@ struct IssueOrder {
                 const bool a_part = (k == 0) == kAFirst;
                 const int step = g + (a_part ? S::STAGES : S::BSTAGES);
                 if (step < 0) continue;
-                total += a_part ? S::kDmaA : S::kVmB;
-                // (4-bit weights are awaited where they are converted)
-                if (step == s && (a_part || !S::kBMx4)) (a_part ? end_a : end_b) = total;
+                total += a_part ? S::kDmaA : S::kDmaB;
+                if (step == s) (a_part ? end_a : end_b) = total;
             }
         }
         return total - (end_a > end_b ? end_a : end_b);
     }
-    // before step 0 (the prologue has issued groups up to -1)
-    static constexpr int kWaitPrologue = loads_after(0, -1);
+    // 4-bit weights are awaited where they are converted, in the first substep of the
+    // step before theirs, and the codes of two steps on are fetched there.  The
+    // prologue issues B's step 0, then A's STAGES steps; a step's first substep B's
+    // fetch, its last A's.  Behind A's step t+1 step t has then issued STAGES - 2
+    // panels of A and at least one fetch of B (exactly one in step 0: a wait that
+    // holds for every step).
+    static constexpr int kWaitPrologue =
+        S::kBMx4 ? (S::STAGES - 1) * S::kDmaA : loads_after(0, -1);   // before step 0
     // before step t+1, in step t (groups up to t-1 issued); the same for every t
-    static constexpr int kWaitSteady = loads_after(2 * kDeep + 3, 2 * kDeep + 1);
-    static_assert(loads_after(2 * kDeep + 4, 2 * kDeep + 2) == kWaitSteady, "steady state");
+    static constexpr int kWaitSteady = S::kBMx4 ? (S::STAGES - 2) * S::kDmaA + S::kVmB
+                                                : loads_after(2 * kDeep + 3, 2 * kDeep + 1);
+    static_assert(S::kBMx4 || loads_after(2 * kDeep + 4, 2 * kDeep + 2) == kWaitSteady, "steady state");
     // every wait from the first step on is the steady one
     static constexpr bool steady_from_start() {
         for (int t = 0; t <= 2 * kDeep; ++t)
-            if (loads_after(t + 1, t - 1) != kWaitSteady) return false;
+            if (!S::kBMx4 && loads_after(t + 1, t - 1) != kWaitSteady) return false;
         return true;
     }
     static_assert(steady_from_start(), "the first steps wait as the steady state does");
@@ -975,8 +982,14 @@ struct Pipeline {
     // epilogue (the ring must be idle: after drain()).
     template <class Issue>
     __device__ __forceinline__ void prologue_issue(const Issue &issue) {
+        if constexpr (S::kBMx4) {
+            issue(0, 1, stage_b(0), -1);
 #pragma unroll
-        for (int g = -Order::kDeep; g < 0; ++g) issue_group(issue, g);
+            for (int t = 0; t < S::STAGES; ++t) issue(t, 0, stage_a(t), -1);
+        } else {
+#pragma unroll
+            for (int g = -Order::kDeep; g < 0; ++g) issue_group(issue, g);
+        }
     }
     __device__ __forceinline__ void prologue_wait() {
         wait_vmcnt<Order::kWaitPrologue>();
@@ -1001,8 +1014,19 @@ struct Pipeline {
         if constexpr (KS < last) {
             if constexpr (S::MI == 16) {
                 hook(KS);
-                mma16<S, KS + 1, true, 0, 0, kMfma16, kInit && KS == 0>(
-                    f[KS & 1], f[(KS + 1) & 1], reads_of<PH>(t), acc, [](int) {});
+                // (4-bit weights: step t+1's panel is converted and written here, into
+                // the stage that the barrier in step t-1 freed, between the MFMAs that
+                // have the fewest loads and reads beside them)
+                constexpr int kChunks = S::kBMx4 && KS == 0 ? S::kDmaB : 0;
+                mma16<S, KS + 1, true, kChunks, 0, kMfma16, kInit && KS == 0>(
+                    f[KS & 1], f[(KS + 1) & 1], reads_of<PH>(t), acc, [&](int d) {
+                        if constexpr (kChunks > 0) {
+                            if constexpr (PH >= 0)
+                                issue(t + 1, 1, lds + S::kBRing + ((PH + 1) % S::BSTAGES) * S::kBBytes, d);
+                            else
+                                issue(t + 1, 1, stage_b(t + 1), d);
+                        }
+                    });
             } else {
                 read_frags<S, KS + 1>(addr_a(t), addr_b(t), off, f[(KS + 1) & 1]);
                 hook(KS);
@@ -1032,9 +1056,15 @@ struct Pipeline {
                 wait_vmcnt<Order::kWaitSteady>();
                 block_barrier();
                 constexpr int kNext = PH >= 0 ? (PH + 1) % kPeriod : -1;
-                mma16<S, 0, true, S::kDmaPerStep, kEarlyMfma, kMfma16>(
+                constexpr int kLoads = S::kBMx4 ? S::kDmaA : S::kDmaPerStep;
+                mma16<S, 0, true, kLoads, kEarlyMfma, kMfma16>(
                     f[KS & 1], f[(KS + 1) & 1], reads_of<kNext>(t + 1), acc, [&](int d) {
-                        if constexpr (PH >= 0)
+                        if constexpr (S::kBMx4) {
+                            if constexpr (PH >= 0)
+                                issue(t + S::STAGES, 0, lds + (PH % S::STAGES) * S::kABytes, d);
+                            else
+                                issue(t + S::STAGES, 0, stage_a(t + S::STAGES), d);
+                        } else if constexpr (PH >= 0)
                             issue_one<PH % S::STAGES, PH % S::BSTAGES>(issue, t, d);
                         else
                             issue_one(issue, t, d);

@@ -130,48 +130,48 @@ template struct ReduceLaunch<ShapeSmallLora, StoreEpilogue>;
 #elif SWIGLU_INSTANCE == 23
 template struct TilesLaunch<ShapeWideDx, GateGradEpilogue, kTailSplit>;
 #elif SWIGLU_INSTANCE == 24
-template struct TilesLaunch<ShapeWideDx, ActivationGradEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeWideDx, StorePairs, kTailSplit>;
 #elif SWIGLU_INSTANCE == 25
 template struct TilesLaunch<ShapeWideDw, WeightGradEpilogue, kTailSplit>;
 #elif SWIGLU_INSTANCE == 26
 template struct TilesLaunch<ShapeWide, PairMulKeep, kTailSplit>;
 #elif SWIGLU_INSTANCE == 27
 template struct TilesLaunch<ShapeQuadDx, GateGradEpilogue, kTailSplit>;
-template struct TilesLaunch<ShapeQuadDx, ActivationGradEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeQuadDx, StorePairs, kTailSplit>;
 #elif SWIGLU_INSTANCE == 28
 template struct TilesLaunch<ShapeQuadDw, WeightGradEpilogue, kTailSplit>;
 template struct TilesLaunch<ShapeQuad, PairMulKeep, kTailSplit>;
 #elif SWIGLU_INSTANCE == 29
 template struct TilesLaunch<ShapeSmallDx, GateGradEpilogue, kTailSplit>;
-template struct TilesLaunch<ShapeSmallDx, ActivationGradEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeSmallDx, StorePairs, kTailSplit>;
 template struct TilesLaunch<ShapeSmallLora, PairMulKeep, kTailSplit>;
 template struct ReduceLaunch<ShapeWideDx, GateGradEpilogue>;
-template struct ReduceLaunch<ShapeWideDx, ActivationGradEpilogue>;
+template struct ReduceLaunch<ShapeWideDx, StorePairs>;
 template struct ReduceLaunch<ShapeWideDw, WeightGradEpilogue>;
 template struct ReduceLaunch<ShapeWide, PairMulKeep>;
 template struct ReduceLaunch<ShapeQuadDx, GateGradEpilogue>;
-template struct ReduceLaunch<ShapeQuadDx, ActivationGradEpilogue>;
+template struct ReduceLaunch<ShapeQuadDx, StorePairs>;
 template struct ReduceLaunch<ShapeQuadDw, WeightGradEpilogue>;
 template struct ReduceLaunch<ShapeQuad, PairMulKeep>;
 template struct ReduceLaunch<ShapeSmallDx, GateGradEpilogue>;
-template struct ReduceLaunch<ShapeSmallDx, ActivationGradEpilogue>;
+template struct ReduceLaunch<ShapeSmallDx, StorePairs>;
 template struct ReduceLaunch<ShapeSmallLora, PairMulKeep>;
 #elif SWIGLU_INSTANCE == 30
-template struct TilesLaunch<ShapeWideMx4, PairMulEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeWideMx4, PairMulPairs, kTailSplit>;
 #elif SWIGLU_INSTANCE == 31
-template struct TilesLaunch<ShapeWideMx4, StoreEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeWideMx4, StorePairs, kTailSplit>;
 #elif SWIGLU_INSTANCE == 32
-template struct TilesLaunch<ShapeQuadMx4, PairMulEpilogue, kTailSplit>;
-template struct TilesLaunch<ShapeQuadMx4, StoreEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeQuadMx4, PairMulPairs, kTailSplit>;
+template struct TilesLaunch<ShapeQuadMx4, StorePairs, kTailSplit>;
 #elif SWIGLU_INSTANCE == 33
-template struct TilesLaunch<ShapeSmallMx4, PairMulEpilogue, kTailSplit>;
-template struct TilesLaunch<ShapeSmallMx4, StoreEpilogue, kTailSplit>;
-template struct ReduceLaunch<ShapeWideMx4, PairMulEpilogue>;
-template struct ReduceLaunch<ShapeWideMx4, StoreEpilogue>;
-template struct ReduceLaunch<ShapeQuadMx4, PairMulEpilogue>;
-template struct ReduceLaunch<ShapeQuadMx4, StoreEpilogue>;
-template struct ReduceLaunch<ShapeSmallMx4, PairMulEpilogue>;
-template struct ReduceLaunch<ShapeSmallMx4, StoreEpilogue>;
+template struct TilesLaunch<ShapeSmallMx4, PairMulPairs, kTailSplit>;
+template struct TilesLaunch<ShapeSmallMx4, StorePairs, kTailSplit>;
+template struct ReduceLaunch<ShapeWideMx4, PairMulPairs>;
+template struct ReduceLaunch<ShapeWideMx4, StorePairs>;
+template struct ReduceLaunch<ShapeQuadMx4, PairMulPairs>;
+template struct ReduceLaunch<ShapeQuadMx4, StorePairs>;
+template struct ReduceLaunch<ShapeSmallMx4, PairMulPairs>;
+template struct ReduceLaunch<ShapeSmallMx4, StorePairs>;
 #elif SWIGLU_INSTANCE == 34
 template struct TilesLaunch<ShapeWideDx, GateGradEpilogue, kTailQuarter>;
 #elif SWIGLU_INSTANCE == 35

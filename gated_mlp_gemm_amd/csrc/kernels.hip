@@ -808,6 +808,15 @@ hipError_t launch_down_train(const uint16_t *H, const uint16_t *W3t, uint16_t *O
     return launch_wide_or_quad<ShapeWide, ShapeQuad>(A, B, M, D, N, epi, 0.0, ws, stream);
 }
 
+static StorePairs store_pairs(uint16_t *C, int M, int cols) {
+    StorePairs epi;
+    epi.C = C;
+    epi.add = nullptr;
+    epi.M = M;
+    epi.N = cols;
+    return epi;
+}
+
 // D [M][cols] = dY [M][C] . W [C][cols], with a weight contracted by its rows.
 template <class Epi, bool kQuarters = false>
 static hipError_t launch_dx(const uint16_t *dY, const uint16_t *W, int M, int cols, int C,
@@ -821,12 +830,7 @@ static hipError_t launch_dx(const uint16_t *dY, const uint16_t *W, int M, int co
 }
 hipError_t launch_grad_input(const uint16_t *dY, const uint16_t *W, uint16_t *dX, int M, int cols,
                              int C, const GemmWorkspace &ws, hipStream_t stream) {
-    ActivationGradEpilogue epi;
-    epi.C = dX;
-    epi.add = nullptr;
-    epi.M = M;
-    epi.N = cols;
-    return launch_dx(dY, W, M, cols, C, epi, 0.0, ws, stream);
+    return launch_dx(dY, W, M, cols, C, store_pairs(dX, M, cols), 0.0, ws, stream);
 }
 hipError_t launch_grad_gate_up(const uint16_t *dOut, const uint16_t *W3t, const uint16_t *GU,
                                uint16_t *dGU, int M, int N, int D, const GemmWorkspace &ws,
@@ -860,10 +864,10 @@ static hipError_t launch_mx4(const uint16_t *X, const KMajor &B, int M, int cols
                              const Epi &epi, const GemmWorkspace &ws, hipStream_t stream) {
     const KMajor A{X, M, 1, 0, 0, 0, nullptr};
     if (M <= kMx4FewRows) {
-        constexpr bool kGated = std::is_same<Epi, PairMulEpilogue>::value;
+        constexpr bool kGated = std::is_same<Epi, PairMulPairs>::value;
         uint16_t *y;
         if constexpr (kGated) y = epi.Y;
-        else y = epi.C;
+        else y = static_cast<uint16_t *>(epi.C);
         const hipError_t e =
             launch_mx4_few(X, static_cast<const uint8_t *>(B.base), B.scales, y, M, cols, K, kGated,
                            ws.cus, stream);
@@ -875,13 +879,12 @@ static hipError_t launch_mx4(const uint16_t *X, const KMajor &B, int M, int cols
 hipError_t launch_fused_mx4(const uint16_t *A, const uint8_t *Wq, const uint8_t *Ws, uint16_t *Y,
                             int M, int N, int K, const GemmWorkspace &ws, hipStream_t stream) {
     return launch_mx4(A, KMajor{Wq, 2 * N, 1, 0, 0, 0, Ws}, M, 2 * N, K,
-                      PairMulEpilogue{Y, M, N, N, 1.0f}, ws, stream);
+                      PairMulPairs{{Y, M, N, N, 1.0f}}, ws, stream);
 }
 hipError_t launch_down_proj_mx4(const uint16_t *H, const uint8_t *W3q, const uint8_t *W3s,
                                 uint16_t *Out, int M, int N, int D, const GemmWorkspace &ws,
                                 hipStream_t stream) {
-    return launch_mx4(H, KMajor{W3q, D, 1, 0, 0, 0, W3s}, M, D, N, StoreEpilogue{Out, M, D}, ws,
-                      stream);
+    return launch_mx4(H, KMajor{W3q, D, 1, 0, 0, 0, W3s}, M, D, N, store_pairs(Out, M, D), ws, stream);
 }
 
 // dGU of a given dH: the epilogue's arithmetic, 8 outputs of H a lane.

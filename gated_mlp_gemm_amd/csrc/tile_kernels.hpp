@@ -378,6 +378,45 @@ struct PairMulKeep : PairMulEpilogue {
     }
 };
 
+// The same without GU: SiLU(Gate) Up of the products with 4-bit weights.
+struct PairMulPairs : PairMulEpilogue {
+    template <class S, bool kFromAcc = true>
+    __device__ __forceinline__ void unit(const typename S::Acc &g, const typename S::Acc &up, int u,
+                                         int m0, int n0, int tid) const {
+        static_assert(S::TN % 2 == 0, "paired layout");
+        const int lane = tid & 63, wave = tid >> 6;
+        const int tm = u / (S::TN / 2), tp = u % (S::TN / 2);
+        const int y0 = n0 / 2;
+        const uint32_t pitch = static_cast<uint32_t>(N) * 2u;
+        const __amdgpu_buffer_rsrc_t ry = rows_rsrc(Y, m0, min(S::BM, M - m0), pitch);
+        const uint32_t off =
+            Pairs::offset<S>((wave / S::WN) * S::kWaveM, (wave % S::WN) * (S::kWaveN / 2) + tp * 32,
+                             y0, min(S::BN / 2, N - y0), static_cast<uint32_t>(N), 2u, lane);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            // (the product before the exchange: one instead of two)
+            const float y0_ = silu(acc_value<kFromAcc>(g.get(Pairs::left(p)))) *
+                              acc_value<kFromAcc>(up.get(Pairs::left(p)));
+            const float y1_ = silu(acc_value<kFromAcc>(g.get(Pairs::right(p)))) *
+                              acc_value<kFromAcc>(up.get(Pairs::right(p)));
+            float lo, hi;
+            Pairs::exchange(y0_, y1_, lo, hi);
+            store4(ry, off, static_cast<uint32_t>(tm * 32 + Pairs::row(p)) * pitch, pack_bf16x2(lo, hi));
+        }
+    }
+    template <class S>
+    __device__ __forceinline__ void apply(const typename S::Acc (&acc)[S::TM][S::TN], int m0, int n0,
+                                          int tid) const {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < S::TM * S::TN / 2; ++u) {
+            unit<S>(acc[u / (S::TN / 2)][2 * (u % (S::TN / 2))],
+                    acc[u / (S::TN / 2)][2 * (u % (S::TN / 2)) + 1], u, m0, n0, tid);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+};
+
 // Epilogues of one block at a time, which may read a matrix of the output's shape
 // beside the accumulators: D::load fetches a block's values and D::finish uses them.
 // A block's loads go out kAhead blocks before its use, so that a tile waits for
@@ -524,8 +563,8 @@ struct SumEpilogue : BlockEpilogue<SumEpilogue<kF32, kAdd>> {
     }
 };
 
-// A gradient by an activation: bf16.
-struct ActivationGradEpilogue : SumEpilogue<false, false> {};
+// bf16 results: a gradient by an activation, the down projection with 4-bit weights.
+struct StorePairs : SumEpilogue<false, false> {};
 
 // A weight's gradient: bf16 or fp32 (f32), with add or without (NULL).
 struct WeightGradEpilogue {
