@@ -1036,14 +1036,10 @@ int swiglu_down_proj_backward(const uint16_t *dOut, const uint16_t *H, const uin
     st = check_device(&cus);
     if (st != SWIGLU_OK) return st;
     const hipStream_t s = (hipStream_t)stream;
-    const swiglu::GemmWorkspace ws = make_ws(workspace, workspace_bytes, cus);
-    hipError_t e = hipSuccess;
-    if (dH && M > 0)
-        e = swiglu::launch_grad_input(dOut, W3t, dH, (int)M, (int)N, (int)D, ws, s);
-    if (e == hipSuccess && dW3t)
-        e = swiglu::launch_weight_grad(dOut, H, dW3t, dW3t_add, grad_type == SWIGLU_F32, (int)M,
-                                       (int)D, (int)N, ws, s);
-    return launched(e, "down projection backward");
+    return launched(swiglu::launch_down_backward(dOut, H, W3t, dH, dW3t, dW3t_add,
+                                                 grad_type == SWIGLU_F32, (int)M, (int)N, (int)D,
+                                                 make_ws(workspace, workspace_bytes, cus), s),
+                    "down projection backward");
 }
 
 int swiglu_fused_gemm_backward(const uint16_t *dH, const uint16_t *A, const uint16_t *W_fused,
@@ -1076,14 +1072,12 @@ int swiglu_fused_gemm_backward(const uint16_t *dH, const uint16_t *A, const uint
     st = check_device(&cus);
     if (st != SWIGLU_OK) return st;
     const hipStream_t s = (hipStream_t)stream;
-    const swiglu::GemmWorkspace ws = make_ws(workspace, workspace_bytes, cus);
     hipError_t e = hipSuccess;
     if (M > 0) e = swiglu::launch_gate_grad(dH, GU, dGU, M * N, s);
-    if (e == hipSuccess && dA && M > 0)
-        e = swiglu::launch_grad_input(dGU, W_fused, dA, (int)M, (int)K, (int)(2 * N), ws, s);
-    if (e == hipSuccess && dW_fused)
-        e = swiglu::launch_weight_grad(dGU, A, dW_fused, dW_fused_add, grad_type == SWIGLU_F32,
-                                       (int)M, (int)(2 * N), (int)K, ws, s);
+    if (e == hipSuccess)
+        e = swiglu::launch_stage_backward(dGU, A, W_fused, dA, dW_fused, dW_fused_add,
+                                          grad_type == SWIGLU_F32, (int)M, (int)N, (int)K,
+                                          make_ws(workspace, workspace_bytes, cus), s);
     return launched(e, "fused SwiGLU backward");
 }
 
@@ -1122,18 +1116,14 @@ int swiglu_gated_mlp_backward(const uint16_t *dOut, const uint16_t *A, const uin
     st = check_device(&cus);
     if (st != SWIGLU_OK) return st;
     const hipStream_t s = (hipStream_t)stream;
-    const swiglu::GemmWorkspace ws = make_ws(workspace, workspace_bytes, cus);
+    swiglu::GemmWorkspace ws = make_ws(workspace, workspace_bytes, cus);
     const bool f32 = grad_type == SWIGLU_F32;
-    hipError_t e = hipSuccess;
-    if (M > 0)
-        e = swiglu::launch_grad_gate_up(dOut, W3t, GU, dGU, (int)M, (int)N, (int)K, ws, s);
-    if (e == hipSuccess && dW3t)
-        e = swiglu::launch_weight_grad(dOut, H, dW3t, dW3t_add, f32, (int)M, (int)K, (int)N, ws, s);
-    if (e == hipSuccess && dA && M > 0)
-        e = swiglu::launch_grad_input(dGU, W_fused, dA, (int)M, (int)K, (int)(2 * N), ws, s);
-    if (e == hipSuccess && dW_fused)
-        e = swiglu::launch_weight_grad(dGU, A, dW_fused, dW_fused_add, f32, (int)M, (int)(2 * N),
-                                       (int)K, ws, s);
+    hipError_t e = swiglu::launch_gate_backward(dOut, H, W3t, GU, dGU, dW3t, dW3t_add, f32, (int)M,
+                                                (int)N, (int)K, ws, s);
+    ws.tag = next_arrival_tag();
+    if (e == hipSuccess)
+        e = swiglu::launch_stage_backward(dGU, A, W_fused, dA, dW_fused, dW_fused_add, f32, (int)M,
+                                          (int)N, (int)K, ws, s);
     return launched(e, "gated MLP backward");
 }
 

@@ -9,6 +9,7 @@
 // with fewer workers than groups starts the longest compiles first.  A group
 // left out of the list leaves its run() undefined, which the link of the
 // library reports.
+#include "pair_kernels.hpp"
 #include "tile_kernels.hpp"
 
 namespace swiglu {
@@ -19,6 +20,17 @@ hipError_t TilesLaunch<S, Epi, TAIL>::run(int grid, const KMajor &A, const KMajo
                                           hipStream_t stream) {
     hipLaunchKernelGGL((gemm_tiles_kernel<S, Epi, TAIL>), dim3(grid), dim3(S::kThreads), 0,
                        stream, A, B, M, K, epi, sch);
+    return hipGetLastError();
+}
+
+template <class SX, class EX, class SW>
+hipError_t PairLaunch<SX, EX, SW>::run(int grid, const KMajor &Ax, const KMajor &Bx, int Mx, int Kx,
+                                       const EX &ex, const Schedule &sx, const KMajor &Aw,
+                                       const KMajor &Bw, int Mw, int Kw,
+                                       const WeightGradEpilogue &ew, const Schedule &sw,
+                                       const PairCounts &counts, hipStream_t stream) {
+    hipLaunchKernelGGL((gemm_pair_kernel<SX, EX, SW>), dim3(grid), dim3(256), 0, stream, Ax, Bx, Mx,
+                       Kx, ex, sx, Aw, Bw, Mw, Kw, ew, sw, counts);
     return hipGetLastError();
 }
 
@@ -176,6 +188,10 @@ template struct ReduceLaunch<ShapeSmallMx4, StorePairs>;
 template struct TilesLaunch<ShapeWideDx, GateGradEpilogue, kTailQuarter>;
 #elif SWIGLU_INSTANCE == 35
 template struct TilesLaunch<ShapeWide, PairMulKeep, kTailQuarter>;
+#elif SWIGLU_INSTANCE == 36
+template struct PairLaunch<ShapeWideDx, GateGradEpilogue, ShapeWideDw>;
+#elif SWIGLU_INSTANCE == 37
+template struct PairLaunch<ShapeWideDx, StorePairs, ShapeWideDw>;
 #else
 #error "SWIGLU_INSTANCE is past the end of the instance list"
 #endif

@@ -6,6 +6,7 @@
 // gist.science technical summary, section X.
 #include "launch.hpp"
 
+#include "pair_kernels.hpp"
 #include "tile_kernels.hpp"
 
 #include <cmath>
@@ -818,42 +819,187 @@ static StorePairs store_pairs(uint16_t *C, int M, int cols) {
 }
 
 // D [M][cols] = dY [M][C] . W [C][cols], with a weight contracted by its rows.
-template <class Epi, bool kQuarters = false>
-static hipError_t launch_dx(const uint16_t *dY, const uint16_t *W, int M, int cols, int C,
-                            const Epi &epi, double extra, const GemmWorkspace &ws,
-                            hipStream_t stream) {
-    const KMajor A{dY, M, 1, 0, 0, 0, nullptr};
-    const KMajor B{W, cols, 1, 0, 0, cols, nullptr};
-    if (M <= 128) return launch_split_gemm<ShapeSmallDx>(A, B, M, cols, C, epi, ws, stream);
-    return launch_wide_or_quad<ShapeWideDx, ShapeQuadDx, Epi, kQuarters>(A, B, M, cols, C, epi,
-                                                                         extra, ws, stream);
+// One side of a backward pass: D [M][cols] = A . B over K.
+template <class Epi>
+struct GradProduct {
+    KMajor A, B;
+    int M, cols, K;
+    Epi epi;
+    double extra;   // make_grad_schedule
+};
+// dY [M][C] . W [C][cols], with a weight contracted by its rows.
+template <class Epi>
+static GradProduct<Epi> dx_product(const uint16_t *dY, const uint16_t *W, int M, int cols, int C,
+                                   const Epi &epi, double extra) {
+    return {KMajor{dY, M, 1, 0, 0, 0, nullptr}, KMajor{W, cols, 1, 0, 0, cols, nullptr}, M, cols, C,
+            epi, extra};
 }
-hipError_t launch_grad_input(const uint16_t *dY, const uint16_t *W, uint16_t *dX, int M, int cols,
-                             int C, const GemmWorkspace &ws, hipStream_t stream) {
-    return launch_dx(dY, W, M, cols, C, store_pairs(dX, M, cols), 0.0, ws, stream);
+static GradProduct<StorePairs> input_product(const uint16_t *dY, const uint16_t *W, uint16_t *dX,
+                                             int M, int cols, int C) {
+    return dx_product(dY, W, M, cols, C, store_pairs(dX, M, cols), 0.0);
 }
-hipError_t launch_grad_gate_up(const uint16_t *dOut, const uint16_t *W3t, const uint16_t *GU,
-                               uint16_t *dGU, int M, int N, int D, const GemmWorkspace &ws,
-                               hipStream_t stream) {
+static GradProduct<GateGradEpilogue> gate_product(const uint16_t *dOut, const uint16_t *W3t,
+                                                  const uint16_t *GU, uint16_t *dGU, int M, int N,
+                                                  int D) {
     GateGradEpilogue epi;
     epi.GU = GU;
     epi.dGU = dGU;
     epi.M = M;
     epi.N = N;
-    return launch_dx<GateGradEpilogue, true>(dOut, W3t, M, N, D, epi, kGateGradUs, ws, stream);
+    return dx_product(dOut, W3t, M, N, D, epi, kGateGradUs);
 }
-
-hipError_t launch_weight_grad(const uint16_t *dY, const uint16_t *X, void *dW, const void *add,
-                              bool f32, int M, int rows, int cols, const GemmWorkspace &ws_,
-                              hipStream_t stream) {
-    const KMajor A{dY, rows, 1, 0, 0, rows, nullptr};
-    const KMajor B{X, cols, 1, 0, 0, cols, nullptr};
-    const WeightGradEpilogue epi{dW, add, rows, cols, f32 ? 1 : 0};
-    GemmWorkspace ws = ws_;
-    if (M == 0) ws.tail = kTailWhole;   // no K step to split: the tiles store zeros (+ add)
+// dY [M][rows]^T . X [M][cols].
+static GradProduct<WeightGradEpilogue> weight_product(const uint16_t *dY, const uint16_t *X, void *dW,
+                                                      const void *add, bool f32, int M, int rows,
+                                                      int cols) {
     // 2 bytes more an element in fp32, and what is added is read
     const double extra = ((f32 ? 2 : 0) + (add ? (f32 ? 4 : 2) : 0)) * (kGateGradUs / 8.0);
-    return launch_wide_or_quad<ShapeWideDw, ShapeQuadDw>(A, B, rows, cols, M, epi, extra, ws, stream);
+    return {KMajor{dY, rows, 1, 0, 0, rows, nullptr}, KMajor{X, cols, 1, 0, 0, cols, nullptr}, rows,
+            cols, M, WeightGradEpilogue{dW, add, rows, cols, f32 ? 1 : 0}, extra};
+}
+
+template <class Epi>
+static hipError_t launch_dx(const GradProduct<Epi> &p, const GemmWorkspace &ws, hipStream_t stream) {
+    if (p.M <= 128) return launch_split_gemm<ShapeSmallDx>(p.A, p.B, p.M, p.cols, p.K, p.epi, ws, stream);
+    return launch_wide_or_quad<ShapeWideDx, ShapeQuadDx, Epi,
+                               std::is_same<Epi, GateGradEpilogue>::value>(
+        p.A, p.B, p.M, p.cols, p.K, p.epi, p.extra, ws, stream);
+}
+static hipError_t launch_dw(const GradProduct<WeightGradEpilogue> &p, const GemmWorkspace &ws_,
+                            hipStream_t stream) {
+    GemmWorkspace ws = ws_;
+    if (p.K == 0) ws.tail = kTailWhole;   // no K step to split: the tiles store zeros (+ add)
+    return launch_wide_or_quad<ShapeWideDw, ShapeQuadDw>(p.A, p.B, p.M, p.cols, p.K, p.epi, p.extra, ws,
+                                                         stream);
+}
+
+// Tiles of S over a product, all whole, or all split where one would take more than half
+// of the `fair` share of a compute unit (`slots` partials left).
+template <class S, class Epi>
+static Schedule pair_schedule(const GradProduct<Epi> &p, double fair, int slots, int cus, float *partials) {
+    Schedule sch{};
+    sch.tiles_m = cdiv(p.M, S::BM);
+    sch.tiles_n = cdiv(p.cols, S::BN);
+    sch.nk = cdiv(p.K, S::BK);
+    sch.group_m = sch.tiles_m <= 8 && sch.nk <= 32 ? 4 : 8;
+    const int64_t T = static_cast<int64_t>(sch.tiles_m) * sch.tiles_n;
+    sch.dp = static_cast<int>(T);
+    const double tile = GradCost<S>::kRound + p.extra + sch.nk * GradCost<S>::step(cus, cus);
+    if (fair > 0.0 && tile > 0.6 * fair) {
+        int64_t s = static_cast<int64_t>(tile / (0.5 * fair)) + 1;
+        if (s > slots / T) s = slots / T;
+        if (s > sch.nk) s = sch.nk;
+        if (s >= 2) {
+            sch.dp = 0;
+            sch.split_tiles = static_cast<int>(T);
+            sch.pieces = static_cast<int>(s);
+            sch.partials = partials;
+        }
+    }
+    return sch;
+}
+// Compute-unit time of a product's tiles.  (Half of the extra that their epilogues move:
+// beside the other product's K steps the rest costs nothing.)
+template <class S, class Epi>
+static double product_us(const GradProduct<Epi> &p, int cus) {
+    const double T = static_cast<double>(cdiv(p.M, S::BM)) * cdiv(p.cols, S::BN);
+    return T * (GradCost<S>::kRound + 0.5 * p.extra + cdiv(p.K, S::BK) * GradCost<S>::step(cus, cus));
+}
+
+// Both products in one launch, if that is predicted to be faster than `apart`;
+// hipErrorNotSupported, nothing launched, if it is not or there is no workspace for it.
+// Measured one after the other and together (us; dH and dW3t, dA and dW_fused):
+//   M=512 K=3584 N=18944 154 / 130, 302 / 293;   M=2048 K=1536 N=8960 105 / 87, 202 / 199;
+//   M=2048 K=5120 N=13824 434 / 403, 1023 / 814; M=8192 K=5120 N=13824 1528 / 1526,
+//   3284 / 3277; but M=512 K=896 N=4864 23 / 42, where 128x128 tiles fill the device
+//   better, and M=33 K=896 N=4872 (with 128x64 tiles beside the weight's) 13 / 22: so
+//   not for few rows, nor where a compute unit's share is short.
+constexpr double kPairUs = 30.0;
+template <class EX>
+static hipError_t launch_pair(const GradProduct<EX> &x, const GradProduct<WeightGradEpilogue> &w,
+                              const GemmWorkspace &ws, double apart, hipStream_t stream) {
+    using SX = ShapeWideDx;
+    using SW = ShapeWideDw;
+    if (ws.base == nullptr || ws.bytes < workspace_bytes_for(ws.cus) || ws.cus < 8 || ws.cus % 8 != 0 ||
+        ws.tile != 0 || ws.tail != kTailAuto || w.K == 0)
+        return hipErrorNotSupported;
+    const double fair = (product_us<SX>(x, ws.cus) + product_us<SW>(w, ws.cus)) / ws.cus;
+    if (fair < kPairUs) return hipErrorNotSupported;
+    // the partials' slots but one, which holds the counts
+    const int slots = ws.cus - 1;
+    constexpr int64_t kSlot = SX::BM * SX::BN;
+    float *partials = reinterpret_cast<float *>(ws.base);
+    const Schedule sx = pair_schedule<SX>(x, fair, slots, ws.cus, partials);
+    const int used = sx.split_tiles * sx.pieces;
+    const Schedule sw = pair_schedule<SW>(w, fair, slots - used, ws.cus, partials + used * kSlot);
+    const int partial_slots = used + sw.split_tiles * sw.pieces;
+    auto item_us = [&](const Schedule &s, double extra) {
+        return GradCost<SX>::kRound + 0.5 * extra +
+               (s.pieces ? cdiv(s.nk, s.pieces) : s.nk) * GradCost<SX>::step(ws.cus, ws.cus);
+    };
+    const double ix = item_us(sx, x.extra), iw = item_us(sw, w.extra);
+    const double together = fair + 0.5 * (ix < iw ? ix : iw) +
+                            (partial_slots ? kReduceUs + partial_slots * kSlot * 8.0 / kPartialBytesPerUs : 0.0);
+    const int64_t items = static_cast<int64_t>(sx.dp) + sw.dp + partial_slots;
+    if (together >= apart || items / 8 >= (1 << kArrivalBits) - 8) return hipErrorNotSupported;
+    // (the longer items first: the others even the end out)
+    const PairCounts counts{reinterpret_cast<uint64_t *>(partials + slots * kSlot), ws.tag,
+                            iw >= ix ? 1 : 0};
+    hipError_t e = PairLaunch<SX, EX, SW>::run(ws.cus, x.A, x.B, x.M, x.K, x.epi, sx, w.A, w.B, w.M, w.K,
+                                               w.epi, sw, counts, stream);
+    if (e == hipSuccess && sx.pieces)
+        e = ReduceLaunch<SX, EX>::run(sx.split_tiles * SX::kWaves * SX::TM * SX::TN, x.epi, sx, stream);
+    if (e == hipSuccess && sw.pieces)
+        e = ReduceLaunch<SW, WeightGradEpilogue>::run(sw.split_tiles * SW::kWaves * SW::TM * SW::TN,
+                                                      w.epi, sw, stream);
+    return e;
+}
+template <class Wide, class Quad, bool kQuarters, class Epi>
+static double apart_us(const GradProduct<Epi> &p, const GemmWorkspace &ws) {
+    double wide = 0.0, quad = 0.0;
+    make_grad_schedule<Wide, kQuarters>(p.M, p.cols, p.K, p.extra, ws, &wide);
+    make_grad_schedule<Quad, false>(p.M, p.cols, p.K, p.extra, ws, &quad);
+    return wide < quad ? wide : quad;
+}
+// The gradients by an activation and by a weight.
+template <class EX>
+static hipError_t launch_grads(const GradProduct<EX> &x, const GradProduct<WeightGradEpilogue> &w,
+                               const GemmWorkspace &ws, hipStream_t stream) {
+    constexpr double kLaunchUs = 2.0;   // of the second launch
+    if (x.M > 128) {
+        const double apart =
+            apart_us<ShapeWideDx, ShapeQuadDx, std::is_same<EX, GateGradEpilogue>::value>(x, ws) +
+            apart_us<ShapeWideDw, ShapeQuadDw, false>(w, ws) + kLaunchUs;
+        const hipError_t e = launch_pair(x, w, ws, apart, stream);
+        if (e != hipErrorNotSupported) return e;
+    }
+    const hipError_t e = launch_dx(x, ws, stream);
+    return e != hipSuccess ? e : launch_dw(w, ws, stream);
+}
+
+hipError_t launch_down_backward(const uint16_t *dOut, const uint16_t *H, const uint16_t *W3t,
+                                uint16_t *dH, void *dW3t, const void *add, bool f32, int M, int N,
+                                int D, const GemmWorkspace &ws, hipStream_t stream) {
+    const auto x = input_product(dOut, W3t, dH, M, N, D);
+    const auto w = weight_product(dOut, H, dW3t, add, f32, M, D, N);
+    if (dH && dW3t && M > 0) return launch_grads(x, w, ws, stream);
+    if (dH && M > 0) return launch_dx(x, ws, stream);
+    return dW3t ? launch_dw(w, ws, stream) : hipSuccess;
+}
+hipError_t launch_gate_backward(const uint16_t *dOut, const uint16_t *H, const uint16_t *W3t,
+                                const uint16_t *GU, uint16_t *dGU, void *dW3t, const void *add,
+                                bool f32, int M, int N, int D, const GemmWorkspace &ws,
+                                hipStream_t stream) {
+    const auto x = gate_product(dOut, W3t, GU, dGU, M, N, D);
+    const auto w = weight_product(dOut, H, dW3t, add, f32, M, D, N);
+    if (dW3t && M > 0) return launch_grads(x, w, ws, stream);
+    if (M > 0) return launch_dx(x, ws, stream);
+    return dW3t ? launch_dw(w, ws, stream) : hipSuccess;
+}
+hipError_t launch_stage_backward(const uint16_t *dGU, const uint16_t *A, const uint16_t *W_fused,
+                                 uint16_t *dA, void *dW, const void *add, bool f32, int M, int N,
+                                 int K, const GemmWorkspace &ws, hipStream_t stream) {
+    return launch_down_backward(dGU, A, W_fused, dA, dW, add, f32, M, K, 2 * N, ws, stream);
 }
 
 // ---------------------------------------------------------------------------

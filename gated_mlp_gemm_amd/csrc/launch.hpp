@@ -61,20 +61,24 @@ hipError_t launch_fused_train(const uint16_t *A, const uint16_t *Wf, uint16_t *H
 // launch_down_proj with the training calls' schedules.
 hipError_t launch_down_train(const uint16_t *H, const uint16_t *W3t, uint16_t *Out, int M, int N,
                              int D, const GemmWorkspace &ws, hipStream_t stream);
-// dX [M][cols] = bf16(dY [M][C] . W), W [C][cols] as the forward pass holds it.
-hipError_t launch_grad_input(const uint16_t *dY, const uint16_t *W, uint16_t *dX, int M, int cols,
-                             int C, const GemmWorkspace &ws, hipStream_t stream);
-// dGU [M][2N] of dH = dOut [M][D] . W3 (W3t [D][N]), which stays in registers; dGU may be GU.
-hipError_t launch_grad_gate_up(const uint16_t *dOut, const uint16_t *W3t, const uint16_t *GU,
-                               uint16_t *dGU, int M, int N, int D, const GemmWorkspace &ws,
-                               hipStream_t stream);
-// ... of a given dH, count = M N (a multiple of 8).
+// dGU of a given dH, count = M N (a multiple of 8); dGU may be GU.
 hipError_t launch_gate_grad(const uint16_t *dH, const uint16_t *GU, uint16_t *dGU, int64_t count,
                             hipStream_t stream);
-// dW [rows][cols] = dY [M][rows]^T . X [M][cols] (+ add), fp32 (f32) or bf16; add may be dW.
-hipError_t launch_weight_grad(const uint16_t *dY, const uint16_t *X, void *dW, const void *add,
-                              bool f32, int M, int rows, int cols, const GemmWorkspace &ws,
-                              hipStream_t stream);
+// Gradients by an activation (bf16) and by a weight (fp32 or bf16, f32; + add, which may
+// be the gradient itself), each unless it is NULL; M == 0: the weight's is zeros (+ add).
+//   down projection: dH [M][N] = dOut [M][D] . W3, dW3t [D][N] = dOut^T . H
+hipError_t launch_down_backward(const uint16_t *dOut, const uint16_t *H, const uint16_t *W3t,
+                                uint16_t *dH, void *dW3t, const void *add, bool f32, int M, int N,
+                                int D, const GemmWorkspace &ws, hipStream_t stream);
+//   ... with dGU [M][2N] of that dH, which stays in registers (dGU may be GU)
+hipError_t launch_gate_backward(const uint16_t *dOut, const uint16_t *H, const uint16_t *W3t,
+                                const uint16_t *GU, uint16_t *dGU, void *dW3t, const void *add,
+                                bool f32, int M, int N, int D, const GemmWorkspace &ws,
+                                hipStream_t stream);
+//   SwiGLU stage: dA [M][K] = dGU [M][2N] . W_fused^T, dW_fused [2N][K] = dGU^T . A
+hipError_t launch_stage_backward(const uint16_t *dGU, const uint16_t *A, const uint16_t *W_fused,
+                                 uint16_t *dA, void *dW, const void *add, bool f32, int M, int N,
+                                 int K, const GemmWorkspace &ws, hipStream_t stream);
 // 4-bit weights: codes [rows][K / 2] and scales [rows][K / 32] of `count` numbers.
 hipError_t launch_quantize_mx4(const uint16_t *x, uint8_t *q, uint8_t *s, int64_t count,
                                hipStream_t stream);

@@ -233,12 +233,14 @@ def test_down_proj_backward(dev, M, N, D):
         out.check()
         within(dH, dh, "dH")
         within(dW, want_dw(c["dOut"], c["H"], dtype), "dW3t")
-    # one without the other, and the types that are chosen
+    # one without the other (their schedules may be others), and the types that are chosen
     only, none = sw.swiglu_down_proj_backward(d["dOut"], d["H"], d["W3"], need_dW=False, workspace=ws)
-    assert none is None and torch.equal(only, dH)
+    assert none is None
+    within(only, dh, "dH alone")
     none, only = sw.swiglu_down_proj_backward(d["dOut"], d["H"], d["W3"], need_dH=False, workspace=ws,
                                               grad_dtype=F32)
-    assert none is None and torch.equal(only, dW)
+    assert none is None and only.dtype == F32
+    within(only, want_dw(c["dOut"], c["H"], F32), "dW3t alone")
     add = d["addW3"]
     got = sw.swiglu_down_proj_backward(d["dOut"], d["H"], d["W3"], dW3t_add=add)[1]
     assert got.dtype == F32
@@ -268,7 +270,8 @@ def test_fused_gemm_backward(dev, M, K, N):
     assert dGU2 is GU and torch.equal(GU, dGU) and torch.equal(dA2, dA) and torch.equal(dW2, dW)
     dA2, none, dGU2 = sw.swiglu_fused_gemm_backward(d["dH"], d["A"], d["W"], d["GU"], need_dW=False,
                                                     workspace=ws)
-    assert none is None and torch.equal(dA2, dA) and torch.equal(dGU2, dGU)
+    assert none is None and torch.equal(dGU2, dGU)
+    within(dA2, rounded(*product(own, c["W"]), BF), "dA alone")
 
 
 def test_frozen_weights_and_first_layer(dev):
