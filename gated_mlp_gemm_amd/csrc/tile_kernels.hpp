@@ -326,10 +326,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void *base, in
 __device__ __forceinline__ u32x2 load8(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff) {
     return __builtin_amdgcn_raw_buffer_load_b64(r, static_cast<int>(off), static_cast<int>(soff), 0);
 }
+// kNt: with the non-temporal hint.
+template <bool kNt = false>
 __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff,
                                        uint32_t a, uint32_t b) {
     __builtin_amdgcn_raw_buffer_store_b64(u32x2{a, b}, r, static_cast<int>(off),
-                                          static_cast<int>(soff), 0);
+                                          static_cast<int>(soff), kNt ? 2 : 0);
 }
 __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t soff,
                                        uint32_t a) {
@@ -338,6 +340,13 @@ __device__ __forceinline__ void store4(__amdgpu_buffer_rsrc_t r, uint32_t off, u
 
 // The training forward pass: variant I's epilogue, which also stores Gate and Up
 // as bf16, interleaved as W_fused's columns: GU [M][2N].  Paired layouts only.
+// GU is read again only by the backward pass, so its stores carry the
+// non-temporal hint and leave the caches to A, W_fused and Y, which the down
+// projection reads next: with the hint against without (us, the whole block)
+// M=512 K=1536 N=8960 67.2 / 70.8, M=1024 109 / 111, M=8192 560 / 585;
+// M=4096 K=5120 N=13824 1247 / 1251, M=257 and below the same.  Hints on the
+// backward pass's loads of GU, its stores of dGU and the weight gradients' stores
+// moved nothing or lost (M=2048 K=1536 315 -> 325): dGU is read at once.
 struct PairMulKeep : PairMulEpilogue {
     uint16_t *GU;
 
@@ -362,7 +371,7 @@ struct PairMulKeep : PairMulEpilogue {
             Pairs::of<kFromAcc>(up, p, u0, u1);
             const uint32_t row = static_cast<uint32_t>(tm * 32 + Pairs::row(p)) * pitch;
             store4(ry, off, row, pack_bf16x2(silu(g0) * u0, silu(g1) * u1));
-            store8(rg, goff, 2u * row, pack_bf16x2(g0, u0), pack_bf16x2(g1, u1));
+            store8<true>(rg, goff, 2u * row, pack_bf16x2(g0, u0), pack_bf16x2(g1, u1));
         }
     }
     template <class S>
