@@ -818,7 +818,6 @@ static StorePairs store_pairs(uint16_t *C, int M, int cols) {
     return epi;
 }
 
-// D [M][cols] = dY [M][C] . W [C][cols], with a weight contracted by its rows.
 // One side of a backward pass: D [M][cols] = A . B over K.
 template <class Epi>
 struct GradProduct {

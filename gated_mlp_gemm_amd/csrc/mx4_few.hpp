@@ -63,7 +63,8 @@ struct Mx4Few {
         for (int o = 0; o < here * spitch; o += kThreads * 16)
             dma16(scales, all + o + wave * 1024, static_cast<uint32_t>(threadIdx.x) * 16u,
                   static_cast<uint32_t>(o));
-        rscale = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(all)) + i * spitch + q;
+        rscale = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(all)) + i * spitch +
+                 (q < spitch ? q : 0);
         tile_codes = 16 * pitch;
         tile_scales = 16 * spitch;
         // chunk c of row r lies in place c ^ (r / 4): the 16 lanes of one LDS cycle
@@ -102,7 +103,8 @@ struct Mx4Few {
         u32x4 w[R], x[MB][4];
         uint32_t scale[R];
     };
-    // (a lane past K reads zeros of codes and its own first scale, a number)
+    // (A lane past K reads zeros of codes and a scale of its own row: zeros times a number,
+    // or NaN in a row whose sum is NaN by that group already.)
     template <int SLOT, int... T>
     __device__ __forceinline__ void read(Block &f, int b, std::integer_sequence<int, T...>) const {
         const uint32_t at = rscale + static_cast<uint32_t>(b * 128 < ks ? b * 4 : 0);

@@ -275,6 +275,37 @@ def test_broken_groups_and_rows_stay_their_own(dev, M):
     assert bool(y[w == 0].isnan().all()) and torch.equal(y[w != 0], w[w != 0].sign() * float("inf"))
 
 
+# Weights of less than four groups a row, where a group's neighbours are other rows'.
+@pytest.mark.parametrize("M", [1, 6, 20, 40, 64, 100, 300])
+@pytest.mark.parametrize("K", [32, 64, 96, 160])
+def test_broken_groups_of_short_rows(dev, M, K):
+    N = 312
+    g = torch.Generator().manual_seed(M * K)
+    x = torch.randn(M, K, generator=g).to(BF).to(dev)
+    q, s = (t.to(dev) for t in codes_of(g, N, K))
+    hit = torch.arange(N, device=dev) % 3 == 1
+    clean = sw.swiglu_down_proj_mx4(x, q, s)
+    for group in range(K // 32):
+        s2 = s.clone()
+        s2[hit, group] = 255
+        y = sw.swiglu_down_proj_mx4(x, q, s2)
+        assert bool(y[:, hit].isnan().all()) and torch.equal(y[:, ~hit], clean[:, ~hit])
+
+
+# Rows too long for a compute unit's LDS beside the activations of the few-row kernel.
+@pytest.mark.parametrize("M,K", [(1, 1 << 18), (4, 1 << 17), (24, 96 * 1024), (64, 131072 + 32)])
+def test_very_long_rows(dev, M, K):
+    N = 24
+    g = torch.Generator(device=dev).manual_seed(M)
+    x = torch.randn(M, K, generator=g, device=dev).to(BF)
+    q = torch.randint(0, 256, (N, K // 2), generator=g, device=dev, dtype=torch.uint8)
+    s = torch.randint(115, 119, (N, K // 32), generator=g, device=dev).to(torch.uint8)
+    v = sw.swiglu_dequantize_mx4(q, s)
+    assert torch.equal(v.cpu().double(), values_of(q.cpu(), s.cpu()))
+    y = sw.swiglu_down_proj_mx4(x, q, s)
+    within(y, rounded(*product(x.cpu(), v.cpu().double())), f"M={M} K={K}")
+
+
 def test_other_streams_and_graphs(dev):
     K, N = 544, 1056
     g = torch.Generator().manual_seed(9)
