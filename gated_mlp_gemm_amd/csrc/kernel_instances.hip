@@ -67,44 +67,48 @@ hipError_t PersistentSequentialLaunch<S>::run(int grid, const void *A, const voi
 #if !defined(SWIGLU_INSTANCE)
 #error "compile once per group: -DSWIGLU_INSTANCE=<group>"
 #elif SWIGLU_INSTANCE == 0
-template struct TilesLaunch<ShapeWide, PairMulEpilogue, kTailQuarter>;
+template struct PairLaunch<ShapeWideDx, GateGradEpilogue, ShapeWideDw>;
 #elif SWIGLU_INSTANCE == 1
-template struct TilesLaunch<ShapeWide, StoreEpilogue, kTailQuarter>;
+template struct PairLaunch<ShapeWideDx, StorePairs, ShapeWideDw>;
 #elif SWIGLU_INSTANCE == 2
-template struct TilesLaunch<ShapeWide, PairMulEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeWide, PairMulEpilogue, kTailQuarter>;
 #elif SWIGLU_INSTANCE == 3
-template struct TilesLaunch<ShapeWide, PairMulEpilogue, kTailNone>;
+template struct TilesLaunch<ShapeWide, StoreEpilogue, kTailQuarter>;
 #elif SWIGLU_INSTANCE == 4
-template struct TilesLaunch<ShapeWide, StoreEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeWide, PairMulEpilogue, kTailSplit>;
 #elif SWIGLU_INSTANCE == 5
-template struct TilesLaunch<ShapeWide, StoreEpilogue, kTailNone>;
+template struct TilesLaunch<ShapeWide, PairMulEpilogue, kTailNone>;
 #elif SWIGLU_INSTANCE == 6
-template struct PersistentSequentialLaunch<ShapeSeqP>;
+template struct TilesLaunch<ShapeWide, StoreEpilogue, kTailSplit>;
 #elif SWIGLU_INSTANCE == 7
-template struct TilesLaunch<ShapeQuad, PairMulEpilogue, kTailNone>;
+template struct TilesLaunch<ShapeWide, StoreEpilogue, kTailNone>;
 #elif SWIGLU_INSTANCE == 8
-template struct TilesLaunch<ShapeQuad, PairMulEpilogue, kTailSplit>;
+template struct PersistentSequentialLaunch<ShapeSeqP>;
 #elif SWIGLU_INSTANCE == 9
-template struct TilesLaunch<ShapeQuad, StoreEpilogue, kTailNone>;
+template struct TilesLaunch<ShapeQuad, PairMulEpilogue, kTailNone>;
 #elif SWIGLU_INSTANCE == 10
-template struct TilesLaunch<ShapeQuad, StoreEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeQuad, PairMulEpilogue, kTailSplit>;
 #elif SWIGLU_INSTANCE == 11
-template struct TilesLaunch<ShapeSplitK, PairMulEpilogue, kTailReduceInKernel>;
+template struct TilesLaunch<ShapeQuad, StoreEpilogue, kTailNone>;
 #elif SWIGLU_INSTANCE == 12
+template struct TilesLaunch<ShapeQuad, StoreEpilogue, kTailSplit>;
+#elif SWIGLU_INSTANCE == 13
+template struct TilesLaunch<ShapeSplitK, PairMulEpilogue, kTailReduceInKernel>;
+#elif SWIGLU_INSTANCE == 14
 template struct TilesLaunch<ShapeWide8, PairMulEpilogueFp8, kTailQuarter>;
 template struct TilesLaunch<ShapeWide8, PairMulEpilogueFp8, kTailNone>;
 template struct TilesLaunch<ShapeWide8, PairMulEpilogueFp8, kTailSplit>;
-#elif SWIGLU_INSTANCE == 13
+#elif SWIGLU_INSTANCE == 15
 template struct TilesLaunch<ShapeQuad8, PairMulEpilogueFp8, kTailNone>;
 template struct TilesLaunch<ShapeQuad8, PairMulEpilogueFp8, kTailSplit>;
 template struct TilesLaunch<ShapeSmall8, PairMulEpilogueFp8, kTailNone>;
 template struct TilesLaunch<ShapeSmall8, PairMulEpilogueFp8, kTailSplit>;
-#elif SWIGLU_INSTANCE == 14
+#elif SWIGLU_INSTANCE == 16
 template struct TilesLaunch<ShapeSmall, PairMulEpilogue, kTailNone>;
 template struct TilesLaunch<ShapeSmall, PairMulEpilogue, kTailSplit>;
 template struct TilesLaunch<ShapeSmall, StoreEpilogue, kTailNone>;
 template struct TilesLaunch<ShapeSmall, StoreEpilogue, kTailSplit>;
-#elif SWIGLU_INSTANCE == 15
+#elif SWIGLU_INSTANCE == 17
 template struct SequentialLaunch<ShapeSmall>;
 template struct SequentialLaunch<ShapeSmall8>;
 template struct SequentialLaunch<ShapeSeq8>;
@@ -117,43 +121,43 @@ template struct ReduceLaunch<ShapeSmall, StoreEpilogue>;
 template struct ReduceLaunch<ShapeWide8, PairMulEpilogueFp8>;
 template struct ReduceLaunch<ShapeQuad8, PairMulEpilogueFp8>;
 template struct ReduceLaunch<ShapeSmall8, PairMulEpilogueFp8>;
-#elif SWIGLU_INSTANCE == 16
-template struct TilesLaunch<ShapeWide, PairMulLora, kTailQuarter>;
-#elif SWIGLU_INSTANCE == 17
-template struct TilesLaunch<ShapeWide, StoreLora, kTailQuarter>;
 #elif SWIGLU_INSTANCE == 18
-template struct TilesLaunch<ShapeWide, PairMulLora, kTailSplit>;
+template struct TilesLaunch<ShapeWide, PairMulLora, kTailQuarter>;
 #elif SWIGLU_INSTANCE == 19
-template struct TilesLaunch<ShapeWide, StoreLora, kTailSplit>;
+template struct TilesLaunch<ShapeWide, StoreLora, kTailQuarter>;
 #elif SWIGLU_INSTANCE == 20
+template struct TilesLaunch<ShapeWide, PairMulLora, kTailSplit>;
+#elif SWIGLU_INSTANCE == 21
+template struct TilesLaunch<ShapeWide, StoreLora, kTailSplit>;
+#elif SWIGLU_INSTANCE == 22
 template struct TilesLaunch<ShapeQuad, PairMulLora, kTailSplit>;
 template struct TilesLaunch<ShapeQuad, StoreLora, kTailSplit>;
-#elif SWIGLU_INSTANCE == 21
+#elif SWIGLU_INSTANCE == 23
 template struct TilesLaunch<ShapeSplitK, PairMulLora, kTailReduceInKernel>;
 template struct TilesLaunch<ShapeSmallLora, PairMulLora, kTailSplit>;
 template struct TilesLaunch<ShapeSmallLora, StoreLora, kTailSplit>;
-#elif SWIGLU_INSTANCE == 22
+#elif SWIGLU_INSTANCE == 24
 template struct TilesLaunch<ShapeThinLora, PairMulLora, kTailSplit>;
 template struct TilesLaunch<ShapeThinLora, StoreLora, kTailSplit>;
 template struct ReduceLaunch<ShapeThinLora, PairMulEpilogue>;
 template struct ReduceLaunch<ShapeThinLora, StoreEpilogue>;
 template struct ReduceLaunch<ShapeSmallLora, PairMulEpilogue>;
 template struct ReduceLaunch<ShapeSmallLora, StoreEpilogue>;
-#elif SWIGLU_INSTANCE == 23
-template struct TilesLaunch<ShapeWideDx, GateGradEpilogue, kTailSplit>;
-#elif SWIGLU_INSTANCE == 24
-template struct TilesLaunch<ShapeWideDx, StorePairs, kTailSplit>;
 #elif SWIGLU_INSTANCE == 25
-template struct TilesLaunch<ShapeWideDw, WeightGradEpilogue, kTailSplit>;
+template struct TilesLaunch<ShapeWideDx, GateGradEpilogue, kTailSplit>;
 #elif SWIGLU_INSTANCE == 26
-template struct TilesLaunch<ShapeWide, PairMulKeep, kTailSplit>;
+template struct TilesLaunch<ShapeWideDx, StorePairs, kTailSplit>;
 #elif SWIGLU_INSTANCE == 27
+template struct TilesLaunch<ShapeWideDw, WeightGradEpilogue, kTailSplit>;
+#elif SWIGLU_INSTANCE == 28
+template struct TilesLaunch<ShapeWide, PairMulKeep, kTailSplit>;
+#elif SWIGLU_INSTANCE == 29
 template struct TilesLaunch<ShapeQuadDx, GateGradEpilogue, kTailSplit>;
 template struct TilesLaunch<ShapeQuadDx, StorePairs, kTailSplit>;
-#elif SWIGLU_INSTANCE == 28
+#elif SWIGLU_INSTANCE == 30
 template struct TilesLaunch<ShapeQuadDw, WeightGradEpilogue, kTailSplit>;
 template struct TilesLaunch<ShapeQuad, PairMulKeep, kTailSplit>;
-#elif SWIGLU_INSTANCE == 29
+#elif SWIGLU_INSTANCE == 31
 template struct TilesLaunch<ShapeSmallDx, GateGradEpilogue, kTailSplit>;
 template struct TilesLaunch<ShapeSmallDx, StorePairs, kTailSplit>;
 template struct TilesLaunch<ShapeSmallLora, PairMulKeep, kTailSplit>;
@@ -168,14 +172,14 @@ template struct ReduceLaunch<ShapeQuad, PairMulKeep>;
 template struct ReduceLaunch<ShapeSmallDx, GateGradEpilogue>;
 template struct ReduceLaunch<ShapeSmallDx, StorePairs>;
 template struct ReduceLaunch<ShapeSmallLora, PairMulKeep>;
-#elif SWIGLU_INSTANCE == 30
-template struct TilesLaunch<ShapeWideMx4, PairMulPairs, kTailSplit>;
-#elif SWIGLU_INSTANCE == 31
-template struct TilesLaunch<ShapeWideMx4, StorePairs, kTailSplit>;
 #elif SWIGLU_INSTANCE == 32
+template struct TilesLaunch<ShapeWideMx4, PairMulPairs, kTailSplit>;
+#elif SWIGLU_INSTANCE == 33
+template struct TilesLaunch<ShapeWideMx4, StorePairs, kTailSplit>;
+#elif SWIGLU_INSTANCE == 34
 template struct TilesLaunch<ShapeQuadMx4, PairMulPairs, kTailSplit>;
 template struct TilesLaunch<ShapeQuadMx4, StorePairs, kTailSplit>;
-#elif SWIGLU_INSTANCE == 33
+#elif SWIGLU_INSTANCE == 35
 template struct TilesLaunch<ShapeSmallMx4, PairMulPairs, kTailSplit>;
 template struct TilesLaunch<ShapeSmallMx4, StorePairs, kTailSplit>;
 template struct ReduceLaunch<ShapeWideMx4, PairMulPairs>;
@@ -184,14 +188,10 @@ template struct ReduceLaunch<ShapeQuadMx4, PairMulPairs>;
 template struct ReduceLaunch<ShapeQuadMx4, StorePairs>;
 template struct ReduceLaunch<ShapeSmallMx4, PairMulPairs>;
 template struct ReduceLaunch<ShapeSmallMx4, StorePairs>;
-#elif SWIGLU_INSTANCE == 34
-template struct TilesLaunch<ShapeWideDx, GateGradEpilogue, kTailQuarter>;
-#elif SWIGLU_INSTANCE == 35
-template struct TilesLaunch<ShapeWide, PairMulKeep, kTailQuarter>;
 #elif SWIGLU_INSTANCE == 36
-template struct PairLaunch<ShapeWideDx, GateGradEpilogue, ShapeWideDw>;
+template struct TilesLaunch<ShapeWideDx, GateGradEpilogue, kTailQuarter>;
 #elif SWIGLU_INSTANCE == 37
-template struct PairLaunch<ShapeWideDx, StorePairs, ShapeWideDw>;
+template struct TilesLaunch<ShapeWide, PairMulKeep, kTailQuarter>;
 #else
 #error "SWIGLU_INSTANCE is past the end of the instance list"
 #endif

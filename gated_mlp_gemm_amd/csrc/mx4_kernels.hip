@@ -30,7 +30,8 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
 
 // S from the largest magnitude's exponent, so that it lies in [4, 8) of 2^(S - 127):
 // what is above 6 becomes 6.  (Groups below 2^-124 keep S = 0, and zeros.)  Four lanes
-// have a group, 8 numbers each: 16 bytes in, 4 bytes out a lane.
+// have a group, 8 numbers each: 16 bytes in, 4 bytes out a lane.  Bound by its bytes:
+// 37889 x 3616 66 us, 5.2 TB/s; 9728 x 896 5.6 us.
 __global__ __launch_bounds__(256) void quantize_mx4_kernel(const uint16_t *__restrict__ x,
                                                            uint32_t *__restrict__ q,
                                                            uint8_t *__restrict__ s,

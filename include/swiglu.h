@@ -494,8 +494,8 @@ int swiglu_gated_mlp_lora(const uint16_t *X, const uint16_t *W_fused, const uint
  * Preconditions: those of the calls without "mx4", and the contraction (K; N of the
  * down projection) a multiple of 32; matrices and codes 16-byte aligned, scales 4-byte
  * (at any address in the two calls above).  Up to 64 rows need no workspace (but for
- * contractions of many tens of thousands).  workspace: optional, as for swiglu_fused_gemm (size from
- * swiglu_workspace_size(M, N, K, -1, ...)).
+ * contractions of many tens of thousands).  workspace: optional, as for
+ * swiglu_fused_gemm (size from swiglu_workspace_size(M, N, K, -1, ...)).
  */
 int swiglu_quantize_mx4(const uint16_t *X, uint8_t *Q, uint8_t *S, int64_t rows, int64_t K,
                         void *stream);
