@@ -226,7 +226,7 @@ __device__ __forceinline__ void shrink_body(const ShrinkArgs &x, char *smem,
     xp.init(KMajor{x.X, x.M, 1, 0, 0, 0}, m0, x.K);
     for (int job = y; job < items * splits; job += G) {
         const int item = job / splits, split = job % splits;
-        const int kb = split * nk / splits, len = (split + 1) * nk / splits - kb;
+        const int kb = piece_begin(split, nk, splits), len = piece_begin(split + 1, nk, splits) - kb;
         AdapterPanel ap;
         ap.init(x, list, cols, item * S::BM, total);
         Pipeline<S> pl;

@@ -90,8 +90,8 @@ __device__ __forceinline__ int pair_items(char *smem, const KMajor &A, const KMa
     while (item < n) {
         const int j = item - sch.dp;
         const int piece = j % sch.pieces;
-        const int kb = piece * nk / sch.pieces;
-        const int ke = (piece + 1) * nk / sch.pieces;
+        const int kb = piece_begin(piece, nk, sch.pieces);
+        const int ke = piece_begin(piece + 1, nk, sch.pieces);
         int tm, tn;
         tile_coords(sch.dp + j / sch.pieces, sch.tiles_m, sch.tiles_n, sch.group_m, tm, tn);
         typename S::Acc acc[S::TM][S::TN];

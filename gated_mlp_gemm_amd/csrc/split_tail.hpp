@@ -39,6 +39,7 @@
 
 #include "arrivals.hpp"
 #include "gemm_core.hpp"
+#include "pieces.hpp"
 
 namespace swiglu {
 

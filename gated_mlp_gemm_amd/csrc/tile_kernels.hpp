@@ -822,8 +822,8 @@ __device__ __forceinline__ bool gemm_tiles_body(char *smem, const KMajor &Ak, co
         for (int j = b; j < np; j += grid) {
             const int i = j / sch.pieces;
             const int piece = j % sch.pieces;
-            const int kb = piece * sch.nk / sch.pieces;
-            const int ke = (piece + 1) * sch.nk / sch.pieces;
+            const int kb = piece_begin(piece, sch.nk, sch.pieces);
+            const int ke = piece_begin(piece + 1, sch.nk, sch.pieces);
             Arrival meeting{};
             if (threadIdx.x == 0) meeting.announce(sch.arrivals + i, sch.tag);
             int tm, tn;
@@ -873,8 +873,8 @@ __device__ __forceinline__ bool gemm_tiles_body(char *smem, const KMajor &Ak, co
         for (int j = b; j < np; j += grid) {
             const int t = sch.dp + j / sch.pieces;
             const int piece = j % sch.pieces;
-            const int kb = piece * sch.nk / sch.pieces;
-            const int ke = (piece + 1) * sch.nk / sch.pieces;
+            const int kb = piece_begin(piece, sch.nk, sch.pieces);
+            const int ke = piece_begin(piece + 1, sch.nk, sch.pieces);
             int tm, tn;
             tile_coords(t, sch.tiles_m, sch.tiles_n, sch.group_m, tm, tn);
             typename S::Acc acc[S::TM][S::TN];
