@@ -7,7 +7,8 @@ fails loudly if it is not built (``python -m gated_mlp_gemm_amd.build``).
 """
 from .swiglu import (  # noqa: F401
     SWIGLU_AUTO, SWIGLU_VARIANT_I, SWIGLU_VARIANT_S, SwigluError, SwigluLora, load_library,
-    make_lora_workspace, make_workspace, swiglu_dequantize_mx4, swiglu_describe_launch,
+    make_lora_workspace, make_workspace, swiglu_dequantize_mx4, swiglu_describe_backward,
+    swiglu_describe_launch,
     swiglu_down_proj, swiglu_down_proj_backward, swiglu_down_proj_lora, swiglu_down_proj_mx4,
     swiglu_fp8_scale_exp, swiglu_fused_gemm, swiglu_fused_gemm_backward, swiglu_fused_gemm_fp8,
     swiglu_fused_gemm_lora, swiglu_fused_gemm_mx4, swiglu_fused_gemm_noalloc,

@@ -294,6 +294,26 @@ int check_train_shape(int64_t M, int64_t N, int64_t K) {
         return fail(SWIGLU_ERR_SHAPE, "tile grid too large");
     return SWIGLU_OK;
 }
+int check_down_backward_shape(int64_t M, int64_t N, int64_t D) {
+    int st = check_down_shape(M, N, D);
+    if (st != SWIGLU_OK) return st;
+    if (D < 8) return fail(SWIGLU_ERR_SHAPE, "D=%lld must be >= 8", (long long)D);
+    if (M > kMaxTrainM || D > kMaxK || swiglu::max_tiles(M, N) > 2147483647 ||
+        swiglu::max_tiles(D, N) > 2147483647)
+        return fail(SWIGLU_ERR_SHAPE, "size beyond limits (M<=2^30, D<=2^21, tile grids)");
+    return SWIGLU_OK;
+}
+int check_stage_backward_shape(int64_t M, int64_t N, int64_t K) {
+    int st = check_train_shape(M, N, K);
+    if (st != SWIGLU_OK) return st;
+    if (N < 8) return fail(SWIGLU_ERR_SHAPE, "N=%lld must be >= 8", (long long)N);
+    return SWIGLU_OK;
+}
+int check_block_backward_shape(int64_t M, int64_t N, int64_t K) {
+    int st = check_train_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_down_shape(M, N, K);
+    return st;
+}
 int check_grad_type(int grad_type) {
     if (grad_type != SWIGLU_F32 && grad_type != SWIGLU_BF16)
         return fail(SWIGLU_ERR_UNSUPPORTED, "unknown gradient type %d", grad_type);
@@ -428,6 +448,30 @@ int swiglu_describe_launch(int64_t M, int64_t N, int64_t K, int variant,
         swiglu::describe_gemm((int)M, (int)N, (int)K, ws, "StoreEpilogue", g, sizeof g);
         std::snprintf(buf, buf_bytes, "2 x %s + silu_mul_kernel", g);
     }
+    return ok();
+}
+
+int swiglu_describe_backward(int64_t M, int64_t N, int64_t K, int call, int grad_type, int add,
+                             uint64_t workspace_bytes, char *buf, uint64_t buf_bytes) {
+    if (!buf || buf_bytes == 0) return fail(SWIGLU_ERR_NULL, "buf is required");
+    buf[0] = '\0';
+    if (call < SWIGLU_DOWN_PROJ_BACKWARD || call > SWIGLU_GATED_MLP_BACKWARD)
+        return fail(SWIGLU_ERR_UNSUPPORTED, "unknown backward call %d", call);
+    int st = check_grad_type(grad_type);
+    if (st == SWIGLU_OK)
+        st = call == SWIGLU_DOWN_PROJ_BACKWARD    ? check_down_backward_shape(M, N, K)
+             : call == SWIGLU_FUSED_GEMM_BACKWARD ? check_stage_backward_shape(M, N, K)
+                                                  : check_block_backward_shape(M, N, K);
+    if (st != SWIGLU_OK) return st;
+    int cus = 0;
+    st = check_device(&cus);
+    if (st != SWIGLU_OK) return st;
+    // only the size of the workspace matters for the plan
+    const swiglu::GemmWorkspace ws =
+        make_ws(workspace_bytes ? reinterpret_cast<void *>(uintptr_t{256}) : nullptr,
+                workspace_bytes, cus);
+    swiglu::describe_backward(static_cast<swiglu::BackwardCall>(call), grad_type == SWIGLU_F32, add != 0,
+                              (int)M, (int)N, (int)K, ws, buf, buf_bytes);
     return ok();
 }
 
@@ -1012,12 +1056,8 @@ int swiglu_down_proj_backward(const uint16_t *dOut, const uint16_t *H, const uin
                               int64_t M, int64_t N, int64_t D, void *workspace,
                               uint64_t workspace_bytes, void *stream) {
     int st = check_grad_type(grad_type);
-    if (st == SWIGLU_OK) st = check_down_shape(M, N, D);
+    if (st == SWIGLU_OK) st = check_down_backward_shape(M, N, D);
     if (st != SWIGLU_OK) return st;
-    if (D < 8) return fail(SWIGLU_ERR_SHAPE, "D=%lld must be >= 8", (long long)D);
-    if (M > kMaxTrainM || D > kMaxK || swiglu::max_tiles(M, N) > 2147483647 ||
-        swiglu::max_tiles(D, N) > 2147483647)
-        return fail(SWIGLU_ERR_SHAPE, "size beyond limits (M<=2^30, D<=2^21, tile grids)");
     if (!dH && !dW3t) return fail(SWIGLU_ERR_NULL, "dH or dW3t is required");
     if (dW3t_add && !dW3t) return fail(SWIGLU_ERR_NULL, "dW3t_add without dW3t");
     const bool none = M == 0;
@@ -1048,9 +1088,8 @@ int swiglu_fused_gemm_backward(const uint16_t *dH, const uint16_t *A, const uint
                                int64_t K, void *workspace, uint64_t workspace_bytes,
                                void *stream) {
     int st = check_grad_type(grad_type);
-    if (st == SWIGLU_OK) st = check_train_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_stage_backward_shape(M, N, K);
     if (st != SWIGLU_OK) return st;
-    if (N < 8) return fail(SWIGLU_ERR_SHAPE, "N=%lld must be >= 8", (long long)N);
     if (dW_fused_add && !dW_fused) return fail(SWIGLU_ERR_NULL, "dW_fused_add without dW_fused");
     const bool none = M == 0;
     const int64_t weight = 2 * N * K;
@@ -1088,8 +1127,7 @@ int swiglu_gated_mlp_backward(const uint16_t *dOut, const uint16_t *A, const uin
                               int grad_type, int64_t M, int64_t N, int64_t K, void *workspace,
                               uint64_t workspace_bytes, void *stream) {
     int st = check_grad_type(grad_type);
-    if (st == SWIGLU_OK) st = check_train_shape(M, N, K);
-    if (st == SWIGLU_OK) st = check_down_shape(M, N, K);
+    if (st == SWIGLU_OK) st = check_block_backward_shape(M, N, K);
     if (st != SWIGLU_OK) return st;
     if (dW_fused_add && !dW_fused) return fail(SWIGLU_ERR_NULL, "dW_fused_add without dW_fused");
     if (dW3t_add && !dW3t) return fail(SWIGLU_ERR_NULL, "dW3t_add without dW3t");

@@ -766,16 +766,19 @@ static hipError_t launch_split_gemm(const KMajor &A, KMajor B, int M, int cols, 
     return ReduceLaunch<S, Epi>::run(sch.split_tiles * kWavesPerTile, epi, sch, stream);
 }
 // The 256x256 tiles or the 128x128 ones, whichever the model predicts faster.
+template <class Wide, class Quad, bool kQuarters>
+static bool grad_quad_faster(int M, int cols, int K, double extra, const GemmWorkspace &ws) {
+    if (ws.tile != 0) return ws.tile == 128;
+    double wide = 0.0, quad = 0.0;
+    make_grad_schedule<Wide, kQuarters>(M, cols, K, extra, ws, &wide);
+    make_grad_schedule<Quad, false>(M, cols, K, extra, ws, &quad);
+    return quad < wide;
+}
 template <class Wide, class Quad, class Epi, bool kQuarters = false>
 static hipError_t launch_wide_or_quad(const KMajor &A, const KMajor &B, int M, int cols, int K,
                                       const Epi &epi, double extra, const GemmWorkspace &ws,
                                       hipStream_t stream) {
-    double wide = 0.0, quad = 1.0;
-    if (ws.tile == 0) {
-        make_grad_schedule<Wide, kQuarters>(M, cols, K, extra, ws, &wide);
-        make_grad_schedule<Quad, false>(M, cols, K, extra, ws, &quad);
-    }
-    if (ws.tile == 128 || (ws.tile == 0 && quad < wide))
+    if (grad_quad_faster<Wide, Quad, kQuarters>(M, cols, K, extra, ws))
         return launch_split_gemm<Quad>(A, B, M, cols, K, epi, ws, stream, extra);
     return launch_split_gemm<Wide, Epi, kQuarters>(A, B, M, cols, K, epi, ws, stream, extra);
 }
@@ -857,19 +860,25 @@ static GradProduct<WeightGradEpilogue> weight_product(const uint16_t *dY, const 
             cols, M, WeightGradEpilogue{dW, add, rows, cols, f32 ? 1 : 0}, extra};
 }
 
+// (only dGU's epilogue, which moves the most, runs quarter-size tails)
+template <class Epi>
+constexpr bool kDxQuarters = std::is_same<Epi, GateGradEpilogue>::value;
 template <class Epi>
 static hipError_t launch_dx(const GradProduct<Epi> &p, const GemmWorkspace &ws, hipStream_t stream) {
     if (p.M <= 128) return launch_split_gemm<ShapeSmallDx>(p.A, p.B, p.M, p.cols, p.K, p.epi, ws, stream);
-    return launch_wide_or_quad<ShapeWideDx, ShapeQuadDx, Epi,
-                               std::is_same<Epi, GateGradEpilogue>::value>(
+    return launch_wide_or_quad<ShapeWideDx, ShapeQuadDx, Epi, kDxQuarters<Epi>>(
         p.A, p.B, p.M, p.cols, p.K, p.epi, p.extra, ws, stream);
 }
-static hipError_t launch_dw(const GradProduct<WeightGradEpilogue> &p, const GemmWorkspace &ws_,
-                            hipStream_t stream) {
+// (no K step to split: the tiles store zeros (+ add))
+static GemmWorkspace dw_workspace(const GradProduct<WeightGradEpilogue> &p, const GemmWorkspace &ws_) {
     GemmWorkspace ws = ws_;
-    if (p.K == 0) ws.tail = kTailWhole;   // no K step to split: the tiles store zeros (+ add)
-    return launch_wide_or_quad<ShapeWideDw, ShapeQuadDw>(p.A, p.B, p.M, p.cols, p.K, p.epi, p.extra, ws,
-                                                         stream);
+    if (p.K == 0) ws.tail = kTailWhole;
+    return ws;
+}
+static hipError_t launch_dw(const GradProduct<WeightGradEpilogue> &p, const GemmWorkspace &ws,
+                            hipStream_t stream) {
+    return launch_wide_or_quad<ShapeWideDw, ShapeQuadDw>(p.A, p.B, p.M, p.cols, p.K, p.epi, p.extra,
+                                                         dw_workspace(p, ws), stream);
 }
 
 // Tiles of S over a product, all whole, or all split where one would take more than half
@@ -905,8 +914,8 @@ static double product_us(const GradProduct<Epi> &p, int cus) {
     return T * (GradCost<S>::kRound + 0.5 * p.extra + cdiv(p.K, S::BK) * GradCost<S>::step(cus, cus));
 }
 
-// Both products in one launch, if that is predicted to be faster than `apart`;
-// hipErrorNotSupported, nothing launched, if it is not or there is no workspace for it.
+// Both products in one launch: whether that is predicted to be faster than `apart` and there
+// is a workspace for it, and then how.
 // Measured one after the other and together (us; dH and dW3t, dA and dW_fused):
 //   M=512 K=3584 N=18944 154 / 130, 302 / 293;   M=2048 K=1536 N=8960 105 / 87, 202 / 199;
 //   M=2048 K=5120 N=13824 434 / 403, 1023 / 814; M=8192 K=5120 N=13824 1528 / 1526,
@@ -914,36 +923,49 @@ static double product_us(const GradProduct<Epi> &p, int cus) {
 //   better, and M=33 K=896 N=4872 (with 128x64 tiles beside the weight's) 13 / 22: so
 //   not for few rows, nor where a compute unit's share is short.
 constexpr double kPairUs = 30.0;
+constexpr int64_t kPairSlot = ShapeWideDx::BM * ShapeWideDx::BN;   // floats of a partial
+struct PairPlan {
+    Schedule sx, sw;
+    int slots;       // for partials; the counts are in the one behind them
+    bool w_first;
+};
 template <class EX>
-static hipError_t launch_pair(const GradProduct<EX> &x, const GradProduct<WeightGradEpilogue> &w,
-                              const GemmWorkspace &ws, double apart, hipStream_t stream) {
+static bool plan_pair(const GradProduct<EX> &x, const GradProduct<WeightGradEpilogue> &w,
+                      const GemmWorkspace &ws, double apart, PairPlan &plan) {
     using SX = ShapeWideDx;
     using SW = ShapeWideDw;
     if (ws.base == nullptr || ws.bytes < workspace_bytes_for(ws.cus) || ws.cus < 8 || ws.cus % 8 != 0 ||
         ws.tile != 0 || ws.tail != kTailAuto || w.K == 0)
-        return hipErrorNotSupported;
+        return false;
     const double fair = (product_us<SX>(x, ws.cus) + product_us<SW>(w, ws.cus)) / ws.cus;
-    if (fair < kPairUs) return hipErrorNotSupported;
-    // the partials' slots but one, which holds the counts
-    const int slots = ws.cus - 1;
-    constexpr int64_t kSlot = SX::BM * SX::BN;
+    if (fair < kPairUs) return false;
+    plan.slots = ws.cus - 1;
     float *partials = reinterpret_cast<float *>(ws.base);
-    const Schedule sx = pair_schedule<SX>(x, fair, slots, ws.cus, partials);
-    const int used = sx.split_tiles * sx.pieces;
-    const Schedule sw = pair_schedule<SW>(w, fair, slots - used, ws.cus, partials + used * kSlot);
-    const int partial_slots = used + sw.split_tiles * sw.pieces;
+    plan.sx = pair_schedule<SX>(x, fair, plan.slots, ws.cus, partials);
+    const int used = plan.sx.split_tiles * plan.sx.pieces;
+    plan.sw = pair_schedule<SW>(w, fair, plan.slots - used, ws.cus, partials + used * kPairSlot);
+    const int partial_slots = used + plan.sw.split_tiles * plan.sw.pieces;
     auto item_us = [&](const Schedule &s, double extra) {
         return GradCost<SX>::kRound + 0.5 * extra +
                (s.pieces ? cdiv(s.nk, s.pieces) : s.nk) * GradCost<SX>::step(ws.cus, ws.cus);
     };
-    const double ix = item_us(sx, x.extra), iw = item_us(sw, w.extra);
-    const double together = fair + 0.5 * (ix < iw ? ix : iw) +
-                            (partial_slots ? kReduceUs + partial_slots * kSlot * 8.0 / kPartialBytesPerUs : 0.0);
-    const int64_t items = static_cast<int64_t>(sx.dp) + sw.dp + partial_slots;
-    if (together >= apart || items / 8 >= (1 << kArrivalBits) - 8) return hipErrorNotSupported;
-    // (the longer items first: the others even the end out)
-    const PairCounts counts{reinterpret_cast<uint64_t *>(partials + slots * kSlot), ws.tag,
-                            iw >= ix ? 1 : 0};
+    const double ix = item_us(plan.sx, x.extra), iw = item_us(plan.sw, w.extra);
+    plan.w_first = iw >= ix;   // (the longer items first: the others even the end out)
+    const double together =
+        fair + 0.5 * (ix < iw ? ix : iw) +
+        (partial_slots ? kReduceUs + partial_slots * kPairSlot * 8.0 / kPartialBytesPerUs : 0.0);
+    const int64_t items = static_cast<int64_t>(plan.sx.dp) + plan.sw.dp + partial_slots;
+    return together < apart && items / 8 < (1 << kArrivalBits) - 8;
+}
+template <class EX>
+static hipError_t launch_pair(const GradProduct<EX> &x, const GradProduct<WeightGradEpilogue> &w,
+                              const PairPlan &plan, const GemmWorkspace &ws, hipStream_t stream) {
+    using SX = ShapeWideDx;
+    using SW = ShapeWideDw;
+    const Schedule &sx = plan.sx, &sw = plan.sw;
+    float *partials = reinterpret_cast<float *>(ws.base);
+    const PairCounts counts{reinterpret_cast<uint64_t *>(partials + plan.slots * kPairSlot), ws.tag,
+                            plan.w_first ? 1 : 0};
     hipError_t e = PairLaunch<SX, EX, SW>::run(ws.cus, x.A, x.B, x.M, x.K, x.epi, sx, w.A, w.B, w.M, w.K,
                                                w.epi, sw, counts, stream);
     if (e == hipSuccess && sx.pieces)
@@ -960,18 +982,21 @@ static double apart_us(const GradProduct<Epi> &p, const GemmWorkspace &ws) {
     make_grad_schedule<Quad, false>(p.M, p.cols, p.K, p.extra, ws, &quad);
     return wide < quad ? wide : quad;
 }
+template <class EX>
+static bool plan_grads(const GradProduct<EX> &x, const GradProduct<WeightGradEpilogue> &w,
+                       const GemmWorkspace &ws, PairPlan &plan) {
+    constexpr double kLaunchUs = 2.0;   // of the second launch
+    if (x.M <= 128) return false;
+    const double apart = apart_us<ShapeWideDx, ShapeQuadDx, kDxQuarters<EX>>(x, ws) +
+                         apart_us<ShapeWideDw, ShapeQuadDw, false>(w, ws) + kLaunchUs;
+    return plan_pair(x, w, ws, apart, plan);
+}
 // The gradients by an activation and by a weight.
 template <class EX>
 static hipError_t launch_grads(const GradProduct<EX> &x, const GradProduct<WeightGradEpilogue> &w,
                                const GemmWorkspace &ws, hipStream_t stream) {
-    constexpr double kLaunchUs = 2.0;   // of the second launch
-    if (x.M > 128) {
-        const double apart =
-            apart_us<ShapeWideDx, ShapeQuadDx, std::is_same<EX, GateGradEpilogue>::value>(x, ws) +
-            apart_us<ShapeWideDw, ShapeQuadDw, false>(w, ws) + kLaunchUs;
-        const hipError_t e = launch_pair(x, w, ws, apart, stream);
-        if (e != hipErrorNotSupported) return e;
-    }
+    PairPlan plan;
+    if (plan_grads(x, w, ws, plan)) return launch_pair(x, w, plan, ws, stream);
     const hipError_t e = launch_dx(x, ws, stream);
     return e != hipSuccess ? e : launch_dw(w, ws, stream);
 }
@@ -999,6 +1024,70 @@ hipError_t launch_stage_backward(const uint16_t *dGU, const uint16_t *A, const u
                                  uint16_t *dA, void *dW, const void *add, bool f32, int M, int N,
                                  int K, const GemmWorkspace &ws, hipStream_t stream) {
     return launch_down_backward(dGU, A, W_fused, dA, dW, add, f32, M, K, 2 * N, ws, stream);
+}
+
+// What the backward calls with all their gradients launch, as text.
+template <class S, bool kQuarters, class Epi>
+static int describe_product(const GradProduct<Epi> &p, const char *epi, const GemmWorkspace &ws,
+                            char *buf, size_t n) {
+    return describe<S>("gemm_tiles_kernel", epi,
+                       make_grad_schedule<S, kQuarters>(p.M, p.cols, p.K, p.extra, ws), ws.cus, buf, n);
+}
+static void describe_items(const Schedule &s, char *buf, size_t n) {
+    if (s.pieces) std::snprintf(buf, n, "%d tiles split %d ways along K", s.split_tiles, s.pieces);
+    else std::snprintf(buf, n, "%d whole tiles", s.dp);
+}
+template <class EX>
+static void describe_grads(const GradProduct<EX> &x, const GradProduct<WeightGradEpilogue> &w,
+                           const char *epi, const GemmWorkspace &ws, char *buf, size_t n) {
+    char tx[192], tw[192];
+    PairPlan plan;
+    if (x.M > 0 && plan_grads(x, w, ws, plan)) {
+        describe_items(plan.sx, tx, sizeof tx);
+        describe_items(plan.sw, tw, sizeof tw);
+        std::snprintf(buf, n, "gemm_pair_kernel<%s> (%s of the activation's gradient, %s of the"
+                      " weight's; %d workgroups)%s%s",
+                      epi, tx, tw, ws.cus, plan.sx.pieces ? " + split_reduce_kernel" : "",
+                      plan.sw.pieces ? " + split_reduce_kernel" : "");
+        return;
+    }
+    const GemmWorkspace dws = dw_workspace(w, ws);
+    if (grad_quad_faster<ShapeWideDw, ShapeQuadDw, false>(w.M, w.cols, w.K, w.extra, dws))
+        describe_product<ShapeQuadDw, false>(w, "WeightGradEpilogue", dws, tw, sizeof tw);
+    else
+        describe_product<ShapeWideDw, false>(w, "WeightGradEpilogue", dws, tw, sizeof tw);
+    if (x.M == 0) {
+        std::snprintf(buf, n, "%s", tw);
+        return;
+    }
+    constexpr bool kQ = kDxQuarters<EX>;
+    if (x.M <= 128)
+        describe_product<ShapeSmallDx, false>(x, epi, ws, tx, sizeof tx);
+    else if (grad_quad_faster<ShapeWideDx, ShapeQuadDx, kQ>(x.M, x.cols, x.K, x.extra, ws))
+        describe_product<ShapeQuadDx, false>(x, epi, ws, tx, sizeof tx);
+    else
+        describe_product<ShapeWideDx, kQ>(x, epi, ws, tx, sizeof tx);
+    std::snprintf(buf, n, "%s + %s", tx, tw);
+}
+void describe_backward(BackwardCall call, bool f32, bool add, int M, int N, int K,
+                       const GemmWorkspace &ws, char *buf, size_t n) {
+    const void *added = add ? &ws : nullptr;   // (only whether there is one matters)
+    char first[512], second[512];
+    const auto by_h = weight_product(nullptr, nullptr, nullptr, added, f32, M, K, N);
+    if (call == kDownBackward) {
+        describe_grads(input_product(nullptr, nullptr, nullptr, M, N, K), by_h, "StorePairs", ws, buf, n);
+        return;
+    }
+    if (call == kBlockBackward)
+        describe_grads(gate_product(nullptr, nullptr, nullptr, nullptr, M, N, K), by_h,
+                       "GateGradEpilogue", ws, first, sizeof first);
+    else
+        std::snprintf(first, sizeof first, "gate_grad_kernel");
+    describe_grads(input_product(nullptr, nullptr, nullptr, M, K, 2 * N),
+                   weight_product(nullptr, nullptr, nullptr, added, f32, M, 2 * N, K), "StorePairs", ws,
+                   second, sizeof second);
+    if (call == kStageBackward && M == 0) std::snprintf(buf, n, "%s", second);
+    else std::snprintf(buf, n, "%s, then %s", first, second);
 }
 
 // ---------------------------------------------------------------------------

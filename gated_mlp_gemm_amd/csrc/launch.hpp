@@ -79,6 +79,11 @@ hipError_t launch_gate_backward(const uint16_t *dOut, const uint16_t *H, const u
 hipError_t launch_stage_backward(const uint16_t *dGU, const uint16_t *A, const uint16_t *W_fused,
                                  uint16_t *dA, void *dW, const void *add, bool f32, int M, int N,
                                  int K, const GemmWorkspace &ws, hipStream_t stream);
+// What a backward call with all its gradients launches, as text (snprintf semantics); add:
+// the weights' gradients are added to sums.
+enum BackwardCall { kDownBackward = 0, kStageBackward = 1, kBlockBackward = 2 };
+void describe_backward(BackwardCall call, bool f32, bool add, int M, int N, int K,
+                       const GemmWorkspace &ws, char *buf, size_t n);
 // 4-bit weights: codes [rows][K / 2] and scales [rows][K / 32] of `count` numbers.
 hipError_t launch_quantize_mx4(const uint16_t *x, uint8_t *q, uint8_t *s, int64_t count,
                                hipStream_t stream);

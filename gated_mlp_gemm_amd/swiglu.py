@@ -89,6 +89,7 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
                                                P]
     lib.swiglu_gated_mlp_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, I32, I64, I64,
                                               I64, P, U64, P]
+    lib.swiglu_describe_backward.argtypes = [I64, I64, I64, I32, I32, I32, U64, ctypes.c_char_p, U64]
     lib.swiglu_quantize_mx4.argtypes = [P, P, P, I64, I64, P]
     lib.swiglu_dequantize_mx4.argtypes = [P, P, P, I64, I64, P]
     lib.swiglu_fused_gemm_mx4.argtypes = [P, P, P, P, I64, I64, I64, P, U64, P]
@@ -110,7 +111,8 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
                  "swiglu_route_backward", "swiglu_lora_workspace_size", "swiglu_fused_gemm_lora",
                  "swiglu_down_proj_lora", "swiglu_gated_mlp_lora", "swiglu_fused_gemm_train",
                  "swiglu_gated_mlp_train", "swiglu_down_proj_backward",
-                 "swiglu_fused_gemm_backward", "swiglu_gated_mlp_backward", "swiglu_quantize_mx4",
+                 "swiglu_fused_gemm_backward", "swiglu_gated_mlp_backward", "swiglu_describe_backward",
+                 "swiglu_quantize_mx4",
                  "swiglu_dequantize_mx4", "swiglu_fused_gemm_mx4", "swiglu_down_proj_mx4",
                  "swiglu_gated_mlp_mx4"):
         getattr(lib, name).restype = I32
@@ -608,6 +610,21 @@ def swiglu_gated_mlp_backward(dOut: torch.Tensor, A: torch.Tensor, W_fused: torc
                                              _GRAD_TYPES[dtype], M, N, K, ws, wsb,
                                              _stream(A.device)), "swiglu_gated_mlp_backward")
     return dA, dW_fused, dW3t, dGU
+
+
+_BACKWARD_CALLS = {"down_proj": 0, "fused_gemm": 1, "gated_mlp": 2}
+
+
+def swiglu_describe_backward(M: int, N: int, K: int, call="gated_mlp", grad_dtype=torch.bfloat16,
+                             add: bool = False, workspace_bytes: int = 0) -> str:
+    """The kernels that a backward call ('gated_mlp', 'fused_gemm'; 'down_proj', with D = K)
+    would launch for all its gradients, the weights' of grad_dtype and added to sums or not."""
+    buf = ctypes.create_string_buffer(1024)
+    c = _BACKWARD_CALLS[call.lower()] if isinstance(call, str) else int(call)
+    _check(load_library().swiglu_describe_backward(M, N, K, c, _GRAD_TYPES[_grad_dtype(grad_dtype)],
+                                                   int(add), workspace_bytes, buf, len(buf)),
+           "swiglu_describe_backward")
+    return buf.value.decode()
 
 
 def swiglu_silu_mul(gate: torch.Tensor, up: torch.Tensor,

@@ -530,6 +530,21 @@ int swiglu_describe_launch(int64_t M, int64_t N, int64_t K, int variant,
                            uint64_t workspace_bytes, char *buf, uint64_t buf_bytes);
 
 /*
+ * The same for a backward call with all its gradients (SWIGLU_DOWN_PROJ_BACKWARD, with
+ * D = K; SWIGLU_FUSED_GEMM_BACKWARD; SWIGLU_GATED_MLP_BACKWARD), whose weights' gradients
+ * are of type grad_type and added to sums (add != 0) or not.  Launches are joined by "+",
+ * stages by ", then"; two products in one launch are a gemm_pair_kernel, each with its
+ * tiles.  Same shape validation as the call's.
+ */
+typedef enum swiglu_backward_call {
+    SWIGLU_DOWN_PROJ_BACKWARD = 0,
+    SWIGLU_FUSED_GEMM_BACKWARD = 1,
+    SWIGLU_GATED_MLP_BACKWARD = 2
+} swiglu_backward_call;
+int swiglu_describe_backward(int64_t M, int64_t N, int64_t K, int call, int grad_type, int add,
+                             uint64_t workspace_bytes, char *buf, uint64_t buf_bytes);
+
+/*
  * The ablation's activation stage on its own: Y[i] = bf16(SiLU(gate[i]) *
  * up[i]) for i < count, fp32 arithmetic, one rounding.  count % 8 == 0,
  * count >= 0; pointers 16-byte aligned, device.
