@@ -425,7 +425,6 @@ struct Mx4Loader {
     uint32_t out[kWords];                  // LDS addresses of the lane's chunks, stage 0, unit 0
     SWIGLU_LDS char *ring;                 // the B ring
     int klim;                              // K minus the first k of the lane's codes
-    int klen;
     mutable Raw raw[2];
 
     __device__ __forceinline__ void init(const KMajor &op, int r0, int K, SWIGLU_LDS char *ring_,
@@ -437,7 +436,6 @@ struct Mx4Loader {
         scales = make_rsrc(op.scales + static_cast<int64_t>(r0) * row_scales,
                            static_cast<uint32_t>(min(left, static_cast<int64_t>(NROWS)) * row_scales));
         ring = ring_;
-        klen = K;
         const int tid = threadIdx.x;
         const int part = tid % kPerRow;
         klim = K - part * kBytes * 2;
