@@ -678,6 +678,10 @@ hipError_t launch_lora_project(const uint16_t *X, const uint16_t *W, uint16_t *Y
 // idle.  A split tail takes as many pieces as are worth their partials.  Against the
 // schedules of make_schedule(), whose steps of 256x256 tiles are dearer: M=8192 K=17920,
 // 1536 columns 414 -> 372 us, M=2048 K=1536, 8960 columns 67 -> 60.
+// (Two models of one machine: make_schedule() counts 3.7 us for a round of 256x256 tiles and
+// 1.69 for a K step where this one counts 8.0 and 1.05 to 1.2.  Its constants were fitted to the
+// forward calls, and there pick within 0.5 % of the fastest schedule on the points they were
+// fitted to, so those calls keep them; one model would have to be fitted to both.)
 // ---------------------------------------------------------------------------
 template <class S>
 struct GradCost {

@@ -128,14 +128,35 @@ static hipError_t run_few(const uint16_t *X, const uint8_t *Q, const uint8_t *S,
 
 // Rows of the weight a workgroup takes, by the 16-row tiles there are for a compute
 // unit: every workgroup reads all the activations, so more where that leaves the
-// device enough of them.  Measured, us, activations x weight (R = 1 / 2 / 4):
-//   M=16  896 x 4864 4.2 / 5.0 / 6.7, 8192 x 29568 47.1 / 36.5 / 49.6,
-//         27648 x 5120 29.0 / 24.7 / 20.9
-//   M=64  896 x 4864 8.8 / 9.8 / 14.8, 8192 x 29568 113 / 71 / 94,
-//         27648 x 5120 68 / 50 / 41
-// With at most 4 rows of activations there is little to share: R = 1 (37888 x 3584 14.0
-// against 14.5 us), with 8 waves for 4 where a compute unit has one workgroup (3584 x
-// 18944 8.3 against 9.5), R = 2 for long rows of many (59136 x 8192 47.5 against 51.3).
+// device enough of them.  Measured, us with the weights streamed from memory (R = 1 / 2 /
+// 4); the weights have 56, 224 (one form), 320, 512, 608 (the next), 1728, 2368 and 3696
+// tiles:
+//   M=8   896 x 4864 3.8 / 4.5 / 6.1, 3584 x 18944 12.3 / 16.4 / 25.1, 5120 x 13824 16.3 / 13.1
+//         / 19.5, 8192 x 29568 36.1 / 28.5 / 41.8, 9728 x 896 4.7 / 3.5 / 3.4, 27648 x 5120 22.8
+//         / 19.7 / 19.0, 37888 x 3584 21.7 / 17.9 / 17.7, 59136 x 8192 63.9 / 56.0 / 53.9
+//   M=16  4.3 / 5.1 / 6.4, 16.0 / 21.6 / 29.4, 22.0 / 17.2 / 21.8, 47.4 / 36.7 / 49.4, 3.7 / 3.7
+//         / 3.6, 29.3 / 24.9 / 21.4, 27.5 / 21.8 / 19.9, 85.8 / 67.4 / 59.9
+//   M=32  5.8 / 6.6 / 8.6, 23.9 / 27.3 / 38.7, 33.4 / 21.5 / 29.5, 70.8 / 45.3 / 65.3, 5.6 / 6.0
+//         / 4.5, 43.1 / 34.2 / 25.8, 41.9 / 32.7 / 24.6, 127.2 / 96.4 / 73.4
+//   M=48  7.4 / 8.5 / 11.7, 30.3 / 35.4 / 47.0, 42.6 / 27.3 / 35.9, 93.4 / 59.1 / 74.2, 8.8 /
+//         7.2 / 5.4, 63.4 / 44.1 / 30.0, 67.2 / 42.5 / 29.2, 190.7 / 124.7 / 96.1
+//   M=64  9.0 / 10.7 / 14.0, 37.0 / 44.3 / 57.6, 52.3 / 33.9 / 44.4, 113.4 / 71.4 / 91.6, 10.2 /
+//         6.7 / 6.1, 76.5 / 52.4 / 38.9, 81.3 / 40.8 / 39.3, 231.1 / 159.0 / 118.8
+// The rule takes the fastest of the three but at 9728 x 896 (short contractions would take
+// R = 4 from fewer tiles on: up to 25 % at M=32 and 48) and, 4 % slower at most, for M <= 8
+// and wide weights, which share the form of fewer tiles.  Forms between (R = 3, 5, 6, 8, rings
+// of 24 rows) are not offered: at M=24 they are within 5 % at 59136 x 8192, but 19.7 (R = 5)
+// against 23.7 at 37888 x 3584 and 21.8 (R = 8) against 24.5 at 27648 x 5120.
+// With at most 4 rows of activations there is little to share (8 waves, R = 1 / 4 waves,
+// R = 1 / 4 waves, R = 2):
+//   M=1  896 x 4864 3.6 / 3.7 / 4.6, 3584 x 18944 8.6 / 9.7 / 11.7, 8192 x 29568 25.5 / 24.7 /
+//        24.2, 37888 x 3584 18.2 / 13.8 / 14.7, 27648 x 5120 17.5 / 15.0 / 16.5, 59136 x 8192
+//        48.6 / 51.4 / 47.7
+//   M=4  3.7 / 3.7 / 4.7, 10.1 / 9.9 / 13.8, 29.7 / 28.8 / 25.6, 18.9 / 16.1 / 15.2, 20.1 /
+//        17.9 / 17.4, 52.1 / 54.9 / 48.2
+// so R = 1, with 8 waves for 4 where a compute unit has one workgroup, and R = 2 for long
+// rows of many; the border K = 8192 lies between the last two weights, where M=1 changes
+// sides (M=4 would take R = 2 at the three before, by 3 to 11 %).
 template <bool GATED>
 static hipError_t launch_few(const uint16_t *X, const uint8_t *Q, const uint8_t *S, uint16_t *Y,
                              int M, int rows, int K, int cus, hipStream_t stream) {
