@@ -26,8 +26,8 @@
 // times the bytes, 6 or 12 waves and rings without the rows past the 24th are within 5 %;
 // at 37888 x 3584 and 27648 x 5120 a workgroup of 80 or 128 rows is 17 and 11 % faster
 // than the forms there are (launch_few).  LDS is at work in 30 and 17 % of the two launches'
-// cycles; of those 73 and 47 % count as bank conflicts, the reads of 16 activation rows
-// among them: not looked into.
+// cycles; of those 73 and 47 % count as bank conflicts.  (The scales of a tile's 16 rows are
+// K / 32 bytes apart: at K=8192 all in one bank.  A pitch apart from K's is not built.)
 #pragma once
 
 #include "gemm_core.hpp"
