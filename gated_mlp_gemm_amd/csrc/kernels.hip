@@ -1032,10 +1032,10 @@ hipError_t launch_stage_backward(const uint16_t *dGU, const uint16_t *A, const u
 
 // What the backward calls with all their gradients launch, as text.
 template <class S, bool kQuarters, class Epi>
-static int describe_product(const GradProduct<Epi> &p, const char *epi, const GemmWorkspace &ws,
-                            char *buf, size_t n) {
+static int describe_product(const GradProduct<Epi> &p, double extra, const char *epi,
+                            const GemmWorkspace &ws, char *buf, size_t n) {
     return describe<S>("gemm_tiles_kernel", epi,
-                       make_grad_schedule<S, kQuarters>(p.M, p.cols, p.K, p.extra, ws), ws.cus, buf, n);
+                       make_grad_schedule<S, kQuarters>(p.M, p.cols, p.K, extra, ws), ws.cus, buf, n);
 }
 static void describe_items(const Schedule &s, char *buf, size_t n) {
     if (s.pieces) std::snprintf(buf, n, "%d tiles split %d ways along K", s.split_tiles, s.pieces);
@@ -1057,20 +1057,20 @@ static void describe_grads(const GradProduct<EX> &x, const GradProduct<WeightGra
     }
     const GemmWorkspace dws = dw_workspace(w, ws);
     if (grad_quad_faster<ShapeWideDw, ShapeQuadDw, false>(w.M, w.cols, w.K, w.extra, dws))
-        describe_product<ShapeQuadDw, false>(w, "WeightGradEpilogue", dws, tw, sizeof tw);
+        describe_product<ShapeQuadDw, false>(w, w.extra, "WeightGradEpilogue", dws, tw, sizeof tw);
     else
-        describe_product<ShapeWideDw, false>(w, "WeightGradEpilogue", dws, tw, sizeof tw);
+        describe_product<ShapeWideDw, false>(w, w.extra, "WeightGradEpilogue", dws, tw, sizeof tw);
     if (x.M == 0) {
         std::snprintf(buf, n, "%s", tw);
         return;
     }
     constexpr bool kQ = kDxQuarters<EX>;
     if (x.M <= 128)
-        describe_product<ShapeSmallDx, false>(x, epi, ws, tx, sizeof tx);
+        describe_product<ShapeSmallDx, false>(x, 0.0, epi, ws, tx, sizeof tx);
     else if (grad_quad_faster<ShapeWideDx, ShapeQuadDx, kQ>(x.M, x.cols, x.K, x.extra, ws))
-        describe_product<ShapeQuadDx, false>(x, epi, ws, tx, sizeof tx);
+        describe_product<ShapeQuadDx, false>(x, x.extra, epi, ws, tx, sizeof tx);
     else
-        describe_product<ShapeWideDx, kQ>(x, epi, ws, tx, sizeof tx);
+        describe_product<ShapeWideDx, kQ>(x, x.extra, epi, ws, tx, sizeof tx);
     std::snprintf(buf, n, "%s + %s", tx, tw);
 }
 void describe_backward(BackwardCall call, bool f32, bool add, int M, int N, int K,

@@ -486,7 +486,7 @@ struct BlockEpilogue {
 //     dGate = D u s (1 + g (1 - s)),   dUp = D g s,
 // stored as dGU [M][2N], interleaved as GU.  D is never stored, and both halves are
 // rounded to bf16 here: they are an operand of the MFMAs of two more products.
-// (With dW3t in one launch: M=8192 K=5120 N=13824 1660 us, 1396 TFLOP/s, MFMA busy in 72 %
+// (With dW3t in one launch: M=8192 K=5120 N=13824 1660 us, 1396 TFLOP/s, MFMA busy in 71 %
 // of the cycles at 1.76 GHz; M=2048 K=1536 N=8960 122 to 124 us, 910, busy in 39 %: a tile's
 // 24 K steps are followed by 512 KB of GU read and dGU written, and by no MFMA meanwhile.)
 __device__ __forceinline__ uint32_t gate_grad(float d, uint32_t gu) {
